@@ -14,6 +14,7 @@ from .binding import (  # noqa: F401
     block_sparse_attn_varlen_backward,
     build_vsa_metadata,
     check_device_status,
+    dense_attn_varlen,
     gather_tokens,
     get_device_status,
     lib,
@@ -26,6 +27,6 @@ from .binding import (  # noqa: F401
 __all__ = [
     "VSAError", "block_sparse_attn", "block_sparse_attn_backward",
     "block_sparse_attn_from_indices", "block_sparse_attn_varlen_backward", "block_sparse_attn_varlen", "build_vsa_metadata",
-    "check_device_status", "gather_tokens", "get_device_status", "lib", "scatter_tokens",
+    "check_device_status", "dense_attn_varlen", "gather_tokens", "get_device_status", "lib", "scatter_tokens",
     "vsa_forward", "vsa_forward_host", "video_sparse_attn_bshd",
 ]

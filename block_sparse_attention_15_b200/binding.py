@@ -46,7 +46,13 @@ class VsaLayout(ctypes.Structure):
                 ("gate", VsaStrides)]
 
 
+class VsaDenseLayout(ctypes.Structure):
+    """vsa_dense_layout: the strides of the [H, rows, D] views of one dense call."""
+    _fields_ = [(n, VsaStrides) for n in ("q", "k", "v", "out", "dout", "dq", "dk", "dv")]
+
+
 _PL = ctypes.POINTER(VsaLayout)
+_PDL = ctypes.POINTER(VsaDenseLayout)
 VSA_LAYOUT_BHSD, VSA_LAYOUT_BSHD = 0, 1
 
 # name -> (restype, argtypes); mirrors include/vsa.h
@@ -97,6 +103,8 @@ SIGNATURES = {
                                  [_c_int] * 3 + [_c_void_p, _c_void_p, _c_int, _c_float,
                                                  _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                                  _c_void_p, _c_size_t, _c_void_p]),
+    "dense_attn_varlen": (_c_int, [_c_void_p] * 3 + [_PDL, _P32, _P32] + [_c_int] * 4 +
+                          [_c_int64, _c_int64, _c_int, _c_float, _c_void_p, _c_void_p, _c_void_p]),
     "build_vsa_metadata": (_c_int, [_c_int] * 6 + [_P64, _P64, _P32, _P64, _P64, _P32]),
     "vsa_gather_tokens": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_int64, _c_int64, _c_int64,
                                    _c_int, _c_void_p]),
@@ -577,6 +585,113 @@ def block_sparse_attn_varlen_backward(q, k, v, out, dout, lse, cu_seqlens_q, cu_
         ws.numel(), _stream(stream)))
     del cq, ck
     return dq, dk, dv
+
+
+def _require_rows(t, name):
+    """A bf16 CUDA [H, rows, D] view: head dim contiguous, other strides
+    multiples of 8 elements (token-major memory transposed, a slice of a
+    fused tensor)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be a 3-D [H, rows, D] view")
+    if t.numel() == 0:
+        return
+    if t.stride(2) != 1 or any(t.shape[a] > 1 and (t.stride(a) <= 0 or t.stride(a) % 8) for a in (0, 1)):
+        raise ValueError(f"{name}: strides {t.stride()} must be positive multiples of 8 elements, "
+                         "the last 1")
+    if t.data_ptr() % 16:
+        raise ValueError(f"{name} must start on a 16-byte boundary")
+
+
+def _same_device(dev, **tensors):
+    for n, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{n} is on {t.device}, q on {dev}")
+
+
+def _strides_rows(t):
+    return VsaStrides(0, t.stride(0), t.stride(1))
+
+
+class _Launch:
+    """The device and stream of a call: the tensors' device becomes the current
+    one, and memory allocated inside belongs to the stream the kernels run on."""
+
+    def __init__(self, dev, stream):
+        self._dev = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+        self._ctx = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self._dev is not None:
+            self._dev.__enter__()
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        return _c_void_p(torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+        if self._dev is not None:
+            self._dev.__exit__(*exc)
+
+
+def _dense_common(q, k, v, cu_seqlens_q, cu_seqlens_kv):
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        _require_rows(t, n)
+    Hq, Sq, D = q.shape
+    Hkv, Skv = k.shape[0], k.shape[1]
+    if v.shape != k.shape or k.shape[2] != D:
+        raise ValueError("k and v must be [Hkv, kv_rows, D] with q's D")
+    _same_device(q.device, k=k, v=v)
+    cq, cq_p = _host_i32(cu_seqlens_q)
+    ck, ck_p = _host_i32(cu_seqlens_kv)
+    if cq.ndim != 1 or cq.shape != ck.shape or len(cq) < 1:
+        raise ValueError("cu_seqlens_q and cu_seqlens_kv must have n_seqs + 1 entries each")
+    return Hq, Hkv, D, Sq, Skv, cq, cq_p, ck, ck_p
+
+
+def dense_attn_varlen(q, k, v, cu_seqlens_q, cu_seqlens_kv, *, causal: bool = True,
+                      scale: float | None = None, out=None, return_lse: bool = False, stream=None):
+    """Dense attention of packed sequences with grouped heads
+    (``dense_attn_varlen``): causal (a sequence's last row sees all its keys,
+    the row before it one fewer, ...) or full.
+
+    q: [Hq, q_rows, D]; k, v: [Hkv, kv_rows, D]; any of them a strided view
+    (token-major [rows, H, D] memory transposed, a slice of a fused QKV
+    tensor).  cu_seqlens_*: host sequences of n + 1 ints from 0, as in
+    :func:`block_sparse_attn_varlen`; lengths may be 0.  Rows of a given
+    ``out`` past the last sequence are left as they were (0 when it is
+    allocated here).  With ``return_lse`` also returns the fp32 [Hq, q_rows]
+    natural-log log-sum-exp (-inf where a row sees no key), which
+    :func:`dense_attn_varlen_backward` takes."""
+    Hq, Hkv, D, Sq, Skv, cq, cq_p, ck, ck_p = _dense_common(q, k, v, cu_seqlens_q, cu_seqlens_kv)
+    L = lib()
+    with _Launch(q.device, stream) as st:
+        tail = int(cq[-1]) if 0 <= cq[-1] <= Sq else Sq
+        if out is None:
+            out = torch.empty_like(q)
+            if tail < Sq:
+                out[:, tail:].zero_()
+        else:
+            _require_rows(out, "out")
+            _same_device(q.device, out=out)
+            if out.shape != q.shape:
+                raise ValueError("out must be shaped like q")
+        lse = None
+        if return_lse:
+            lse = torch.empty((Hq, Sq), dtype=torch.float32, device=q.device)
+            if tail < Sq:
+                lse[:, tail:].zero_()
+        lay = VsaDenseLayout(_strides_rows(q), _strides_rows(k), _strides_rows(v), _strides_rows(out))
+        _check("dense_attn_varlen", L.dense_attn_varlen(
+            _ptr(q), _ptr(k), _ptr(v), ctypes.byref(lay), cq_p, ck_p, len(cq) - 1, Hq, Hkv, D, Sq, Skv,
+            1 if causal else 0, float(scale) if scale is not None else 0.0, _ptr(out), _ptr(lse), st))
+    return (out, lse) if return_lse else out
 
 
 def build_vsa_metadata(T: int, Hh: int, W: int, tile=(4, 4, 4)) -> dict:

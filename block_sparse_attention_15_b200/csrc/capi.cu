@@ -293,7 +293,7 @@ const char* vsa_status_string(int status) {
   }
 }
 
-int vsa_abi_version(void) { return (2 << 16) | 1; }
+int vsa_abi_version(void) { return (2 << 16) | 2; }
 
 int vsa_get_device_status(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return VSA_ERR_CUDA;

@@ -1,0 +1,77 @@
+// What the dense-attention kernels (forward, dq, dk/dv) share: the packed
+// sequences of a launch, the order in which their tiles are worked on, and the
+// tile loads.
+#pragma once
+
+#include <cuda.h>
+#include <stdint.h>
+
+#include "dense_launch.h"
+#include "vsa_device.cuh"
+
+namespace vsa {
+namespace dense {
+
+// Work item i of a launch: one tile unit of one sequence.  Sequences are sorted
+// by their unit counts n_0 >= n_1 >= ..., and units are taken by descending
+// rank t (unit t of a causal sequence costs about t + 1 key tiles), every
+// sequence that has a unit of that rank in turn: longest work first, so the
+// last wave is made of the short items.  The ranks n_r .. n_{r-1} - 1 are those
+// that exactly r sequences have; their items start at first[r].
+struct Unit {
+  int seq;   // index into DenseSeqs::seq
+  int rank;  // 0 .. units[seq] - 1
+};
+
+__device__ __forceinline__ Unit find_unit(const DenseSeqs& t, int i) {
+  // largest r in [1, n] with first[r] <= i
+  int lo = 1, hi = t.n;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.first[mid] <= i) lo = mid;
+    else hi = mid - 1;
+  }
+  const int o = i - t.first[lo];
+  Unit u;
+  u.seq = o % lo;
+  u.rank = t.units[lo - 1] - 1 - o / lo;
+  return u;
+}
+
+// The w-th item of CTA c of a persistent grid of g: waves alternate direction,
+// so the CTA that got a wave's longest item gets the next wave's shortest.
+__device__ __forceinline__ int wave_item(int w, int c, int g) {
+  return w * g + ((w & 1) ? g - 1 - c : c);
+}
+
+// 64 head dims x box rows of a [H, S, D] view through its tile map.
+__device__ __forceinline__ void load_rows(void* dst, const CUtensorMap* map, TmaAxes ax,
+                                          uint64_t* bar, int d0, int s, int h, int b,
+                                          uint64_t hint) {
+  const int c1 = ax.s == 1 ? s : (ax.h == 1 ? h : b);
+  const int c2 = ax.s == 2 ? s : (ax.h == 2 ? h : b);
+  const int c3 = ax.s == 3 ? s : (ax.h == 3 ? h : b);
+  tma_load_4d(dst, map, bar, d0, c1, c2, c3, hint);
+}
+
+// Rows `from` .. `to` - 1 of a tile of `slabs` 64-column slabs (ROWS rows of
+// 128 bytes each) become zero: the warp's lanes write 16 bytes each.  The
+// swizzle only permutes a row's eight 16-byte chunks, so it can be ignored.
+template <int ROWS>
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int slabs, int from, int to, int lane) {
+  const int n = (to - from) * 8;
+  for (int sl = 0; sl < slabs; ++sl)
+    for (int i = lane; i < n; i += 32)
+      *reinterpret_cast<uint4*>(tile + sl * (ROWS * 128) + from * 128 + i * 16) =
+          make_uint4(0u, 0u, 0u, 0u);
+}
+
+// A launch whose waits ran out leaves only after copies that may still be in
+// flight have landed (they take microseconds).
+__device__ __forceinline__ void settle_after_abort(volatile int* abort_flag) {
+  if (*abort_flag)
+    for (int i = 0; i < 20; ++i) __nanosleep(100000);
+}
+
+}  // namespace dense
+}  // namespace vsa

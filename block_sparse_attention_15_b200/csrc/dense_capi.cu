@@ -1,0 +1,96 @@
+// C ABI of the dense-attention entries (vsa.h): argument checks and launches.
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "dense_launch.h"
+#include "vsa.h"
+#include "vsa_launch.h"
+
+namespace vsa {
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// A [H, S, D] view: strides of axes longer than one are positive multiples of
+// 8 elements (16 bytes: tile maps and 16-byte accesses).
+bool view_ok(const vsa_strides& s, long long H, long long S) {
+  auto ok = [](long long stride, long long extent) {
+    return extent <= 1 || (stride > 0 && stride % 8 == 0);
+  };
+  return ok(s.head, H) && ok(s.seq, S);
+}
+
+Strides3 to3(const vsa_strides& s) { return Strides3{s.batch, s.head, s.seq}; }
+
+// Cumulative lengths: start at 0, never fall, end within the tensor's rows.
+bool cumulative_ok(const int32_t* cu, int n, long long rows) {
+  if (cu[0] != 0) return false;
+  for (int i = 0; i < n; ++i)
+    if (cu[i + 1] < cu[i]) return false;
+  return cu[n] <= rows;
+}
+
+constexpr long long kMaxRows = 0x7FFFFFFFLL - 256;  // tile coordinates are 32-bit
+
+int check_dense(int n_seqs, const int32_t* cu_q, const int32_t* cu_kv, int Hq, int Hkv, int D,
+                int64_t q_rows, int64_t kv_rows, float scale) {
+  if (!cu_q || !cu_kv || Hq <= 0 || Hkv <= 0 || q_rows < 0 || kv_rows < 0 || !(scale == scale))
+    return VSA_ERR_INVALID_ARG;
+  if (n_seqs <= 0) return VSA_ERR_SHAPE;
+  if (D != 64 && D != 128) return VSA_ERR_UNSUPPORTED;
+  if (Hq % Hkv) return VSA_ERR_SHAPE;
+  if (q_rows > kMaxRows || kv_rows > kMaxRows || Hq > 65535) return VSA_ERR_UNSUPPORTED;
+  if (!cumulative_ok(cu_q, n_seqs, q_rows) || !cumulative_ok(cu_kv, n_seqs, kv_rows)) return VSA_ERR_SHAPE;
+  return VSA_OK;
+}
+
+void contiguous_layout(vsa_dense_layout* L, int64_t q_rows, int64_t kv_rows, int D) {
+  const vsa_strides q{0, q_rows * D, D}, kv{0, kv_rows * D, D};
+  L->q = L->out = L->dout = L->dq = q;
+  L->k = L->v = L->dk = L->dv = kv;
+}
+
+}  // namespace
+}  // namespace vsa
+
+using namespace vsa;
+
+extern "C" {
+
+int dense_attn_varlen(const void* q, const void* k, const void* v, const vsa_dense_layout* layout,
+                      const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_kv, int n_seqs, int Hq,
+                      int Hkv, int D, int64_t q_rows, int64_t kv_rows, int causal, float scale,
+                      void* out, float* lse, void* stream) {
+  int rc = check_dense(n_seqs, cu_seqlens_q, cu_seqlens_kv, Hq, Hkv, D, q_rows, kv_rows, scale);
+  if (rc != VSA_OK) return rc;
+  if (cu_seqlens_q[n_seqs] == 0) return VSA_OK;  // no rows
+  const bool keys = cu_seqlens_kv[n_seqs] > 0;
+  if (!q || !out || (keys && (!k || !v))) return VSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || (keys && (!aligned16(k) || !aligned16(v))))
+    return VSA_ERR_INVALID_ARG;
+  vsa_dense_layout L;
+  if (layout) L = *layout;
+  else contiguous_layout(&L, q_rows, kv_rows, D);
+  if (!view_ok(L.q, Hq, q_rows) || !view_ok(L.out, Hq, q_rows) ||
+      (keys && (!view_ok(L.k, Hkv, kv_rows) || !view_ok(L.v, Hkv, kv_rows))))
+    return VSA_ERR_UNSUPPORTED;
+  DenseParams p;
+  memset(&p, 0, sizeof(p));
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.out_st = to3(L.out);
+  p.lse = lse;
+  p.lse_seq = q_rows;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.group = Hq / Hkv;
+  p.causal = causal ? 1 : 0;
+  p.scale_log2 = resolve_scale(scale, D) * kLog2e;
+  p.status = device_status_ptr();
+  if (!p.status) return VSA_ERR_CUDA;
+  const DenseTensors t{q, k, v, to3(L.q), to3(L.k), to3(L.v), q_rows, keys ? kv_rows : 0};
+  const DenseBatch b{cu_seqlens_q, cu_seqlens_kv, n_seqs};
+  return launch_dense_fwd(p, t, b, D, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,73 @@
+// Host-side parameter blocks and launchers of the dense-attention kernels.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "vsa_launch.h"
+
+namespace vsa {
+
+// Sequences one launch takes; longer batches are split over launches.
+constexpr int kDenseMaxSeqs = 256;
+
+// Packed sequences of one launch, passed by value (so a captured launch keeps
+// its lengths), sorted by units descending.  5.1 KB of the kernel's 32 KB of
+// parameters.
+struct DenseSeqs {
+  int n;
+  int n_items;                      // units of all sequences
+  int4 seq[kDenseMaxSeqs];          // first q row, q rows, first kv row, kv rows
+  int units[kDenseMaxSeqs];         // units of the sequence (what a unit is, each kernel says)
+  int first[kDenseMaxSeqs + 2];     // items before the ranks that exactly r sequences have
+};
+
+struct DenseParams {
+  __nv_bfloat16* out;
+  Strides3 out_st;                  // b unused
+  float* lse;                       // [Hq, lse_seq] or null
+  long long lse_seq;
+  TmaAxes q_ax, k_ax, v_ax;
+  int Hq, Hkv, group;               // group = Hq / Hkv
+  int causal;
+  int slots;                        // row tiles per work item: 1 or 2
+  int n_work;                 // work items of the launch
+  float scale_log2;
+  int* status;
+};
+
+// One call's tensors: [H, S, D] views (Strides3::b unused).
+struct DenseTensors {
+  const void *q, *k, *v;
+  Strides3 q_st, k_st, v_st;
+  long long q_seq, kv_seq;          // rows of the q and k/v views
+};
+
+// Host cumulative lengths of a batch (checked by the caller).
+struct DenseBatch {
+  const int32_t* cu_q;
+  const int32_t* cu_kv;
+  int n;
+  // sequences i0 .. of at most kDenseMaxSeqs, as DenseSeqs::seq entries
+  int chunk(int i0, int4* seqs) const;
+};
+
+// Once per device: the kernel has the register count its split needs, and its
+// shared memory limit is raised.
+struct KernelReady {
+  std::atomic<unsigned long long> done{0};
+  int check(const void* kern, int regs, int smem);
+};
+
+int device_sm_count();
+// Sorts sequences by units (dropping those without) and fills the table;
+// `units` in the order of `seqs`, their sum below 2^30.
+void fill_dense_seqs(DenseSeqs* t, const int4* seqs, const int* units, int n);
+int launch_dense_fwd(const DenseParams& p, const DenseTensors& t, const DenseBatch& b, int D,
+                     cudaStream_t stream);
+
+}  // namespace vsa

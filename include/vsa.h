@@ -528,6 +528,54 @@ int block_sparse_attn_varlen_backward(
     void* stream);
 
 /* ======================================================================== *
+ * dense attention of packed sequences (ABI 2.2)
+ * ======================================================================== */
+
+/* Strides of the tensors of a dense call, each a [H, rows, D] view with the
+ * head dim contiguous (vsa_strides::batch unused): `head` and `seq` strides of
+ * axes longer than one are positive multiples of 8 elements
+ * (VSA_ERR_UNSUPPORTED otherwise).  Token-major [rows, H, D] memory is
+ * {0, D, H * D}.  The forward uses q, k, v and out. */
+typedef struct vsa_dense_layout {
+  vsa_strides q, k, v, out, dout, dq, dk, dv;
+} vsa_dense_layout;
+
+/*
+ * dense_attn_varlen -- softmax attention of packed sequences of different
+ * lengths with grouped heads, every key visible (causal = 0) or causal: the
+ * dense counterpart of block_sparse_attn_varlen, for the layers of a model
+ * that stay dense, for prompts, and for causal models.
+ *
+ * Sequence i has Lq = cu_seqlens_q[i+1] - cu_seqlens_q[i] query rows and Lk
+ * key rows.  Query head h reads key head h / (Hq / Hkv).  Row r sees its
+ * sequence's first n(r) keys, n(r) = Lk, or, causal, clamp(r + 1 + Lk - Lq,
+ * 0, Lk) (the last row sees every key):
+ *   lse(r) = log sum_{j < n(r)} exp(scale q_r . k_j)
+ *   out(r) = sum_{j < n(r)} exp(scale q_r . k_j - lse(r)) v_j
+ * A row that sees no key gives out = 0 and lse = -inf.  Lengths may be 0.
+ * What k and v hold past a sequence's rows never matters (NaN included); a
+ * NaN or infinity in a sequence's own v reaches the rows that see it and may
+ * reach other rows of that sequence.
+ *
+ * q        device bf16 [Hq, q_rows, D] view
+ * k, v     device bf16 [Hkv, kv_rows, D] views
+ * layout   host, or NULL for contiguous tensors
+ * cu_seqlens_q, cu_seqlens_kv  host int32 [n_seqs + 1], from 0, non-decreasing,
+ *          ending at most at q_rows / kv_rows.  They are read during the call
+ *          and travel with the launch (a captured call keeps them).
+ * out      device bf16 [Hq, q_rows, D] view; rows past the last sequence are
+ *          left as they were
+ * lse      device fp32 [Hq, q_rows] or NULL; rows past the last sequence too
+ * scale    <= 0 selects 1/sqrt(D)
+ * D 64 or 128; Hq a multiple of Hkv (VSA_ERR_SHAPE).  16-byte aligned views.
+ * No workspace; one launch per 256 sequences.
+ */
+int dense_attn_varlen(const void* q, const void* k, const void* v, const vsa_dense_layout* layout,
+                      const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_kv, int n_seqs, int Hq,
+                      int Hkv, int D, int64_t q_rows, int64_t kv_rows, int causal, float scale,
+                      void* out, float* lse, void* stream);
+
+/* ======================================================================== *
  * a7: video tile metadata (host) and token gather / scatter (device)
  * ======================================================================== */
 
