@@ -51,6 +51,11 @@ class VsaDenseLayout(ctypes.Structure):
     _fields_ = [(n, VsaStrides) for n in ("q", "k", "v", "out", "dout", "dq", "dk", "dv")]
 
 
+class VsaPrefixLayout(ctypes.Structure):
+    """vsa_prefix_layout: the strides of one shared_prefix_attn call."""
+    _fields_ = [(n, VsaStrides) for n in ("q", "out", "k_prefix", "v_prefix", "k_suffix", "v_suffix")]
+
+
 _PL = ctypes.POINTER(VsaLayout)
 _PDL = ctypes.POINTER(VsaDenseLayout)
 VSA_LAYOUT_BHSD, VSA_LAYOUT_BSHD = 0, 1
@@ -105,6 +110,10 @@ SIGNATURES = {
                                                  _c_void_p, _c_size_t, _c_void_p]),
     "dense_attn_varlen": (_c_int, [_c_void_p] * 3 + [_PDL, _P32, _P32] + [_c_int] * 4 +
                           [_c_int64, _c_int64, _c_int, _c_float, _c_void_p, _c_void_p, _c_void_p]),
+    "shared_prefix_attn_workspace_size": (_c_size_t, [_c_int] * 5 + [_c_int64] * 2),
+    "shared_prefix_attn": (_c_int, [_c_void_p] * 6 + [ctypes.POINTER(VsaPrefixLayout)] + [_c_int] * 5 +
+                           [_c_int64, _c_int64, _c_float, _c_void_p, _c_void_p, _c_void_p, _c_size_t,
+                            _c_void_p]),
     "build_vsa_metadata": (_c_int, [_c_int] * 6 + [_P64, _P64, _P32, _P64, _P64, _P32]),
     "vsa_gather_tokens": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_int64, _c_int64, _c_int64,
                                    _c_int, _c_void_p]),
@@ -165,16 +174,19 @@ def _require(t, dtype, name, device=True):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _require_view(t, name):
+def _require_view(t, name, empty=False):
     """A bf16 CUDA tensor whose last (head-dim) axis is contiguous and whose
     other strides are multiples of 8 elements (any layout: BHSD, BSHD, a
-    slice of a fused tensor, a transposed view)."""
+    slice of a fused tensor, a transposed view); where `empty` allows it, one
+    without elements, whatever its strides."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if empty and t.dim() == 4 and t.numel() == 0:
+        return
     if t.dim() != 4 or t.stride(3) != 1:
         raise ValueError(f"{name} must be a 4-D view with a contiguous last axis")
     for ax in range(3):
@@ -691,6 +703,57 @@ def dense_attn_varlen(q, k, v, cu_seqlens_q, cu_seqlens_kv, *, causal: bool = Tr
         _check("dense_attn_varlen", L.dense_attn_varlen(
             _ptr(q), _ptr(k), _ptr(v), ctypes.byref(lay), cq_p, ck_p, len(cq) - 1, Hq, Hkv, D, Sq, Skv,
             1 if causal else 0, float(scale) if scale is not None else 0.0, _ptr(out), _ptr(lse), st))
+    return (out, lse) if return_lse else out
+
+
+def shared_prefix_attn(q, k_prefix, v_prefix, k_suffix, v_suffix, suffix_lens, *,
+                       scale: float | None = None, out=None, return_lse: bool = False, workspace=None,
+                       stream=None):
+    """Attention of the newest tokens of many requests over a prefix they share
+    and over their own keys behind it (``shared_prefix_attn``): one decoding
+    step, or the check of a few drafted tokens.
+
+    q: [B, Hq, T, D]; k_prefix, v_prefix: [Hkv, P, D], kept once for all
+    requests (P may be 0); k_suffix, v_suffix: [B, Hkv, capacity, D], the last T
+    of a request's ``suffix_lens[b]`` keys being its new tokens'; all may be
+    strided views (token-major caches transposed).  suffix_lens: CUDA int32
+    [B], read on the device.  Token t sees the prefix and its first
+    ``suffix_lens[b] - T + 1 + t`` suffix keys.  Returns [B, Hq, T, D], with
+    ``return_lse`` also the fp32 [B, Hq, T] natural-log log-sum-exp."""
+    for t, n in ((q, "q"), (k_suffix, "k_suffix"), (v_suffix, "v_suffix")):
+        _require_view(t, n, empty=True)
+    for t, n in ((k_prefix, "k_prefix"), (v_prefix, "v_prefix")):
+        _require_rows(t, n)
+    _require(suffix_lens, torch.int32, "suffix_lens")
+    B, Hq, T, D = q.shape
+    Hkv, P = k_prefix.shape[:2]
+    cap = k_suffix.shape[2]
+    if k_prefix.shape != (Hkv, P, D) or v_prefix.shape != k_prefix.shape:
+        raise ValueError("k_prefix and v_prefix must be [Hkv, P, D] with q's D")
+    if k_suffix.shape != (B, Hkv, cap, D) or v_suffix.shape != k_suffix.shape:
+        raise ValueError(f"k_suffix and v_suffix must be [B, Hkv, capacity, D] = {(B, Hkv, cap, D)}")
+    if suffix_lens.shape != (B,):
+        raise ValueError(f"suffix_lens must be [B] = [{B}]")
+    _same_device(q.device, k_prefix=k_prefix, v_prefix=v_prefix, k_suffix=k_suffix, v_suffix=v_suffix,
+                 suffix_lens=suffix_lens, out=out, workspace=workspace)
+    L = lib()
+    with _Launch(q.device, stream) as st:
+        if out is None:
+            out = torch.empty_like(q)
+        else:
+            _require_view(out, "out", empty=True)
+            if out.shape != q.shape:
+                raise ValueError("out must be shaped like q")
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device) if return_lse else None
+        need = L.shared_prefix_attn_workspace_size(B, Hq, Hkv, T, D, P, cap)
+        if workspace is None:
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        lay = VsaPrefixLayout(_strides_bhsd(q), _strides_bhsd(out), _strides_rows(k_prefix),
+                              _strides_rows(v_prefix), _strides_bhsd(k_suffix), _strides_bhsd(v_suffix))
+        _check("shared_prefix_attn", L.shared_prefix_attn(
+            _ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(k_suffix), _ptr(v_suffix), _ptr(suffix_lens),
+            ctypes.byref(lay), B, Hq, Hkv, T, D, P, cap, float(scale) if scale is not None else 0.0,
+            _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), st))
     return (out, lse) if return_lse else out
 
 

@@ -66,6 +66,37 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int slabs, int from, in
           make_uint4(0u, 0u, 0u, 0u);
 }
 
+// S = Q . K^T: M = N = 128, K = D; tiles are [D / 64][128 rows][128 B].
+template <int D>
+__device__ __forceinline__ void issue_s(uint32_t tmem_d, uint32_t q_base, uint32_t k_base) {
+  constexpr uint32_t idesc = make_idesc_bf16(128, 128, false, false);
+  const uint64_t a0 = make_sdesc_sw128(q_base, 16u, 1024u);
+  const uint64_t b0 = make_sdesc_sw128(k_base, 16u, 1024u);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint64_t off = (uint64_t)(((kk / 4) * 16384 + (kk % 4) * 32) >> 4);
+    umma_bf16(tmem_d, a0 + off, b0 + off, idesc, kk > 0 ? 1u : 0u);
+  }
+}
+
+// O (+)= P . V over the first 16 * steps keys of the tile.
+template <int D>
+__device__ __forceinline__ void issue_pv(uint32_t tmem_o, uint32_t tmem_p, uint32_t v_base,
+                                         int steps, bool accumulate) {
+  constexpr uint32_t idesc = make_idesc_bf16(128, D, false, true);
+  const uint64_t b0 = make_sdesc_sw128(v_base, 16384u, 1024u);
+  if (steps == 8) {
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+      umma_bf16_tmem_a(tmem_o, tmem_p + 8u * kk, b0 + (uint64_t)((kk * 2048) >> 4), idesc,
+                       (accumulate || kk > 0) ? 1u : 0u);
+  } else {
+    for (int kk = 0; kk < steps; ++kk)
+      umma_bf16_tmem_a(tmem_o, tmem_p + 8u * kk, b0 + (uint64_t)((kk * 2048) >> 4), idesc,
+                       (accumulate || kk > 0) ? 1u : 0u);
+  }
+}
+
 // A launch whose waits ran out leaves only after copies that may still be in
 // flight have landed (they take microseconds).
 __device__ __forceinline__ void settle_after_abort(volatile int* abort_flag) {

@@ -45,6 +45,34 @@ int check_dense(int n_seqs, const int32_t* cu_q, const int32_t* cu_kv, int Hq, i
   return VSA_OK;
 }
 
+bool view4_ok(const vsa_strides& s, long long B, long long H, long long S) {
+  return view_ok(s, H, S) && (B <= 1 || (s.batch > 0 && s.batch % 8 == 0));
+}
+
+// Sizes of a shared-prefix call; fills the shape fields of `p`.
+int check_prefix(PrefixParams* p, int B, int Hq, int Hkv, int T, int D, int64_t prefix_len,
+                 int64_t suffix_cap) {
+  if (B < 0 || Hq <= 0 || Hkv <= 0 || T < 0 || prefix_len < 0 || suffix_cap < 0) return VSA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return VSA_ERR_UNSUPPORTED;
+  if (Hq % Hkv) return VSA_ERR_SHAPE;
+  // rows, and the key tiles of one key head, are counted in 32 bits
+  const long long per_req = (long long)(Hq / Hkv) * T;
+  if (prefix_len > kMaxRows || suffix_cap > kMaxRows || Hq > 65535 || per_req > (1 << 24) ||
+      B * per_req > (1 << 28) || (long long)B * Hq * T > (1 << 30))
+    return VSA_ERR_UNSUPPORTED;
+  const long long tiles = (B * per_req + 255) / 256 * ((prefix_len + 127) / 128) +
+                          (long long)B * ((per_req + 255) / 256) * ((suffix_cap + 127) / 128);
+  if (tiles > (1 << 30)) return VSA_ERR_UNSUPPORTED;
+  p->B = B;
+  p->Hq = Hq;
+  p->Hkv = Hkv;
+  p->T = T;
+  p->prefix_len = (int)prefix_len;
+  p->suffix_cap = (int)suffix_cap;
+  prefix_shape(p);
+  return VSA_OK;
+}
+
 void contiguous_layout(vsa_dense_layout* L, int64_t q_rows, int64_t kv_rows, int D) {
   const vsa_strides q{0, q_rows * D, D}, kv{0, kv_rows * D, D};
   L->q = L->out = L->dout = L->dq = q;
@@ -91,6 +119,61 @@ int dense_attn_varlen(const void* q, const void* k, const void* v, const vsa_den
   const DenseTensors t{q, k, v, to3(L.q), to3(L.k), to3(L.v), q_rows, keys ? kv_rows : 0};
   const DenseBatch b{cu_seqlens_q, cu_seqlens_kv, n_seqs};
   return launch_dense_fwd(p, t, b, D, static_cast<cudaStream_t>(stream));
+}
+
+size_t shared_prefix_attn_workspace_size(int B, int Hq, int Hkv, int T, int D, int64_t prefix_len,
+                                         int64_t suffix_cap) {
+  PrefixParams p;
+  memset(&p, 0, sizeof(p));
+  if (check_prefix(&p, B, Hq, Hkv, T, D, prefix_len, suffix_cap) != VSA_OK) return 0;
+  return prefix_workspace(&p, D, nullptr);
+}
+
+int shared_prefix_attn(const void* q, const void* k_prefix, const void* v_prefix, const void* k_suffix,
+                       const void* v_suffix, const int32_t* suffix_lens, const vsa_prefix_layout* layout,
+                       int B, int Hq, int Hkv, int T, int D, int64_t prefix_len, int64_t suffix_cap,
+                       float scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  PrefixParams p;
+  memset(&p, 0, sizeof(p));
+  const int rc = check_prefix(&p, B, Hq, Hkv, T, D, prefix_len, suffix_cap);
+  if (rc != VSA_OK) return rc;
+  if (B == 0 || T == 0) return VSA_OK;  // no rows
+  const bool pfx = prefix_len > 0, sfx = suffix_cap > 0;
+  if (!q || !out || !suffix_lens || !(scale == scale) || (pfx && (!k_prefix || !v_prefix)) ||
+      (sfx && (!k_suffix || !v_suffix)))
+    return VSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || (pfx && (!aligned16(k_prefix) || !aligned16(v_prefix))) ||
+      (sfx && (!aligned16(k_suffix) || !aligned16(v_suffix))) ||
+      (reinterpret_cast<uintptr_t>(suffix_lens) & 3u))
+    return VSA_ERR_INVALID_ARG;
+  vsa_prefix_layout L;
+  if (layout) {
+    L = *layout;
+  } else {
+    L.q = L.out = vsa_strides{(int64_t)Hq * T * D, (int64_t)T * D, D};
+    L.k_prefix = L.v_prefix = vsa_strides{0, prefix_len * D, D};
+    L.k_suffix = L.v_suffix = vsa_strides{Hkv * suffix_cap * D, suffix_cap * D, D};
+  }
+  if (!view4_ok(L.q, B, Hq, T) || !view4_ok(L.out, B, Hq, T) ||
+      (pfx && (!view_ok(L.k_prefix, Hkv, prefix_len) || !view_ok(L.v_prefix, Hkv, prefix_len))) ||
+      (sfx && (!view4_ok(L.k_suffix, B, Hkv, suffix_cap) || !view4_ok(L.v_suffix, B, Hkv, suffix_cap))))
+    return VSA_ERR_UNSUPPORTED;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+      workspace_bytes < prefix_workspace(&p, D, workspace))
+    return VSA_ERR_WORKSPACE;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.q_st = to3(L.q);
+  p.out_st = to3(L.out);
+  p.lse = lse;
+  p.lens = suffix_lens;
+  p.scale_log2 = resolve_scale(scale, D) * kLog2e;
+  p.status = device_status_ptr();
+  if (!p.status) return VSA_ERR_CUDA;
+  const PrefixTensors t{k_prefix, v_prefix, k_suffix, v_suffix, to3(L.k_prefix), to3(L.v_prefix),
+                        to3(L.k_suffix), to3(L.v_suffix)};
+  return launch_prefix(p, t, D, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -70,4 +70,34 @@ void fill_dense_seqs(DenseSeqs* t, const int4* seqs, const int* units, int n);
 int launch_dense_fwd(const DenseParams& p, const DenseTensors& t, const DenseBatch& b, int D,
                      cudaStream_t stream);
 
+// Shared-prefix decoding (prefix_attn.cu).  CTAs of its attention kernel: one
+// per SM, and a constant, so that the workspace and the split of the work (and
+// with it the rounding) depend on the arguments alone.
+constexpr int kPrefixGrid = 148;
+struct PrefixParams {
+  const __nv_bfloat16* q;           // [B, Hq, T, D] view
+  __nv_bfloat16* out;
+  Strides3 q_st, out_st;
+  float* lse;                       // [B, Hq, T] or null
+  const int32_t* lens;              // [B] device
+  int B, Hq, Hkv, T, prefix_len, suffix_cap;
+  float scale_log2;
+  int* status;
+  // filled by prefix_shape
+  int group, rows_per_req;          // Hq / Hkv, group * T
+  int pfx_blocks, sfx_blocks;       // row blocks of 256 of a prefix / suffix segment
+  int pfx_rows, sfx_rows;           // rows of a slot's partial result
+  // workspace
+  float *part_p, *part_s, *part_lse_p, *part_lse_s;
+  TmaAxes kp_ax, vp_ax, ks_ax, vs_ax;
+};
+struct PrefixTensors {
+  const void *k_prefix, *v_prefix, *k_suffix, *v_suffix;
+  Strides3 kp_st, vp_st, ks_st, vs_st;
+};
+void prefix_shape(PrefixParams* p);
+// Lays the workspace out at `base` (may be null to size it); its bytes.
+size_t prefix_workspace(PrefixParams* p, int D, void* base);
+int launch_prefix(const PrefixParams& p, const PrefixTensors& t, int D, cudaStream_t stream);
+
 }  // namespace vsa

@@ -576,6 +576,57 @@ int dense_attn_varlen(const void* q, const void* k, const void* v, const vsa_den
                       void* out, float* lse, void* stream);
 
 /* ======================================================================== *
+ * decoding over a shared prefix (ABI 2.2)
+ * ======================================================================== */
+
+/* Strides of a shared_prefix_attn call, head dim contiguous, strides of axes
+ * longer than one positive multiples of 8 elements: q and out [B, Hq, T, D],
+ * k_prefix and v_prefix [Hkv, prefix_len, D] (batch unused), k_suffix and
+ * v_suffix [B, Hkv, suffix_cap, D]. */
+typedef struct vsa_prefix_layout {
+  vsa_strides q, out, k_prefix, v_prefix, k_suffix, v_suffix;
+} vsa_prefix_layout;
+
+/* Workspace bytes shared_prefix_attn needs (0 for invalid arguments). */
+size_t shared_prefix_attn_workspace_size(int B, int Hq, int Hkv, int T, int D, int64_t prefix_len,
+                                         int64_t suffix_cap);
+
+/*
+ * shared_prefix_attn -- attention of the newest T tokens of each of B
+ * requests over a prefix that all requests share (stored and read once) and
+ * over the keys of their own that follow it: the decoding step of many
+ * answers to one prompt, or of unrelated requests (prefix_len = 0).
+ *
+ * Request b has suffix_lens[b] keys of its own, in [0, suffix_cap], the last T
+ * of which are its new tokens' (they are in the cache already).  Token t sees
+ * the whole prefix and its first suffix_lens[b] - T + 1 + t suffix keys; query
+ * head h reads key head h / (Hq / Hkv):
+ *   out = softmax(scale q . k) v    over the keys the row sees
+ * A row that sees no key gives out = 0 and lse = -inf.  What the caches hold
+ * past the lengths never matters (NaN included).
+ *
+ * q            device bf16 [B, Hq, T, D] view
+ * k_prefix, v_prefix  device bf16 [Hkv, prefix_len, D] views (NULL if empty)
+ * k_suffix, v_suffix  device bf16 [B, Hkv, suffix_cap, D] views (NULL if empty)
+ * suffix_lens  device int32 [B], read by the kernels (a captured call follows
+ *              what it holds at replay).  A length outside [0, suffix_cap]
+ *              counts as 0 and sets the device status VSA_ERR_INDEX_RANGE.
+ * layout       host, or NULL for contiguous tensors
+ * out          device bf16 [B, Hq, T, D] view
+ * lse          device fp32 [B, Hq, T], natural-log log-sum-exp, or NULL
+ * workspace    device, >= shared_prefix_attn_workspace_size(...), 256-aligned;
+ *              no two calls in flight may share it
+ * scale        <= 0 selects 1/sqrt(D)
+ * D 64 or 128; Hq a multiple of Hkv (VSA_ERR_SHAPE).  16-byte aligned views.
+ * Two launches on `stream`.
+ */
+int shared_prefix_attn(const void* q, const void* k_prefix, const void* v_prefix, const void* k_suffix,
+                       const void* v_suffix, const int32_t* suffix_lens, const vsa_prefix_layout* layout,
+                       int B, int Hq, int Hkv, int T, int D, int64_t prefix_len, int64_t suffix_cap,
+                       float scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/* ======================================================================== *
  * a7: video tile metadata (host) and token gather / scatter (device)
  * ======================================================================== */
 

@@ -102,6 +102,26 @@ def backward(q, k, v, dout, cu_q, cu_kv, causal=True, scale=None):
     return tuple(grads), tuple(SLACK * (t + U * x.abs()) + 1e-30 for t, x in zip(tols, grads))
 
 
+def decode(q, kp, vp, ks, vs, lens, scale=None):
+    """(out, lse, tol_out, tol_lse) fp64 on the CPU of shared-prefix decoding;
+    partial results and their joining stay in fp32 (PEXP covers the weights),
+    so the bounds are the forward's."""
+    lens = [int(n) for n in lens]
+    q, kp, vp, ks, vs = (x.detach().double().cpu() for x in (q, kp, vp, ks, vs))
+    scale = 1.0 / math.sqrt(q.shape[3]) if scale is None else scale
+    b, hq, t, _ = q.shape
+    p, g = kp.shape[1], hq // kp.shape[0]
+    out, tol = torch.zeros_like(q), torch.zeros_like(q)
+    lse, tol_lse = torch.zeros(q.shape[:3], dtype=q.dtype), torch.zeros(q.shape[:3], dtype=q.dtype)
+    for i in range(b):
+        seen = torch.arange(p + lens[i])[None, :] < (p + (lens[i] - t + 1 + torch.arange(t)).clamp_min(0))[:, None]
+        for h in range(hq):
+            k = torch.cat([kp[h // g], ks[i, h // g, :lens[i]]])
+            v = torch.cat([vp[h // g], vs[i, h // g, :lens[i]]])
+            _, out[i, h], lse[i, h], tol[i, h], tol_lse[i, h], _, _ = attend(q[i, h], k, v, scale, seen)
+    return out, lse, tol, tol_lse
+
+
 def assert_within(got, want, tol, what):
     got = got.detach().double().cpu()
     assert got.shape == want.shape, (what, got.shape, want.shape)

@@ -53,3 +53,44 @@ def test_dense_argument_checks():
 
 def test_dense_without_rows_is_a_no_op():
     assert _dense(cq=[0, 0], q=None, k=None, v=None, out=None) == 0
+
+
+def _prefix(**kw):
+    a = dict(q=FAKE, kp=FAKE, vp=FAKE, ks=FAKE, vs=FAKE, lens=FAKE, layout=None, b=2, hq=4, hkv=2, t=1, d=128,
+             p=100, s=50, scale=0.0, out=FAKE, lse=None, ws=FAKE, bytes=1 << 30)
+    a.update(kw)
+    return _lib().shared_prefix_attn(
+        _p(a["q"]), _p(a["kp"]), _p(a["vp"]), _p(a["ks"]), _p(a["vs"]), _p(a["lens"]), a["layout"], a["b"],
+        a["hq"], a["hkv"], a["t"], a["d"], a["p"], a["s"], a["scale"], _p(a["out"]), _p(a["lse"]), _p(a["ws"]),
+        a["bytes"], None)
+
+
+def _prefix_layout(**kw):
+    from block_sparse_attention_15_b200 import binding as B
+    base = dict(q=(512, 128, 128), out=(512, 128, 128), k_prefix=(0, 12800, 128), v_prefix=(0, 12800, 128),
+                k_suffix=(12800, 6400, 128), v_suffix=(12800, 6400, 128))
+    base.update(kw)
+    return ctypes.byref(B.VsaPrefixLayout(*[B.VsaStrides(*base[n]) for n, _ in B.VsaPrefixLayout._fields_]))
+
+
+def test_prefix_argument_checks():
+    for n in ("q", "kp", "vp", "ks", "vs", "lens", "out"):
+        assert _prefix(**{n: None}) == 1
+        assert _prefix(**{n: FAKE + 2}) == 1                             # misaligned
+    assert _prefix(b=-1) == 1 and _prefix(t=-1) == 1 and _prefix(p=-1) == 1 and _prefix(s=-1) == 1
+    assert _prefix(hkv=0) == 1 and _prefix(scale=float("nan")) == 1
+    assert _prefix(hq=5) == 2
+    assert _prefix(d=96) == 3 and _prefix(p=1 << 31) == 3 and _prefix(s=1 << 31) == 3
+    assert _prefix(b=1 << 20, t=1 << 10) == 3                            # rows are counted in 32 bits
+    assert _prefix(b=1 << 16, s=1 << 30) == 3                            # key tiles too
+    assert _prefix(layout=_prefix_layout(q=(510, 128, 128))) == 3
+    assert _prefix(layout=_prefix_layout(k_suffix=(0, 6400, 128))) == 3  # broadcast suffix
+    assert _prefix(layout=_prefix_layout(v_prefix=(0, 12800, 132))) == 3
+    assert _prefix(ws=None) == 7 and _prefix(ws=FAKE + 16) == 7
+    need = _lib().shared_prefix_attn_workspace_size(2, 4, 2, 1, 128, 100, 50)
+    assert need > 0 and _prefix(bytes=need - 1) == 7
+
+
+def test_prefix_without_rows_is_a_no_op():
+    assert _prefix(b=0) == 0 and _prefix(t=0) == 0
+    assert _lib().shared_prefix_attn_workspace_size(2, 5, 2, 1, 128, 100, 50) == 0
