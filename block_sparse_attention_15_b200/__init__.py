@@ -15,6 +15,7 @@ from .binding import (  # noqa: F401
     build_vsa_metadata,
     check_device_status,
     dense_attn_varlen,
+    dense_attn_varlen_backward,
     gather_tokens,
     get_device_status,
     lib,
@@ -28,7 +29,7 @@ from .binding import (  # noqa: F401
 __all__ = [
     "VSAError", "block_sparse_attn", "block_sparse_attn_backward",
     "block_sparse_attn_from_indices", "block_sparse_attn_varlen_backward", "block_sparse_attn_varlen", "build_vsa_metadata",
-    "check_device_status", "dense_attn_varlen", "gather_tokens", "get_device_status", "lib", "scatter_tokens",
+    "check_device_status", "dense_attn_varlen", "dense_attn_varlen_backward", "gather_tokens", "get_device_status", "lib", "scatter_tokens",
     "shared_prefix_attn",
     "vsa_forward", "vsa_forward_host", "video_sparse_attn_bshd",
 ]

@@ -110,6 +110,10 @@ SIGNATURES = {
                                                  _c_void_p, _c_size_t, _c_void_p]),
     "dense_attn_varlen": (_c_int, [_c_void_p] * 3 + [_PDL, _P32, _P32] + [_c_int] * 4 +
                           [_c_int64, _c_int64, _c_int, _c_float, _c_void_p, _c_void_p, _c_void_p]),
+    "dense_attn_varlen_backward_workspace_size": (_c_size_t, [_c_int, _c_int64]),
+    "dense_attn_varlen_backward": (_c_int, [_c_void_p] * 6 + [_PDL, _P32, _P32] + [_c_int] * 4 +
+                                   [_c_int64, _c_int64, _c_int, _c_float, _c_void_p, _c_void_p, _c_void_p,
+                                    _c_void_p, _c_size_t, _c_void_p]),
     "shared_prefix_attn_workspace_size": (_c_size_t, [_c_int] * 5 + [_c_int64] * 2),
     "shared_prefix_attn": (_c_int, [_c_void_p] * 6 + [ctypes.POINTER(VsaPrefixLayout)] + [_c_int] * 5 +
                            [_c_int64, _c_int64, _c_float, _c_void_p, _c_void_p, _c_void_p, _c_size_t,
@@ -704,6 +708,52 @@ def dense_attn_varlen(q, k, v, cu_seqlens_q, cu_seqlens_kv, *, causal: bool = Tr
             _ptr(q), _ptr(k), _ptr(v), ctypes.byref(lay), cq_p, ck_p, len(cq) - 1, Hq, Hkv, D, Sq, Skv,
             1 if causal else 0, float(scale) if scale is not None else 0.0, _ptr(out), _ptr(lse), st))
     return (out, lse) if return_lse else out
+
+
+def dense_attn_varlen_backward(q, k, v, out, dout, lse, cu_seqlens_q, cu_seqlens_kv, *, causal: bool = True,
+                               scale: float | None = None, dq=None, dk=None, dv=None, workspace=None,
+                               stream=None):
+    """(dq, dk, dv) of :func:`dense_attn_varlen` (``dense_attn_varlen_backward``);
+    ``out`` and ``lse`` come from that call, the other arguments are its own.
+    ``dout`` and the gradients may be strided views like q and k.  dk and dv sum
+    over the query heads of a key head.  Rows of given gradients past the last
+    sequence are left as they were (0 where they are allocated here)."""
+    Hq, Hkv, D, Sq, Skv, cq, cq_p, ck, ck_p = _dense_common(q, k, v, cu_seqlens_q, cu_seqlens_kv)
+    for t, n in ((out, "out"), (dout, "dout")):
+        _require_rows(t, n)
+        if t.shape != q.shape:
+            raise ValueError(f"{n} must be shaped like q")
+    _require(lse, torch.float32, "lse")
+    if lse.shape != (Hq, Sq):
+        raise ValueError(f"lse must be [Hq, q_rows] = {(Hq, Sq)}")
+    given = {"dq": dq, "dk": dk, "dv": dv}
+    for n, like in (("dq", q), ("dk", k), ("dv", v)):
+        if given[n] is not None:
+            _require_rows(given[n], n)
+            if given[n].shape != like.shape:
+                raise ValueError(f"{n} must be shaped like {n[1]}")
+    _same_device(q.device, out=out, dout=dout, lse=lse, workspace=workspace, **given)
+    L = lib()
+    with _Launch(q.device, stream) as st:
+        grads = []
+        for n, like, cu in (("dq", q, cq), ("dk", k, ck), ("dv", v, ck)):
+            g = given[n]
+            if g is None:
+                g = torch.empty_like(like)
+                rows = like.shape[1]
+                tail = int(cu[-1]) if 0 <= cu[-1] <= rows else rows
+                if tail < rows:
+                    g[:, tail:].zero_()
+            grads.append(g)
+        if workspace is None:
+            need = L.dense_attn_varlen_backward_workspace_size(Hq, Sq)
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        lay = VsaDenseLayout(*[_strides_rows(t) for t in (q, k, v, out, dout, *grads)])
+        _check("dense_attn_varlen_backward", L.dense_attn_varlen_backward(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(dout), _ptr(lse), ctypes.byref(lay), cq_p, ck_p,
+            len(cq) - 1, Hq, Hkv, D, Sq, Skv, 1 if causal else 0, float(scale) if scale is not None else 0.0,
+            _ptr(grads[0]), _ptr(grads[1]), _ptr(grads[2]), _ptr(workspace), workspace.numel(), st))
+    return tuple(grads)
 
 
 def shared_prefix_attn(q, k_prefix, v_prefix, k_suffix, v_suffix, suffix_lens, *,

@@ -1,0 +1,998 @@
+// Dense softmax attention over packed sequences with grouped heads, causal or
+// full: the gradients.
+//
+// What it computes, per sequence and query head h (key head h / G), from the
+// forward's out and lse (row r sees its first n(r) keys, see dense_fwd.cu):
+//   p(r, j) = exp(scale q_r . k_j - lse(r))          (0 for j >= n(r))
+//   delta(r) = sum_d dout(r, d) out(r, d)
+//   ds(r, j) = p(r, j) (dout_r . v_j - delta(r))
+//   dq_r = scale sum_j ds(r, j) k_j
+//   dk_j = scale sum_{h, r} ds(r, j) q_r             (over the heads of the group)
+//   dv_j = sum_{h, r} p(r, j) dout_r
+//
+// How (sm_100a): two kernels, each with one kind of accumulator in TMEM, so
+// that every sum has one owner and a fixed order (no atomics, no fp32 copies
+// of the gradients in memory).  The price is that S and dout V^T are formed
+// twice (7 products of 128 x 128 x D instead of 5).  One kernel for all five
+// would send its dq tiles to memory as fp32 sums, 64 KB per pair of tiles each
+// way through shared memory, and keep dS there too: its shared-memory traffic
+// (128 bytes a cycle) would take as long as these seven products.
+//
+//  dq:     a work item is one 128-row query tile of one head.  Per key tile
+//            S = Q K^T, dP = dO V^T, dQ += dS K
+//          Q, dO (bf16) and dS are A operands in TMEM, so only K and V tiles
+//          are read from shared memory.
+//  dk/dv:  a work item is one 128-row key tile of one key head; it walks the
+//          query tiles of all heads of the group that see it.  Per query tile
+//            S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q
+//          P^T and dS^T are A operands in TMEM, over their own S and dP.
+//
+// Both: persistent grid, one CTA per SM, 512 threads: warp 0 tile loads, warp
+// 1 products, warps 2-3 helpers, warps 4-11 softmax (one thread per TMEM lane
+// and half of the 128 columns), warps 12-15 epilogue.  Products are issued in
+// the order S(i+1), dQ(i), dP(i+1) and dP(i), dV(i), S(i+1), dK(i): the
+// exponentials of a tile run under the previous tile's last product, its dS
+// under the next tile's S.
+// P and dS are rounded to bf16 for the tensor core; everything else is fp32.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "dense_attn.cuh"
+#include "dense_launch.h"
+#include "vsa.h"
+#include "vsa_device.cuh"
+
+namespace vsa {
+namespace dense {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr uint32_t kRegsProducer = 80, kRegsSoftmax = 184, kRegsEpilogue = 64;
+constexpr uint32_t kLaunchRegs = 128;  // 512 x 128 = 65536
+static_assert(128u * (kRegsProducer + 2u * kRegsSoftmax + kRegsEpilogue) <= 512u * kLaunchRegs,
+              "register split exceeds the launch's registers");
+constexpr uint32_t kTmemCols = 512;
+constexpr float kLog2 = 1.4426950408889634f;
+#ifndef DENSE_BWD_POLY8
+#define DENSE_BWD_POLY8 2  // column pairs in eight whose exponential runs on the FMA pipe
+#endif
+
+__device__ __forceinline__ uint32_t sw128(uint32_t row, uint32_t chunk) {
+  return row * 128u + ((chunk ^ (row & 7u)) << 4);
+}
+
+// D = A B^T: A [128][D] bf16 in TMEM, B a tile [D / 64][128 rows][128 B].
+template <int D>
+__device__ __forceinline__ void issue_ta(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_base) {
+  constexpr uint32_t idesc = make_idesc_bf16(128, 128, false, false);
+  const uint64_t b0 = make_sdesc_sw128(b_base, 16u, 1024u);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk)
+    umma_bf16_tmem_a(tmem_d, tmem_a + 8u * kk,
+                     b0 + (uint64_t)(((kk / 4) * 16384 + (kk % 4) * 32) >> 4), idesc, kk > 0 ? 1u : 0u);
+}
+
+// D (+)= A B over the first 16 * steps rows of the tile B [D / 64][128][128 B];
+// A [128][128] bf16 in TMEM: columns 0-63 at tmem_a, 64-127 at tmem_a + 64
+// (each half over the fp32 columns of the softmax warpgroup that wrote it).
+template <int D>
+__device__ __forceinline__ void issue_halves(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_base,
+                                             int steps, bool accumulate) {
+  constexpr uint32_t idesc = make_idesc_bf16(128, D, false, true);
+  const uint64_t b0 = make_sdesc_sw128(b_base, 16384u, 1024u);
+  if (steps == 8) {
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+      umma_bf16_tmem_a(tmem_d, tmem_a + 64u * (kk / 4) + 8u * (kk % 4), b0 + (uint64_t)((kk * 2048) >> 4),
+                       idesc, (accumulate || kk > 0) ? 1u : 0u);
+  } else {
+    for (int kk = 0; kk < steps; ++kk)
+      umma_bf16_tmem_a(tmem_d, tmem_a + 64u * (kk / 4) + 8u * (kk % 4), b0 + (uint64_t)((kk * 2048) >> 4),
+                       idesc, (accumulate || kk > 0) ? 1u : 0u);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dq
+// ---------------------------------------------------------------------------
+template <int D>
+struct QLayout {
+  static constexpr int DH = D / 64;
+  static constexpr uint32_t kTile = 128u * D * 2u;
+  static constexpr int NST = D == 128 ? 6 : 10;  // ring: Q, dO, K(0), V(0), K(1), ...
+  static constexpr uint32_t kRingOff = 0;
+  static constexpr uint32_t kRowOff = kRingOff + NST * kTile;  // [2][2][128] f32: -lse, delta
+  static constexpr uint32_t kBarOff = kRowOff + 2048u;
+  // Q and dO of an item signal a barrier of the item's, K and V tiles their
+  // stage's.  Four of the former: the ring holds the Q and dO of fewer than
+  // four items ahead of the one whose operands are being copied.
+  static constexpr int NOP = 4;
+  static_assert(NST <= 4 * (NOP - 1), "an item takes four stages or more");
+  static constexpr int kFull = 0, kEmpty = NST, kPre = 2 * NST, kOpFull = 3 * NST,
+                       kOpReady = kOpFull + NOP, kOpFree = kOpReady + 2, kSFull = kOpFree + 1, kSFree = kSFull + 1,
+                       kDPFull = kSFree + 1, kDSFull = kDPFull + 1, kOFull = kDSFull + 1,
+                       kOEmpty = kOFull + 1, kNumBars = kOEmpty + 1;
+  static constexpr uint32_t kMiscOff = kBarOff + 8u * kNumBars;
+  static constexpr uint32_t kAlloc = kMiscOff + 16u + 1024u;
+  static_assert(kAlloc <= 227u * 1024u, "shared memory");
+};
+// TMEM columns
+constexpr uint32_t kQS = 0, kQDP = 128, kQDQ = 256, kQQ = 384, kQDO = 448;
+
+struct QItem {
+  int head, hk;
+  int row0, rows;  // rows of q
+  int kv0, kv_len;
+  int lim0;        // keys that tile row 0 sees (causal: row r sees lim0 + r, may be <= 0)
+  int last;        // keys that the last real row sees
+  int n;           // key tiles
+};
+
+__device__ __forceinline__ QItem load_qitem(const DenseBwdParams& p, const DenseSeqs& t, int w) {
+  QItem x;
+  x.hk = w % p.Hkv;
+  const Unit un = find_unit(t, w / p.Hkv);
+  const int4 q = t.seq[un.seq];
+  const int tile = un.rank / p.group;
+  x.head = x.hk * p.group + (un.rank - tile * p.group);
+  x.row0 = q.x + 128 * tile;
+  x.rows = min(128, q.y - 128 * tile);
+  x.kv0 = q.z;
+  x.kv_len = q.w;
+  x.lim0 = p.causal ? q.w - q.y + 128 * tile + 1 : q.w;
+  x.last = p.causal ? max(0, x.lim0 + x.rows - 1) : q.w;
+  x.n = (x.last + 127) >> 7;
+  return x;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    dense_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+                    const __grid_constant__ DenseBwdParams p, const __grid_constant__ DenseSeqs seqs) {
+  using L = QLayout<D>;
+  constexpr int NST = L::NST;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  float* rowv = reinterpret_cast<float*>(smem + L::kRowOff);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
+
+  const int tid = threadIdx.x;
+  const int warp = tid / 32, lane = tid % 32;
+  const int cta = blockIdx.x, grid = gridDim.x;
+
+  if (tid == 0) {
+    for (int i = 0; i < L::kNumBars; ++i) {
+      // a TMA transaction, a commit or one thread's arrival, except where the
+      // epilogue's four or the softmax's eight warps arrive
+      const uint32_t count = (i == L::kOpReady || i == L::kOpReady + 1 || i == L::kOEmpty) ? 4u
+                             : (i == L::kSFree || i == L::kDSFull)                          ? 8u
+                                                                                            : 1u;
+      mbar_init(bars + i, count);
+    }
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    tma_prefetch_desc(&tm_do);
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp < 4) {
+    regs_dec<kRegsProducer>();
+    if (warp == 0) {
+      // ===================== tile loads =====================
+      if (lane == 0) {
+        const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
+        uint32_t g = 0, n_item = 0;
+        bool ok = true;
+        for (int w = 0, it; ok && (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
+          if (it >= p.n_work) continue;
+          const QItem x = load_qitem(p, seqs, it);
+          if (x.n == 0) continue;
+          for (int j = 0; ok && j < 2 * x.n + 2; ++j, ++g) {
+            const int st = (int)(g % NST);
+            const uint32_t u = g / NST;
+            if (u >= 1) ok = mbar_wait(bars + L::kEmpty + st, (u - 1) & 1, abort_flag, p.status);
+            if (!ok) break;
+            uint8_t* dst = smem + L::kRingOff + st * L::kTile;
+            const int key = 128 * ((j >> 1) - 1);
+            const bool second = j & 1;
+            // a K tile with rows past the sequence goes through warp 2 first
+            uint64_t* full = bars + (j < 2 ? L::kOpFull + (int)(n_item % L::NOP)
+                                           : (!second && x.kv_len - key < 128 ? L::kPre : L::kFull) + st);
+            if (j != 1) mbar_arrive_expect_tx(full, j == 0 ? 2 * L::kTile : L::kTile);
+#pragma unroll
+            for (int dh = 0; dh < L::DH; ++dh) {
+              uint8_t* to = dst + dh * 16384;
+              if (j < 2)
+                load_rows(to, second ? &tm_do : &tm_q, second ? p.do_ax : p.q_ax, full, dh * 64, x.row0,
+                          x.head, 0, once);
+              else
+                load_rows(to, second ? &tm_v : &tm_k, second ? p.v_ax : p.k_ax, full, dh * 64, x.kv0 + key,
+                          x.hk, 0, keep);
+            }
+          }
+          ++n_item;
+        }
+        // every stage's release lands before exit
+        for (uint32_t t = (g > (uint32_t)NST ? g - NST : 0u); ok && t < g; ++t)
+          ok = mbar_wait(bars + L::kEmpty + (int)(t % NST), (t / NST) & 1, abort_flag, p.status);
+      }
+      __syncwarp();
+    } else if (warp == 2) {
+      // ===================== zero K rows past a sequence's keys (0 * inf is not 0) =====================
+      uint32_t g = 0, pre = 0;
+      for (int w = 0, it; (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
+        if (it >= p.n_work) continue;
+        const QItem x = load_qitem(p, seqs, it);
+        if (x.n == 0) continue;
+        g += 2 * x.n + 2;
+        const int len = x.kv_len - 128 * (x.n - 1);
+        if (len >= 128) continue;
+        const int st = (int)((g - 2) % NST);
+        if (!warp_wait(bars + L::kPre + st, (pre >> st) & 1, abort_flag, p.status)) break;
+        pre ^= 1u << st;
+        // products stop at the next multiple of 16 keys
+        zero_rows<128>(smem + L::kRingOff + st * L::kTile, L::DH, len, (len + 15) & ~15, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + L::kFull + st);
+      }
+    } else if (warp == 1) {
+      // ===================== MMA issue =====================
+      uint32_t g = 0;            // ring tiles before the current item
+      uint32_t n_item = 0;       // items so far
+      uint32_t ts = 0, tq = 0;   // S and dQ products so far
+      uint32_t phase = 0;        // phase bit per ring stage
+      bool ok = true;
+      QItem x = {};
+      auto full = [&](uint32_t at) {
+        const int st = (int)(at % NST);
+        const bool r = warp_wait(bars + L::kFull + st, (phase >> st) & 1, abort_flag, p.status);
+        phase ^= 1u << st;
+        tc_fence_after_sync();
+        return r;
+      };
+      auto do_s = [&](int j) {
+        if (j == 0) {
+          // Q and dO are in TMEM; their ring stages are free again
+          if (!warp_wait(bars + L::kOpReady + (n_item & 1), (n_item >> 1) & 1, abort_flag, p.status)) { ok = false; return; }
+          if (elect_one()) {
+            mbar_arrive(bars + L::kEmpty + (int)(g % NST));
+            mbar_arrive(bars + L::kEmpty + (int)((g + 1) % NST));
+          }
+          __syncwarp();
+        }
+        const uint32_t at = g + 2 + 2 * j;
+        if (!full(at)) { ok = false; return; }
+        if (ts >= 1 && !warp_wait(bars + L::kSFree, (ts - 1) & 1, abort_flag, p.status)) { ok = false; return; }
+        ++ts;
+        tc_fence_after_sync();
+        if (elect_one()) {
+          issue_ta<D>(tmem_base + kQS, tmem_base + kQQ, sbase + L::kRingOff + (at % NST) * L::kTile);
+          umma_commit(bars + L::kSFull);
+        }
+        __syncwarp();
+      };
+      auto do_dp = [&](int j) {
+        const uint32_t at = g + 3 + 2 * j;
+        if (!full(at)) { ok = false; return; }
+        if (elect_one()) {
+          issue_ta<D>(tmem_base + kQDP, tmem_base + kQDO, sbase + L::kRingOff + (at % NST) * L::kTile);
+          umma_commit(bars + L::kDPFull);
+          umma_commit(bars + L::kEmpty + (int)(at % NST));
+          if (j == x.n - 1) umma_commit(bars + L::kOpFree);
+        }
+        __syncwarp();
+      };
+      for (int w = 0, it; ok && (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
+        if (it >= p.n_work) continue;
+        x = load_qitem(p, seqs, it);
+        if (x.n == 0) continue;
+        do_s(0);
+        if (ok) do_dp(0);
+        for (int j = 0; ok && j < x.n; ++j) {
+          if (j + 1 < x.n) do_s(j + 1);
+          if (!ok) break;
+          // the epilogue has taken the previous item's dQ
+          if (j == 0 && n_item >= 1 &&
+              !warp_wait(bars + L::kOEmpty, (n_item - 1) & 1, abort_flag, p.status)) { ok = false; break; }
+          if (!warp_wait(bars + L::kDSFull, tq & 1, abort_flag, p.status)) { ok = false; break; }
+          ++tq;
+          tc_fence_after_sync();
+          if (elect_one()) {
+            const uint32_t st = (g + 2 + 2 * j) % NST;
+            const int keys = x.last - 128 * j;
+            issue_halves<D>(tmem_base + kQDQ, tmem_base + kQDP, sbase + L::kRingOff + st * L::kTile,
+                            keys >= 128 ? 8 : (keys + 15) >> 4, j > 0);
+            umma_commit(bars + L::kEmpty + (int)st);
+            if (j == x.n - 1) umma_commit(bars + L::kOFull);
+          }
+          __syncwarp();
+          if (j + 1 < x.n) do_dp(j + 1);
+        }
+        g += 2 * x.n + 2;
+        ++n_item;
+      }
+    }
+  } else if (warp < 12) {
+    regs_inc<kRegsSoftmax>();
+    // ===================== p and ds: one thread per query row and 64 keys =====================
+    const int half = (warp - 4) >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t t_lane = tmem_base + (uint32_t((warp & 3) * 32) << 16) + 64u * half;
+    const uint64_t cc = pk2(p.scale_log2, p.scale_log2);
+    uint32_t g = 0, n_item = 0;
+    bool ok = true;
+    for (int w = 0, it; ok && (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
+      if (it >= p.n_work) continue;
+      const QItem x = load_qitem(p, seqs, it);
+      if (x.n == 0) continue;
+      if (!warp_wait(bars + L::kOpReady + (n_item & 1), (n_item >> 1) & 1, abort_flag, p.status)) break;
+      const float nl = rowv[(n_item & 1) * 256 + row], nd = -rowv[(n_item & 1) * 256 + 128 + row];
+      const uint64_t nl2 = pk2(nl, nl), nd2 = pk2(nd, nd);
+      ++n_item;
+      const int limit = p.causal ? min(x.lim0 + row, x.kv_len) : x.kv_len;  // keys this row sees
+      for (int j = 0; j < x.n; ++j, ++g) {
+        if (!warp_wait(bars + L::kSFull, g & 1, abort_flag, p.status)) { ok = false; break; }
+        tc_fence_after_sync();
+        uint32_t v[64];
+        tmem_ld64(t_lane + kQS, v);
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + L::kSFree);
+#pragma unroll
+        for (int q = 0; q < 32; ++q) {
+          const uint64_t e = ffma2(pk2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1])), cc, nl2);
+          float a, b;
+          upk2(e, a, b);
+          if ((q & 7) < DENSE_BWD_POLY8) {
+            upk2(exp2_fma2_t<true>(a, b), a, b);
+          } else {
+            a = fast_exp2(a);
+            b = fast_exp2(b);
+          }
+          v[2 * q] = __float_as_uint(a);
+          v[2 * q + 1] = __float_as_uint(b);
+        }
+        if (!warp_wait(bars + L::kDPFull, g & 1, abort_flag, p.status)) { ok = false; break; }
+        tc_fence_after_sync();
+        const int rem = limit - 128 * j - 64 * half;
+        const bool masked = __any_sync(0xffffffffu, rem < 64);
+#pragma unroll
+        for (int q0 = 0; q0 < 32; q0 += 16) {
+          uint32_t dp[32], pk[16];
+          tmem_ld32(t_lane + kQDP + 2 * q0, dp);
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            const int e = 2 * (q0 + q);
+            float a, b;
+            upk2(fadd2(pk2(__uint_as_float(dp[2 * q]), __uint_as_float(dp[2 * q + 1])), nd2), a, b);
+            a *= __uint_as_float(v[e]);
+            b *= __uint_as_float(v[e + 1]);
+            if (masked) {
+              a = e < rem ? a : 0.f;
+              b = e + 1 < rem ? b : 0.f;
+            }
+            pk[q] = pack_bf16x2(a, b);
+          }
+          // the first 32 words lie over columns that this thread has read
+          VSA_TMEM_ST16(t_lane + kQDP + q0, pk, 0);
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + L::kDSFull);
+      }
+    }
+  } else {
+    regs_dec<kRegsEpilogue>();
+    // ===================== operands, delta and results: one thread per query row =====================
+    const int row = (warp - 12) * 32 + lane;
+    const uint32_t t_lane = tmem_base + (uint32_t((warp - 12) * 32) << 16);
+    uint32_t g = 0, n_item = 0;
+    bool ok = true;
+    QItem prev = {};
+    auto read_out = [&](const QItem& x, uint32_t idx) {
+      if (!warp_wait(bars + L::kOFull, idx & 1, abort_flag, p.status)) return false;
+      tc_fence_after_sync();
+      __nv_bfloat16* to = p.dq + x.head * p.dq_st.h + (long long)(x.row0 + row) * p.dq_st.s;
+#pragma unroll 1
+      for (int q0 = 0; q0 < D; q0 += 32) {
+        uint32_t ov[32];
+        tmem_ld32(t_lane + kQDQ + q0, ov);
+        if (q0 + 32 == D) {
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars + L::kOEmpty);
+        }
+        if (row < x.rows) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t o[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              o[q] = pack_bf16x2(__uint_as_float(ov[e + 2 * q]) * p.scale,
+                                 __uint_as_float(ov[e + 2 * q + 1]) * p.scale);
+            *reinterpret_cast<uint4*>(to + q0 + e) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+      }
+      return true;
+    };
+    for (int w = 0, it; ok && (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
+      if (it >= p.n_work) continue;
+      const QItem x = load_qitem(p, seqs, it);
+      const bool real = row < x.rows;
+      if (x.n == 0) {
+        // rows that see no key
+        if (real) {
+          __nv_bfloat16* to = p.dq + x.head * p.dq_st.h + (long long)(x.row0 + row) * p.dq_st.s;
+#pragma unroll
+          for (int e = 0; e < D; e += 8) *reinterpret_cast<uint4*>(to + e) = make_uint4(0u, 0u, 0u, 0u);
+          p.delta[x.head * p.lse_seq + x.row0 + row] = 0.f;
+        }
+        continue;
+      }
+      const uint32_t sq = g % NST, sd = (g + 1) % NST;
+      if (!warp_wait(bars + L::kOpFull + (int)(n_item % L::NOP), (n_item / L::NOP) & 1, abort_flag, p.status)) break;
+      const uint8_t* qt = smem + L::kRingOff + sq * L::kTile;
+      const uint8_t* dt = smem + L::kRingOff + sd * L::kTile;
+      // delta, from the dO tile and the out row
+      float delta = 0.f, lse = 0.f;
+      if (real) {
+        const __nv_bfloat16* orow = p.out + x.head * p.out_st.h + (long long)(x.row0 + row) * p.out_st.s;
+        lse = p.lse[x.head * p.lse_seq + x.row0 + row];
+#pragma unroll 4
+        for (int ch = 0; ch < D / 8; ++ch) {
+          const uint4 o4 = *reinterpret_cast<const uint4*>(orow + 8 * ch);
+          const uint4 d4 = *reinterpret_cast<const uint4*>(dt + (ch >> 3) * 16384 + sw128(row, ch & 7));
+          const __nv_bfloat162* o2 = reinterpret_cast<const __nv_bfloat162*>(&o4);
+          const __nv_bfloat162* d2 = reinterpret_cast<const __nv_bfloat162*>(&d4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 a = __bfloat1622float2(o2[e]), c = __bfloat1622float2(d2[e]);
+            delta = fmaf(a.x, c.x, delta);
+            delta = fmaf(a.y, c.y, delta);
+          }
+        }
+        if (lse == -INFINITY) lse = delta = 0.f;  // a row that sees no key: all of it is masked
+        p.delta[x.head * p.lse_seq + x.row0 + row] = delta;
+      }
+      rowv[(n_item & 1) * 256 + row] = -lse * kLog2;
+      rowv[(n_item & 1) * 256 + 128 + row] = delta;
+      // the previous item's last product with Q and dO is complete
+      if (n_item >= 1 && !warp_wait(bars + L::kOpFree, (n_item - 1) & 1, abort_flag, p.status)) break;
+      tc_fence_after_sync();
+#pragma unroll 1
+      for (int c0 = 0; c0 < D / 8; c0 += 4) {
+        uint32_t a[16], b[16];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int ch = c0 + c;
+          const uint32_t off = (ch >> 3) * 16384 + sw128(row, ch & 7);
+          const uint4 x4 = *reinterpret_cast<const uint4*>(qt + off);
+          const uint4 y4 = *reinterpret_cast<const uint4*>(dt + off);
+          a[4 * c] = x4.x, a[4 * c + 1] = x4.y, a[4 * c + 2] = x4.z, a[4 * c + 3] = x4.w;
+          b[4 * c] = y4.x, b[4 * c + 1] = y4.y, b[4 * c + 2] = y4.z, b[4 * c + 3] = y4.w;
+        }
+        VSA_TMEM_ST16(t_lane + kQQ + 4 * c0, a, 0);
+        VSA_TMEM_ST16(t_lane + kQDO + 4 * c0, b, 0);
+      }
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + L::kOpReady + (n_item & 1));
+      if (n_item >= 1 && !read_out(prev, n_item - 1)) { ok = false; break; }
+      prev = x;
+      g += 2 * x.n + 2;
+      ++n_item;
+    }
+    if (ok && !*abort_flag && n_item >= 1) read_out(prev, n_item - 1);
+  }
+
+  settle_after_abort(abort_flag);
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem_base, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dk and dv
+// ---------------------------------------------------------------------------
+template <int D>
+struct KLayout {
+  static constexpr int DH = D / 64;
+  static constexpr uint32_t kTile = 128u * D * 2u;
+  static constexpr int NST = D == 128 ? 4 : 8;  // ring: Q(0), dO(0), Q(1), ...
+  static constexpr int NROW = 4;                // ring of -lse and delta rows
+  static constexpr uint32_t kKOff = 0, kVOff = kTile;
+  static constexpr uint32_t kRingOff = 2 * kTile;
+  static constexpr uint32_t kRowOff = kRingOff + NST * kTile;  // [NROW][2][128] f32
+  static constexpr uint32_t kBarOff = kRowOff + NROW * 1024u;
+  static constexpr int kFull = 0, kEmpty = NST, kPre = 2 * NST, kRowFull = 3 * NST,
+                       kRowEmpty = kRowFull + NROW, kKVFull = kRowEmpty + NROW, kKVEmpty = kKVFull + 1,
+                       kSFull = kKVEmpty + 1, kPFull = kSFull + 1, kDPFull = kPFull + 1,
+                       kDSFull = kDPFull + 1, kOFull = kDSFull + 1, kOEmpty = kOFull + 1,
+                       kNumBars = kOEmpty + 1;
+  static constexpr uint32_t kMiscOff = kBarOff + 8u * kNumBars;
+  static constexpr uint32_t kAlloc = kMiscOff + 16u + 1024u;
+  static_assert(kAlloc <= 227u * 1024u, "shared memory");
+};
+constexpr uint32_t kKS = 0, kKDP = 128, kKDV = 256, kKDK = 384;
+
+struct KItem {
+  int hk;
+  int key0, keys;  // rows of k
+  int q0, q_len;   // first row of q that sees the tile, and the rows from there on
+  int diag;        // causal: tile key i is seen by rows q0 + r with r + diag >= i
+  int tiles;       // query tiles of one head
+  int n;           // query tiles of all heads of the group
+};
+
+__device__ __forceinline__ KItem load_kitem(const DenseBwdParams& p, const DenseSeqs& t, int w) {
+  KItem x;
+  x.hk = w % p.Hkv;
+  const Unit un = find_unit(t, w / p.Hkv);
+  const int4 q = t.seq[un.seq];
+  // the first key tiles are seen by the most rows: longest first
+  const int tile = t.units[un.seq] - 1 - un.rank;
+  x.key0 = q.z + 128 * tile;
+  x.keys = min(128, q.w - 128 * tile);
+  const int off = q.w - q.y;
+  const int skip = p.causal ? max(0, 128 * tile - off) : 0;
+  x.q0 = q.x + skip;
+  x.q_len = max(0, q.y - skip);
+  x.diag = skip + off - 128 * tile;
+  x.tiles = (x.q_len + 127) >> 7;
+  x.n = x.tiles * p.group;
+  return x;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    dense_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+                     const __grid_constant__ DenseBwdParams p, const __grid_constant__ DenseSeqs seqs) {
+  using L = KLayout<D>;
+  constexpr int NST = L::NST, NROW = L::NROW;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  float* rowv = reinterpret_cast<float*>(smem + L::kRowOff);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
+
+  const int tid = threadIdx.x;
+  const int warp = tid / 32, lane = tid % 32;
+  const int cta = blockIdx.x, grid = gridDim.x;
+
+  if (tid == 0) {
+    for (int i = 0; i < L::kNumBars; ++i) {
+      const uint32_t count = i == L::kOEmpty ? 4u
+                             : (i == L::kPFull || i == L::kDSFull ||
+                                (i >= L::kRowEmpty && i < L::kRowEmpty + NROW)) ? 8u
+                                                                               : 1u;
+      mbar_init(bars + i, count);
+    }
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    tma_prefetch_desc(&tm_do);
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp < 4) {
+    regs_dec<kRegsProducer>();
+    if (warp == 0) {
+      // ===================== Q and dO tiles =====================
+      if (lane == 0) {
+        const uint64_t keep = l2_policy_evict_last();
+        uint32_t g = 0;
+        bool ok = true;
+        for (int w = 0, it; ok && (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
+          if (it >= p.n_work) continue;
+          const KItem x = load_kitem(p, seqs, it);
+          for (int h = 0; ok && h < p.group; ++h)
+            for (int t = 0; ok && t < 2 * x.tiles; ++t, ++g) {
+              const int st = (int)(g % NST);
+              const uint32_t u = g / NST;
+              if (u >= 1) ok = mbar_wait(bars + L::kEmpty + st, (u - 1) & 1, abort_flag, p.status);
+              if (!ok) break;
+              const bool is_do = t & 1;
+              const int r = 128 * (t >> 1);
+              // a tile with rows past the sequence goes through warp 3 first
+              uint64_t* full = bars + (x.q_len - r < 128 ? L::kPre : L::kFull) + st;
+              uint8_t* dst = smem + L::kRingOff + st * L::kTile;
+              mbar_arrive_expect_tx(full, L::kTile);
+#pragma unroll
+              for (int dh = 0; dh < L::DH; ++dh)
+                load_rows(dst + dh * 16384, is_do ? &tm_do : &tm_q, is_do ? p.do_ax : p.q_ax, full, dh * 64,
+                          x.q0 + r, x.hk * p.group + h, 0, keep);
+            }
+        }
+        for (uint32_t t = (g > (uint32_t)NST ? g - NST : 0u); ok && t < g; ++t)
+          ok = mbar_wait(bars + L::kEmpty + (int)(t % NST), (t / NST) & 1, abort_flag, p.status);
+      }
+      __syncwarp();
+    } else if (warp == 2) {
+      // ===================== K and V tiles =====================
+      if (lane == 0) {
+        const uint64_t once = l2_policy_evict_first();
+        uint32_t n_item = 0;
+        bool ok = true;
+        for (int w = 0, it; ok && (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
+          if (it >= p.n_work) continue;
+          const KItem x = load_kitem(p, seqs, it);
+          if (x.n == 0) continue;
+          if (n_item >= 1) ok = mbar_wait(bars + L::kKVEmpty, (n_item - 1) & 1, abort_flag, p.status);
+          if (!ok) break;
+          ++n_item;
+          mbar_arrive_expect_tx(bars + L::kKVFull, 2 * L::kTile);
+#pragma unroll
+          for (int dh = 0; dh < L::DH; ++dh) {
+            load_rows(smem + L::kKOff + dh * 16384, &tm_k, p.k_ax, bars + L::kKVFull, dh * 64, x.key0, x.hk, 0, once);
+            load_rows(smem + L::kVOff + dh * 16384, &tm_v, p.v_ax, bars + L::kKVFull, dh * 64, x.key0, x.hk, 0, once);
+          }
+        }
+        if (ok && n_item >= 1) mbar_wait(bars + L::kKVEmpty, (n_item - 1) & 1, abort_flag, p.status);
+      }
+      __syncwarp();
+    } else if (warp == 3) {
+      // ============ -lse and delta rows; zero Q and dO rows past a sequence ============
+      uint32_t g = 0, pre = 0;  // query tiles so far; phase bit per ring stage
+      bool ok = true;
+      for (int w = 0, it; ok && (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
+        if (it >= p.n_work) continue;
+        const KItem x = load_kitem(p, seqs, it);
+        for (int h = 0; ok && h < p.group; ++h) {
+          const long long at = (x.hk * p.group + h) * p.lse_seq + x.q0;
+          for (int t = 0; ok && t < x.tiles; ++t, ++g) {
+            const int slot = (int)(g % NROW);
+            const int left = x.q_len - 128 * t;
+            float nl[4], de[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int r = 32 * e + lane;
+              const bool real = r < left;
+              nl[e] = real ? -kLog2 * p.lse[at + 128 * t + r] : -INFINITY;  // no row: p = 0
+              de[e] = real ? p.delta[at + 128 * t + r] : 0.f;
+            }
+            if (g >= (uint32_t)NROW &&
+                !warp_wait(bars + L::kRowEmpty + slot, (g / NROW - 1) & 1, abort_flag, p.status)) { ok = false; break; }
+            float* to = rowv + slot * 256;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              to[32 * e + lane] = nl[e];
+              to[128 + 32 * e + lane] = -de[e];
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars + L::kRowFull + slot);
+            if (left >= 128) continue;
+#pragma unroll 1
+            for (int s = 0; ok && s < 2; ++s) {
+              const int st = (int)((2 * g + s) % NST);
+              if (!warp_wait(bars + L::kPre + st, (pre >> st) & 1, abort_flag, p.status)) { ok = false; break; }
+              pre ^= 1u << st;
+              zero_rows<128>(smem + L::kRingOff + st * L::kTile, L::DH, left, (left + 15) & ~15, lane);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bars + L::kFull + st);
+            }
+          }
+        }
+      }
+    } else {
+      // ===================== MMA issue =====================
+      uint32_t g = 0, n_item = 0;  // query tiles, items so far
+      bool ok = true;
+      auto full = [&](uint32_t at) {
+        const bool r = warp_wait(bars + L::kFull + (int)(at % NST), (at / NST) & 1, abort_flag, p.status);
+        tc_fence_after_sync();
+        return r;
+      };
+      auto do_s = [&](uint32_t i) {
+        const uint32_t at = 2 * i;
+        if (!full(at)) { ok = false; return; }
+        if (elect_one()) {
+          issue_s<D>(tmem_base + kKS, sbase + L::kKOff, sbase + L::kRingOff + (at % NST) * L::kTile);
+          umma_commit(bars + L::kSFull);
+        }
+        __syncwarp();
+      };
+      for (int w = 0, it; ok && (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
+        if (it >= p.n_work) continue;
+        const KItem x = load_kitem(p, seqs, it);
+        if (x.n == 0) continue;
+        if (!warp_wait(bars + L::kKVFull, n_item & 1, abort_flag, p.status)) break;
+        do_s(g);
+        int t = 0;  // query tile of the head
+        for (int i = 0; ok && i < x.n; ++i, ++g) {
+          const int left = x.q_len - 128 * t;
+          const int steps = left >= 128 ? 8 : (left + 15) >> 4;
+          if (++t == x.tiles) t = 0;
+          const uint32_t st_q = (2 * g) % NST, st_do = (2 * g + 1) % NST;
+          if (!full(2 * g + 1)) { ok = false; break; }
+          if (elect_one()) {
+            issue_s<D>(tmem_base + kKDP, sbase + L::kVOff, sbase + L::kRingOff + st_do * L::kTile);
+            umma_commit(bars + L::kDPFull);
+            if (i == x.n - 1) umma_commit(bars + L::kKVEmpty);
+          }
+          __syncwarp();
+          // the epilogue has taken the previous item's dK and dV
+          if (i == 0 && n_item >= 1 &&
+              !warp_wait(bars + L::kOEmpty, (n_item - 1) & 1, abort_flag, p.status)) { ok = false; break; }
+          if (!warp_wait(bars + L::kPFull, g & 1, abort_flag, p.status)) { ok = false; break; }
+          tc_fence_after_sync();
+          if (elect_one()) {
+            issue_halves<D>(tmem_base + kKDV, tmem_base + kKS, sbase + L::kRingOff + st_do * L::kTile, steps, i > 0);
+            umma_commit(bars + L::kEmpty + (int)st_do);
+          }
+          __syncwarp();
+          if (i + 1 < x.n) do_s(g + 1);
+          if (!ok) break;
+          if (!warp_wait(bars + L::kDSFull, g & 1, abort_flag, p.status)) { ok = false; break; }
+          tc_fence_after_sync();
+          if (elect_one()) {
+            issue_halves<D>(tmem_base + kKDK, tmem_base + kKDP, sbase + L::kRingOff + st_q * L::kTile, steps, i > 0);
+            umma_commit(bars + L::kEmpty + (int)st_q);
+            if (i == x.n - 1) umma_commit(bars + L::kOFull);
+          }
+          __syncwarp();
+        }
+        ++n_item;
+      }
+    }
+  } else if (warp < 12) {
+    regs_inc<kRegsSoftmax>();
+    // ===================== p and ds: one thread per key and 64 query rows =====================
+    const int half = (warp - 4) >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t t_lane = tmem_base + (uint32_t((warp & 3) * 32) << 16) + 64u * half;
+    const uint64_t cc = pk2(p.scale_log2, p.scale_log2);
+    uint32_t g = 0;
+    bool ok = true;
+    for (int w = 0, it; ok && (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
+      if (it >= p.n_work) continue;
+      const KItem x = load_kitem(p, seqs, it);
+      int t = 0;
+      for (int i = 0; i < x.n; ++i, ++g) {
+        // rows of this half from `first` on see the key
+        const int first = p.causal ? row - x.diag - 128 * t - 64 * half : 0;
+        if (++t == x.tiles) t = 0;
+        const bool masked = __any_sync(0xffffffffu, first > 0);
+        const int slot = (int)(g % NROW);
+        const float* nl = rowv + slot * 256 + 64 * half;
+        if (!warp_wait(bars + L::kRowFull + slot, (g / NROW) & 1, abort_flag, p.status) ||
+            !warp_wait(bars + L::kSFull, g & 1, abort_flag, p.status)) { ok = false; break; }
+        tc_fence_after_sync();
+        uint32_t v[64];
+        tmem_ld64(t_lane + kKS, v);
+#pragma unroll
+        for (int q0 = 0; q0 < 32; q0 += 16) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int q1 = 0; q1 < 16; q1 += 2) {
+            const float4 l4 = *reinterpret_cast<const float4*>(nl + 2 * (q0 + q1));
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int q = q1 + u, e = 2 * (q0 + q);
+              float a, b;
+              upk2(ffma2(pk2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), cc,
+                         u ? pk2(l4.z, l4.w) : pk2(l4.x, l4.y)), a, b);
+              if ((q & 7) < DENSE_BWD_POLY8) {
+                upk2(exp2_fma2_t<true>(a, b), a, b);
+              } else {
+                a = fast_exp2(a);
+                b = fast_exp2(b);
+              }
+              if (masked) {
+                a = e >= first ? a : 0.f;
+                b = e + 1 >= first ? b : 0.f;
+              }
+              v[e] = __float_as_uint(a);
+              v[e + 1] = __float_as_uint(b);
+              pk[q] = pack_bf16x2(a, b);
+            }
+          }
+          VSA_TMEM_ST16(t_lane + kKS + q0, pk, 0);
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + L::kPFull);
+        if (!warp_wait(bars + L::kDPFull, g & 1, abort_flag, p.status)) { ok = false; break; }
+        tc_fence_after_sync();
+#pragma unroll
+        for (int q0 = 0; q0 < 32; q0 += 16) {
+          uint32_t dp[32], pk[16];
+          tmem_ld32(t_lane + kKDP + 2 * q0, dp);
+#pragma unroll
+          for (int q1 = 0; q1 < 16; q1 += 2) {
+            const float4 d4 = *reinterpret_cast<const float4*>(nl + 128 + 2 * (q0 + q1));
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int q = q1 + u, e = 2 * (q0 + q);
+              float a, b;
+              upk2(fadd2(pk2(__uint_as_float(dp[2 * q]), __uint_as_float(dp[2 * q + 1])),
+                         u ? pk2(d4.z, d4.w) : pk2(d4.x, d4.y)), a, b);
+              a *= __uint_as_float(v[e]);
+              b *= __uint_as_float(v[e + 1]);
+              if (masked) {
+                a = e >= first ? a : 0.f;
+                b = e + 1 >= first ? b : 0.f;
+              }
+              pk[q] = pack_bf16x2(a, b);
+            }
+          }
+          VSA_TMEM_ST16(t_lane + kKDP + q0, pk, 0);
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bars + L::kDSFull);
+          mbar_arrive(bars + L::kRowEmpty + slot);
+        }
+      }
+    }
+  } else {
+    regs_dec<kRegsEpilogue>();
+    // ===================== results: one thread per key =====================
+    const int row = (warp - 12) * 32 + lane;
+    const uint32_t t_lane = tmem_base + (uint32_t((warp - 12) * 32) << 16);
+    uint32_t n_item = 0;
+    for (int w = 0, it; (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
+      if (it >= p.n_work) continue;
+      const KItem x = load_kitem(p, seqs, it);
+      const bool real = row < x.keys;
+      __nv_bfloat16* tk = p.dk + x.hk * p.dk_st.h + (long long)(x.key0 + row) * p.dk_st.s;
+      __nv_bfloat16* tv = p.dv + x.hk * p.dv_st.h + (long long)(x.key0 + row) * p.dv_st.s;
+      if (x.n == 0) {
+        // keys that no row sees
+        if (real) {
+#pragma unroll
+          for (int e = 0; e < D; e += 8) {
+            *reinterpret_cast<uint4*>(tk + e) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(tv + e) = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        continue;
+      }
+      if (!warp_wait(bars + L::kOFull, n_item & 1, abort_flag, p.status)) break;
+      ++n_item;
+      tc_fence_after_sync();
+#pragma unroll 1
+      for (int q0 = 0; q0 < 2 * D; q0 += 32) {
+        const bool is_k = q0 >= D;
+        uint32_t ov[32];
+        tmem_ld32(t_lane + (is_k ? kKDK + q0 - D : kKDV + q0), ov);
+        if (q0 + 32 == 2 * D) {
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars + L::kOEmpty);
+        }
+        const float m = is_k ? p.scale : 1.f;
+        if (real) {
+          __nv_bfloat16* to = is_k ? tk + q0 - D : tv + q0;
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t o[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              o[q] = pack_bf16x2(__uint_as_float(ov[e + 2 * q]) * m, __uint_as_float(ov[e + 2 * q + 1]) * m);
+            *reinterpret_cast<uint4*>(to + e) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+      }
+    }
+  }
+
+  settle_after_abort(abort_flag);
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem_base, kTmemCols);
+  }
+}
+
+}  // namespace
+}  // namespace dense
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+template <int D>
+static int launch_dense_bwd_t(DenseBwdParams p, const CUtensorMap* m, const int4* seqs, int n,
+                              cudaStream_t stream) {
+  static KernelReady ready_q, ready_k;
+  auto kq = dense::dense_dq_kernel<D>;
+  auto kk = dense::dense_dkv_kernel<D>;
+  int rc = ready_q.check(reinterpret_cast<const void*>(kq), (int)dense::kLaunchRegs, (int)dense::QLayout<D>::kAlloc);
+  if (rc == VSA_OK)
+    rc = ready_k.check(reinterpret_cast<const void*>(kk), (int)dense::kLaunchRegs, (int)dense::KLayout<D>::kAlloc);
+  if (rc != VSA_OK) return rc;
+  const int sms = device_sm_count();
+  int units[kDenseMaxSeqs];
+  DenseSeqs table;
+  long long q_units = 0, k_units = 0;
+  for (int i = 0; i < n; ++i) {
+    q_units += (seqs[i].y + 127LL) / 128 * p.Hq;
+    k_units += (seqs[i].w + 127LL) / 128 * p.Hkv;
+  }
+  if (q_units >= (1 << 30) || k_units >= (1 << 30)) return VSA_ERR_UNSUPPORTED;  // 32-bit item index
+  if (q_units > 0) {
+    for (int i = 0; i < n; ++i) units[i] = (seqs[i].y + 127) / 128 * p.group;
+    fill_dense_seqs(&table, seqs, units, n);
+    p.n_work = table.n_items * p.Hkv;
+    kq<<<(unsigned)(p.n_work < sms ? p.n_work : sms), dense::kThreads, dense::QLayout<D>::kAlloc, stream>>>(
+        m[0], m[1], m[2], m[3], p, table);
+  }
+  if (k_units > 0) {
+    for (int i = 0; i < n; ++i) units[i] = (seqs[i].w + 127) / 128;
+    fill_dense_seqs(&table, seqs, units, n);
+    p.n_work = table.n_items * p.Hkv;
+    kk<<<(unsigned)(p.n_work < sms ? p.n_work : sms), dense::kThreads, dense::KLayout<D>::kAlloc, stream>>>(
+        m[0], m[1], m[2], m[3], p, table);
+  }
+  return cudaGetLastError() == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
+}
+
+int launch_dense_bwd(const DenseBwdParams& p_in, const DenseTensors& t, const void* dout, Strides3 do_st,
+                     const DenseBatch& b, int D, cudaStream_t stream) {
+  DenseBwdParams p = p_in;
+  // without rows or keys no tile is loaded; the maps only have to be valid
+  const bool rows = t.q_seq > 0, keys = t.kv_seq > 0;
+  const void* any = rows ? t.q : t.k;
+  const long long any_seq = rows ? t.q_seq : t.kv_seq;
+  const int any_h = rows ? p.Hq : p.Hkv;
+  const Strides3 any_st = rows ? t.q_st : t.k_st;
+  CUtensorMap m[4];
+  auto map = [&](CUtensorMap* to, TmaAxes* ax, bool have, const void* base, long long seq, int H, Strides3 st) {
+    return have ? make_view_map_rows(to, ax, base, D, seq, H, 1, st, 128)
+                : make_view_map_rows(to, ax, any, D, any_seq, any_h, 1, any_st, 128);
+  };
+  if (!map(&m[0], &p.q_ax, rows, t.q, t.q_seq, p.Hq, t.q_st) ||
+      !map(&m[1], &p.k_ax, keys, t.k, t.kv_seq, p.Hkv, t.k_st) ||
+      !map(&m[2], &p.v_ax, keys, t.v, t.kv_seq, p.Hkv, t.v_st) ||
+      !map(&m[3], &p.do_ax, rows, dout, t.q_seq, p.Hq, do_st))
+    return VSA_ERR_CUDA;
+  for (int i0 = 0; i0 < b.n; i0 += kDenseMaxSeqs) {
+    int4 seqs[kDenseMaxSeqs];
+    const int n = b.chunk(i0, seqs);
+    const int rc = D == 128 ? launch_dense_bwd_t<128>(p, m, seqs, n, stream)
+                            : launch_dense_bwd_t<64>(p, m, seqs, n, stream);
+    if (rc != VSA_OK) return rc;
+  }
+  return VSA_OK;
+}
+
+}  // namespace vsa

@@ -121,6 +121,63 @@ int dense_attn_varlen(const void* q, const void* k, const void* v, const vsa_den
   return launch_dense_fwd(p, t, b, D, static_cast<cudaStream_t>(stream));
 }
 
+size_t dense_attn_varlen_backward_workspace_size(int Hq, int64_t q_rows) {
+  if (Hq <= 0 || Hq > 65535 || q_rows < 0 || q_rows > kMaxRows) return 0;
+  return (size_t)Hq * (size_t)q_rows * sizeof(float);
+}
+
+int dense_attn_varlen_backward(const void* q, const void* k, const void* v, const void* out, const void* dout,
+                               const float* lse, const vsa_dense_layout* layout, const int32_t* cu_seqlens_q,
+                               const int32_t* cu_seqlens_kv, int n_seqs, int Hq, int Hkv, int D,
+                               int64_t q_rows, int64_t kv_rows, int causal, float scale, void* dq, void* dk,
+                               void* dv, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_dense(n_seqs, cu_seqlens_q, cu_seqlens_kv, Hq, Hkv, D, q_rows, kv_rows, scale);
+  if (rc != VSA_OK) return rc;
+  const bool rows = cu_seqlens_q[n_seqs] > 0, keys = cu_seqlens_kv[n_seqs] > 0;
+  if (!rows && !keys) return VSA_OK;
+  const void* per_row[] = {q, out, dout, dq};
+  const void* per_key[] = {k, v, dk, dv};
+  for (int i = 0; i < 4; ++i)
+    if ((rows && (!per_row[i] || !aligned16(per_row[i]))) || (keys && (!per_key[i] || !aligned16(per_key[i]))))
+      return VSA_ERR_INVALID_ARG;
+  if (rows && !lse) return VSA_ERR_INVALID_ARG;
+  vsa_dense_layout L;
+  if (layout) L = *layout;
+  else contiguous_layout(&L, q_rows, kv_rows, D);
+  if ((rows && (!view_ok(L.q, Hq, q_rows) || !view_ok(L.out, Hq, q_rows) || !view_ok(L.dout, Hq, q_rows) ||
+                !view_ok(L.dq, Hq, q_rows))) ||
+      (keys && (!view_ok(L.k, Hkv, kv_rows) || !view_ok(L.v, Hkv, kv_rows) || !view_ok(L.dk, Hkv, kv_rows) ||
+                !view_ok(L.dv, Hkv, kv_rows))))
+    return VSA_ERR_UNSUPPORTED;
+  if (rows && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+               workspace_bytes < dense_attn_varlen_backward_workspace_size(Hq, q_rows)))
+    return VSA_ERR_WORKSPACE;
+  DenseBwdParams p;
+  memset(&p, 0, sizeof(p));
+  p.out = static_cast<const __nv_bfloat16*>(out);
+  p.dq = static_cast<__nv_bfloat16*>(dq);
+  p.dk = static_cast<__nv_bfloat16*>(dk);
+  p.dv = static_cast<__nv_bfloat16*>(dv);
+  p.out_st = to3(L.out);
+  p.dq_st = to3(L.dq);
+  p.dk_st = to3(L.dk);
+  p.dv_st = to3(L.dv);
+  p.lse = lse;
+  p.delta = static_cast<float*>(workspace);
+  p.lse_seq = q_rows;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.group = Hq / Hkv;
+  p.causal = causal ? 1 : 0;
+  p.scale = resolve_scale(scale, D);
+  p.scale_log2 = p.scale * kLog2e;
+  p.status = device_status_ptr();
+  if (!p.status) return VSA_ERR_CUDA;
+  const DenseTensors t{q, k, v, to3(L.q), to3(L.k), to3(L.v), rows ? q_rows : 0, keys ? kv_rows : 0};
+  const DenseBatch b{cu_seqlens_q, cu_seqlens_kv, n_seqs};
+  return launch_dense_bwd(p, t, dout, to3(L.dout), b, D, static_cast<cudaStream_t>(stream));
+}
+
 size_t shared_prefix_attn_workspace_size(int B, int Hq, int Hkv, int T, int D, int64_t prefix_len,
                                          int64_t suffix_cap) {
   PrefixParams p;

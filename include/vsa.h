@@ -575,6 +575,38 @@ int dense_attn_varlen(const void* q, const void* k, const void* v, const vsa_den
                       int Hkv, int D, int64_t q_rows, int64_t kv_rows, int causal, float scale,
                       void* out, float* lse, void* stream);
 
+/* Workspace bytes dense_attn_varlen_backward needs: delta per query row and
+ * head (0 for invalid arguments, or without rows). */
+size_t dense_attn_varlen_backward_workspace_size(int Hq, int64_t q_rows);
+
+/*
+ * dense_attn_varlen_backward -- dq, dk, dv of dense_attn_varlen:
+ *   p = exp(scale q_r . k_j - lse(r)) where r sees j, delta = sum_d dout out,
+ *   ds = p (dout_r . v_j - delta(r)),  dq = scale ds k,
+ *   dk = scale sum over the group's heads of ds^T q,  dv likewise of p^T dout.
+ * Rows that see no key get dq = 0, keys that no row sees dk = dv = 0.  Sums
+ * are fp32 in a fixed order: the same call gives the same bits.  What the
+ * tensors hold past a sequence's rows never matters; a NaN or infinity in a
+ * sequence's own rows may reach any gradient of that sequence.
+ *
+ * q, k, v, cu_seqlens_*, n_seqs, heads, D, rows, causal, scale: as in the
+ *          forward call
+ * out      device bf16 [Hq, q_rows, D] view: that call's output
+ * dout     device bf16 [Hq, q_rows, D] view
+ * lse      device fp32 [Hq, q_rows]: that call's log-sum-exp
+ * layout   host (all eight members), or NULL for contiguous tensors
+ * dq       device bf16 [Hq, q_rows, D] view; dk, dv [Hkv, kv_rows, D] views;
+ *          rows past the last sequence are left as they were
+ * workspace  device, >= dense_attn_varlen_backward_workspace_size(Hq, q_rows),
+ *          256-aligned; no two calls in flight may share it
+ * Two launches on `stream` per 256 sequences.
+ */
+int dense_attn_varlen_backward(const void* q, const void* k, const void* v, const void* out, const void* dout,
+                               const float* lse, const vsa_dense_layout* layout, const int32_t* cu_seqlens_q,
+                               const int32_t* cu_seqlens_kv, int n_seqs, int Hq, int Hkv, int D,
+                               int64_t q_rows, int64_t kv_rows, int causal, float scale, void* dq, void* dk,
+                               void* dv, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ======================================================================== *
  * decoding over a shared prefix (ABI 2.2)
  * ======================================================================== */

@@ -94,3 +94,30 @@ def test_prefix_argument_checks():
 def test_prefix_without_rows_is_a_no_op():
     assert _prefix(b=0) == 0 and _prefix(t=0) == 0
     assert _lib().shared_prefix_attn_workspace_size(2, 5, 2, 1, 128, 100, 50) == 0
+
+
+def _backward(**kw):
+    a = dict(q=FAKE, k=FAKE, v=FAKE, out=FAKE, dout=FAKE, lse=FAKE, layout=None, cq=[0, 10], ck=[0, 10], n=1, hq=4,
+             hkv=2, d=128, qr=10, kr=10, causal=1, scale=0.0, dq=FAKE, dk=FAKE, dv=FAKE, ws=FAKE, bytes=1 << 20)
+    a.update(kw)
+    keep = [np.asarray(a[n], dtype=np.int32) for n in ("cq", "ck")]
+    ptr = [x.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)) for x in keep]
+    return _lib().dense_attn_varlen_backward(
+        *[_p(a[n]) for n in ("q", "k", "v", "out", "dout", "lse")], a["layout"], ptr[0], ptr[1], a["n"], a["hq"],
+        a["hkv"], a["d"], a["qr"], a["kr"], a["causal"], a["scale"], _p(a["dq"]), _p(a["dk"]), _p(a["dv"]),
+        _p(a["ws"]), a["bytes"], None)
+
+
+def test_backward_argument_checks():
+    from block_sparse_attention_15_b200 import binding as B
+    for n in ("q", "k", "v", "out", "dout", "dq", "dk", "dv"):
+        assert _backward(**{n: None}) == 1 and _backward(**{n: FAKE + 8}) == 1
+    assert _backward(lse=None) == 1 and _backward(n=0) == 2 and _backward(hq=5) == 2 and _backward(d=96) == 3
+    assert _backward(cq=[0, 11]) == 2 and _backward(ck=[3, 10]) == 2
+    assert _backward(ws=None) == 7 and _backward(ws=FAKE + 16) == 7 and _backward(bytes=159) == 7
+    assert _lib().dense_attn_varlen_backward_workspace_size(4, 10) == 160
+    good = dict(zip([n for n, _ in B.VsaDenseLayout._fields_], [(0, 1280, 128)] * 8))
+    for n in good:
+        lay = B.VsaDenseLayout(*[B.VsaStrides(*(good | {n: (0, 1280, 132)})[m]) for m in good])
+        assert _backward(layout=ctypes.byref(lay)) == 3
+    assert _backward(cq=[0, 0], ck=[0, 0], q=None, dk=None, lse=None, ws=None) == 0
