@@ -44,6 +44,42 @@ __device__ __forceinline__ int wave_item(int w, int c, int g) {
   return w * g + ((w & 1) ? g - 1 - c : c);
 }
 
+// Work items of a CTA: one warp finds them (searches and divisions of a few
+// hundred cycles) and hands them to the others through a ring in shared memory.
+constexpr int kItemSlots = 4;
+template <typename Item>
+struct alignas(16) ItemRing {
+  Item item[kItemSlots];
+};
+
+// The finder's side, whole warp: the w-th item, or the end mark (n < 0).
+template <typename Item>
+__device__ __forceinline__ bool put_item(ItemRing<Item>* ring, uint64_t* full, uint64_t* empty, uint32_t w,
+                                         const Item& x, int lane, volatile int* abort_flag, int* status) {
+  const int slot = (int)(w % kItemSlots);
+  if (w >= (uint32_t)kItemSlots && !warp_wait(empty + slot, (w / kItemSlots - 1) & 1, abort_flag, status))
+    return false;
+  if (lane == 0) {
+    ring->item[slot] = x;
+    mbar_arrive(full + slot);
+  }
+  __syncwarp();
+  return true;
+}
+
+// The other warps' side: false at the end.
+template <typename Item>
+__device__ __forceinline__ bool get_item(const ItemRing<Item>* ring, uint64_t* full, uint64_t* empty, uint32_t& w,
+                                         Item& x, int lane, volatile int* abort_flag, int* status) {
+  const int slot = (int)(w % kItemSlots);
+  if (!warp_wait(full + slot, (w / kItemSlots) & 1, abort_flag, status)) return false;
+  x = ring->item[slot];
+  __syncwarp();
+  if (lane == 0) mbar_arrive(empty + slot);
+  ++w;
+  return x.n >= 0;
+}
+
 // 64 head dims x box rows of a [H, S, D] view through its tile map.
 __device__ __forceinline__ void load_rows(void* dst, const CUtensorMap* map, TmaAxes ax,
                                           uint64_t* bar, int d0, int s, int h, int b,

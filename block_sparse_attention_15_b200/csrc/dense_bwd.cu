@@ -39,6 +39,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "dense_attn.cuh"
 #include "dense_launch.h"
 #include "vsa.h"
@@ -49,7 +51,7 @@ namespace dense {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr uint32_t kRegsProducer = 80, kRegsSoftmax = 184, kRegsEpilogue = 64;
+constexpr uint32_t kRegsProducer = 104, kRegsSoftmax = 168, kRegsEpilogue = 72;
 constexpr uint32_t kLaunchRegs = 128;  // 512 x 128 = 65536
 static_assert(128u * (kRegsProducer + 2u * kRegsSoftmax + kRegsEpilogue) <= 512u * kLaunchRegs,
               "register split exceeds the launch's registers");
@@ -94,33 +96,38 @@ __device__ __forceinline__ void issue_halves(uint32_t tmem_d, uint32_t tmem_a, u
   }
 }
 
+// 16 TMEM lanes x 64 fp32 columns: register 4 i + 2 b + e holds lane
+// threadIdx / 4 + 8 b, column 8 i + 2 (threadIdx % 4) + e.
+template <int N>
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, uint32_t (&r)[N], int o) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[o + 0]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]),
+        "=r"(r[o + 6]), "=r"(r[o + 7]), "=r"(r[o + 8]), "=r"(r[o + 9]), "=r"(r[o + 10]), "=r"(r[o + 11]),
+        "=r"(r[o + 12]), "=r"(r[o + 13]), "=r"(r[o + 14]), "=r"(r[o + 15]), "=r"(r[o + 16]), "=r"(r[o + 17]),
+        "=r"(r[o + 18]), "=r"(r[o + 19]), "=r"(r[o + 20]), "=r"(r[o + 21]), "=r"(r[o + 22]), "=r"(r[o + 23]),
+        "=r"(r[o + 24]), "=r"(r[o + 25]), "=r"(r[o + 26]), "=r"(r[o + 27]), "=r"(r[o + 28]), "=r"(r[o + 29]),
+        "=r"(r[o + 30]), "=r"(r[o + 31])
+      : "r"(taddr));
+}
+
+// 16 TMEM lanes x 32 columns of 32 bits: register 2 i + b holds lane
+// threadIdx / 4 + 8 b, column 4 i + threadIdx % 4.
+__device__ __forceinline__ void tmem_st_16x128(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+      "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+      "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
 // ---------------------------------------------------------------------------
 // dq
 // ---------------------------------------------------------------------------
-template <int D>
-struct QLayout {
-  static constexpr int DH = D / 64;
-  static constexpr uint32_t kTile = 128u * D * 2u;
-  static constexpr int NST = D == 128 ? 6 : 10;  // ring: Q, dO, K(0), V(0), K(1), ...
-  static constexpr uint32_t kRingOff = 0;
-  static constexpr uint32_t kRowOff = kRingOff + NST * kTile;  // [2][2][128] f32: -lse, delta
-  static constexpr uint32_t kBarOff = kRowOff + 2048u;
-  // Q and dO of an item signal a barrier of the item's, K and V tiles their
-  // stage's.  Four of the former: the ring holds the Q and dO of fewer than
-  // four items ahead of the one whose operands are being copied.
-  static constexpr int NOP = 4;
-  static_assert(NST <= 4 * (NOP - 1), "an item takes four stages or more");
-  static constexpr int kFull = 0, kEmpty = NST, kPre = 2 * NST, kOpFull = 3 * NST,
-                       kOpReady = kOpFull + NOP, kOpFree = kOpReady + 2, kSFull = kOpFree + 1, kSFree = kSFull + 1,
-                       kDPFull = kSFree + 1, kDSFull = kDPFull + 1, kOFull = kDSFull + 1,
-                       kOEmpty = kOFull + 1, kNumBars = kOEmpty + 1;
-  static constexpr uint32_t kMiscOff = kBarOff + 8u * kNumBars;
-  static constexpr uint32_t kAlloc = kMiscOff + 16u + 1024u;
-  static_assert(kAlloc <= 227u * 1024u, "shared memory");
-};
-// TMEM columns
-constexpr uint32_t kQS = 0, kQDP = 128, kQDQ = 256, kQQ = 384, kQDO = 448;
-
 struct QItem {
   int head, hk;
   int row0, rows;  // rows of q
@@ -129,6 +136,34 @@ struct QItem {
   int last;        // keys that the last real row sees
   int n;           // key tiles
 };
+
+template <int D>
+struct QLayout {
+  static constexpr int DH = D / 64;
+  static constexpr uint32_t kTile = 128u * D * 2u;
+  static constexpr int NST = D == 128 ? 6 : 10;  // ring: Q, dO, out, K(0), V(0), K(1), ...
+  static constexpr uint32_t kRingOff = 0;
+  static constexpr uint32_t kRowOff = kRingOff + NST * kTile;  // [2][2][128] f32: -lse, delta
+  static constexpr uint32_t kItemOff = kRowOff + 2048u;
+  static constexpr uint32_t kBarOff = kItemOff + (uint32_t)sizeof(ItemRing<QItem>);
+  // Q, and dO with out, signal barriers of their item's, K and V tiles their
+  // stage's.  Four of the former: the ring holds those of fewer than four items
+  // ahead of the one whose operands are being copied.
+  static constexpr int NOP = 4;
+  static_assert(NST <= 5 * (NOP - 1), "an item takes five stages or more");
+  static constexpr int kFull = 0, kEmpty = NST, kPre = 2 * NST, kQFull = 3 * NST,
+                       kGFull = kQFull + NOP, kQReady = kGFull + NOP, kGReady = kQReady + 2,
+                       kDReady = kGReady + 1, kQFree = kDReady + 2, kGFree = kQFree + 1,
+                       kSFull = kGFree + 1, kSFree = kSFull + 1,
+                       kDPFull = kSFree + 1, kDSFull = kDPFull + 1, kOFull = kDSFull + 1,
+                       kOEmpty = kOFull + 1, kItFull = kOEmpty + 1, kItEmpty = kItFull + kItemSlots,
+                       kNumBars = kItEmpty + kItemSlots;
+  static constexpr uint32_t kMiscOff = kBarOff + 8u * kNumBars;
+  static constexpr uint32_t kAlloc = kMiscOff + 16u + 1024u;
+  static_assert(kAlloc <= 227u * 1024u, "shared memory");
+};
+// TMEM columns
+constexpr uint32_t kQS = 0, kQDP = 128, kQDQ = 256, kQQ = 384, kQDO = 448;
 
 __device__ __forceinline__ QItem load_qitem(const DenseBwdParams& p, const DenseSeqs& t, int w) {
   QItem x;
@@ -151,7 +186,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
-                    const __grid_constant__ DenseBwdParams p, const __grid_constant__ DenseSeqs seqs) {
+                    const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ DenseBwdParams p, const __grid_constant__ DenseSeqs seqs) {
   using L = QLayout<D>;
   constexpr int NST = L::NST;
   extern __shared__ uint8_t smem_raw[];
@@ -159,6 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   float* rowv = reinterpret_cast<float*>(smem + L::kRowOff);
+  ItemRing<QItem>* items = reinterpret_cast<ItemRing<QItem>*>(smem + L::kItemOff);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
@@ -171,9 +207,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < L::kNumBars; ++i) {
       // a TMA transaction, a commit or one thread's arrival, except where the
       // epilogue's four or the softmax's eight warps arrive
-      const uint32_t count = (i == L::kOpReady || i == L::kOpReady + 1 || i == L::kOEmpty) ? 4u
-                             : (i == L::kSFree || i == L::kDSFull)                          ? 8u
-                                                                                            : 1u;
+      const uint32_t count = ((i >= L::kQReady && i < L::kQFree) || i == L::kOEmpty) ? 4u
+                             : (i == L::kSFree || i == L::kDSFull)                    ? 8u
+                             : (i >= L::kItEmpty)                                     ? 15u  // all warps but one
+                                                                                      : 1u;
       mbar_init(bars + i, count);
     }
     *abort_flag = 0;
@@ -190,57 +227,76 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
+  auto next = [&](uint32_t& w, QItem& x) {
+    return get_item(items, bars + L::kItFull, bars + L::kItEmpty, w, x, lane, abort_flag, p.status);
+  };
 
   if (warp < 4) {
     regs_dec<kRegsProducer>();
     if (warp == 0) {
       // ===================== tile loads =====================
-      if (lane == 0) {
-        const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
-        uint32_t g = 0, n_item = 0;
-        bool ok = true;
-        for (int w = 0, it; ok && (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
-          if (it >= p.n_work) continue;
-          const QItem x = load_qitem(p, seqs, it);
-          if (x.n == 0) continue;
-          for (int j = 0; ok && j < 2 * x.n + 2; ++j, ++g) {
+      const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
+      uint32_t g = 0, n_item = 0;
+      bool ok = true;
+      QItem x;
+      while (ok && next(n_item, x)) {
+        if (lane == 0) {
+          for (int j = -3; ok && j < 2 * x.n; ++j, ++g) {
             const int st = (int)(g % NST);
             const uint32_t u = g / NST;
             if (u >= 1) ok = mbar_wait(bars + L::kEmpty + st, (u - 1) & 1, abort_flag, p.status);
             if (!ok) break;
             uint8_t* dst = smem + L::kRingOff + st * L::kTile;
-            const int key = 128 * ((j >> 1) - 1);
-            const bool second = j & 1;
+            const int key = 128 * (j >> 1);
+            const bool is_v = j & 1;
             // a K tile with rows past the sequence goes through warp 2 first
-            uint64_t* full = bars + (j < 2 ? L::kOpFull + (int)(n_item % L::NOP)
-                                           : (!second && x.kv_len - key < 128 ? L::kPre : L::kFull) + st);
-            if (j != 1) mbar_arrive_expect_tx(full, j == 0 ? 2 * L::kTile : L::kTile);
+            uint64_t* full = bars + (j < 0 ? (j == -3 ? L::kQFull : L::kGFull) + (int)((n_item - 1) % L::NOP)
+                                           : (!is_v && x.kv_len - key < 128 ? L::kPre : L::kFull) + st);
+            if (j != -1) mbar_arrive_expect_tx(full, j == -2 ? 2 * L::kTile : L::kTile);
 #pragma unroll
             for (int dh = 0; dh < L::DH; ++dh) {
               uint8_t* to = dst + dh * 16384;
-              if (j < 2)
-                load_rows(to, second ? &tm_do : &tm_q, second ? p.do_ax : p.q_ax, full, dh * 64, x.row0,
-                          x.head, 0, once);
+              if (j < 0)
+                load_rows(to, j == -3 ? &tm_q : j == -2 ? &tm_do : &tm_o,
+                          j == -3 ? p.q_ax : j == -2 ? p.do_ax : p.o_ax, full, dh * 64, x.row0, x.head, 0, once);
               else
-                load_rows(to, second ? &tm_v : &tm_k, second ? p.v_ax : p.k_ax, full, dh * 64, x.kv0 + key,
-                          x.hk, 0, keep);
+                load_rows(to, is_v ? &tm_v : &tm_k, is_v ? p.v_ax : p.k_ax, full, dh * 64, x.kv0 + key, x.hk, 0, keep);
             }
           }
-          ++n_item;
         }
-        // every stage's release lands before exit
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      }
+      // every stage's release lands before exit
+      if (lane == 0)
         for (uint32_t t = (g > (uint32_t)NST ? g - NST : 0u); ok && t < g; ++t)
           ok = mbar_wait(bars + L::kEmpty + (int)(t % NST), (t / NST) & 1, abort_flag, p.status);
-      }
       __syncwarp();
+    } else if (warp == 3) {
+      // ===================== work items; rows that see no key =====================
+      uint32_t n_item = 0;
+      bool ok = true;
+      QItem x;
+      for (int w = 0, it; ok && (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
+        if (it >= p.n_work) continue;
+        x = load_qitem(p, seqs, it);
+        if (x.n > 0) {
+          ok = put_item(items, bars + L::kItFull, bars + L::kItEmpty, n_item++, x, lane, abort_flag, p.status);
+          continue;
+        }
+        for (int r = lane; r < x.rows; r += 32) {
+          __nv_bfloat16* to = p.dq + x.head * p.dq_st.h + (long long)(x.row0 + r) * p.dq_st.s;
+          for (int e = 0; e < D; e += 8) *reinterpret_cast<uint4*>(to + e) = make_uint4(0u, 0u, 0u, 0u);
+          p.delta[x.head * p.lse_seq + x.row0 + r] = 0.f;
+        }
+      }
+      x.n = -1;
+      if (ok) put_item(items, bars + L::kItFull, bars + L::kItEmpty, n_item, x, lane, abort_flag, p.status);
     } else if (warp == 2) {
       // ===================== zero K rows past a sequence's keys (0 * inf is not 0) =====================
-      uint32_t g = 0, pre = 0;
-      for (int w = 0, it; (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
-        if (it >= p.n_work) continue;
-        const QItem x = load_qitem(p, seqs, it);
-        if (x.n == 0) continue;
-        g += 2 * x.n + 2;
+      uint32_t g = 0, pre = 0, n_item = 0;
+      QItem x;
+      while (next(n_item, x)) {
+        g += 2 * x.n + 3;
         const int len = x.kv_len - 128 * (x.n - 1);
         if (len >= 128) continue;
         const int st = (int)((g - 2) % NST);
@@ -254,12 +310,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 1) {
       // ===================== MMA issue =====================
-      uint32_t g = 0;            // ring tiles before the current item
-      uint32_t n_item = 0;       // items so far
-      uint32_t ts = 0, tq = 0;   // S and dQ products so far
-      uint32_t phase = 0;        // phase bit per ring stage
+      uint32_t ts = 0, tq = 0;     // S and dQ products so far
+      uint32_t n_s = 0, n_dp = 0;  // items whose first S, first dP was issued
+      uint32_t phase = 0;          // phase bit per ring stage
       bool ok = true;
-      QItem x = {};
       auto full = [&](uint32_t at) {
         const int st = (int)(at % NST);
         const bool r = warp_wait(bars + L::kFull + st, (phase >> st) & 1, abort_flag, p.status);
@@ -267,17 +321,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after_sync();
         return r;
       };
-      auto do_s = [&](int j) {
+      auto release = [&](uint32_t at) { mbar_arrive(bars + L::kEmpty + (int)(at % NST)); };
+      // S(j) and dP(j) of item x, whose ring tiles start at g
+      auto do_s = [&](const QItem& x, int j, uint32_t g) {
         if (j == 0) {
-          // Q and dO are in TMEM; their ring stages are free again
-          if (!warp_wait(bars + L::kOpReady + (n_item & 1), (n_item >> 1) & 1, abort_flag, p.status)) { ok = false; return; }
-          if (elect_one()) {
-            mbar_arrive(bars + L::kEmpty + (int)(g % NST));
-            mbar_arrive(bars + L::kEmpty + (int)((g + 1) % NST));
-          }
+          // Q is in TMEM, its ring stage free again
+          if (!warp_wait(bars + L::kQReady + (n_s & 1), (n_s >> 1) & 1, abort_flag, p.status)) { ok = false; return; }
+          ++n_s;
+          if (elect_one()) release(g);
           __syncwarp();
         }
-        const uint32_t at = g + 2 + 2 * j;
+        const uint32_t at = g + 3 + 2 * j;
         if (!full(at)) { ok = false; return; }
         if (ts >= 1 && !warp_wait(bars + L::kSFree, (ts - 1) & 1, abort_flag, p.status)) { ok = false; return; }
         ++ts;
@@ -285,28 +339,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
           issue_ta<D>(tmem_base + kQS, tmem_base + kQQ, sbase + L::kRingOff + (at % NST) * L::kTile);
           umma_commit(bars + L::kSFull);
+          if (j == x.n - 1) umma_commit(bars + L::kQFree);
         }
         __syncwarp();
       };
-      auto do_dp = [&](int j) {
-        const uint32_t at = g + 3 + 2 * j;
+      auto do_dp = [&](const QItem& x, int j, uint32_t g) {
+        if (j == 0) {
+          if (!warp_wait(bars + L::kGReady, n_dp & 1, abort_flag, p.status)) { ok = false; return; }
+          ++n_dp;
+        }
+        const uint32_t at = g + 4 + 2 * j;
         if (!full(at)) { ok = false; return; }
         if (elect_one()) {
           issue_ta<D>(tmem_base + kQDP, tmem_base + kQDO, sbase + L::kRingOff + (at % NST) * L::kTile);
           umma_commit(bars + L::kDPFull);
           umma_commit(bars + L::kEmpty + (int)(at % NST));
-          if (j == x.n - 1) umma_commit(bars + L::kOpFree);
+          if (j == x.n - 1) umma_commit(bars + L::kGFree);
         }
         __syncwarp();
       };
-      for (int w = 0, it; ok && (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
-        if (it >= p.n_work) continue;
-        x = load_qitem(p, seqs, it);
-        if (x.n == 0) continue;
-        do_s(0);
-        if (ok) do_dp(0);
+      uint32_t g = 0, n_got = 0, n_item = 0;
+      QItem x, y;
+      bool have = next(n_got, x);
+      if (have) do_s(x, 0, g);
+      if (ok && have) do_dp(x, 0, g);
+      while (ok && have) {
+        const bool more = next(n_got, y);
+        const uint32_t g_next = g + 2 * x.n + 3;
+        // delta is formed: dO and out are read.  Released here, before the next
+        // item's first S: with one key tile the ring cannot take that item's K
+        // until then.
+        if (!warp_wait(bars + L::kDReady + (n_item & 1), (n_item >> 1) & 1, abort_flag, p.status)) break;
+        if (elect_one()) {
+          release(g + 1);
+          release(g + 2);
+        }
+        __syncwarp();
         for (int j = 0; ok && j < x.n; ++j) {
-          if (j + 1 < x.n) do_s(j + 1);
+          if (j + 1 < x.n) do_s(x, j + 1, g);
+          else if (more) do_s(y, 0, g_next);
           if (!ok) break;
           // the epilogue has taken the previous item's dQ
           if (j == 0 && n_item >= 1 &&
@@ -315,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++tq;
           tc_fence_after_sync();
           if (elect_one()) {
-            const uint32_t st = (g + 2 + 2 * j) % NST;
+            const uint32_t st = (g + 3 + 2 * j) % NST;
             const int keys = x.last - 128 * j;
             issue_halves<D>(tmem_base + kQDQ, tmem_base + kQDP, sbase + L::kRingOff + st * L::kTile,
                             keys >= 128 ? 8 : (keys + 15) >> 4, j > 0);
@@ -323,9 +394,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (j == x.n - 1) umma_commit(bars + L::kOFull);
           }
           __syncwarp();
-          if (j + 1 < x.n) do_dp(j + 1);
+          if (j + 1 < x.n) do_dp(x, j + 1, g);
+          else if (more) do_dp(y, 0, g_next);
         }
-        g += 2 * x.n + 2;
+        g = g_next;
+        x = y;
+        have = more;
         ++n_item;
       }
     }
@@ -336,16 +410,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = (warp & 3) * 32 + lane;
     const uint32_t t_lane = tmem_base + (uint32_t((warp & 3) * 32) << 16) + 64u * half;
     const uint64_t cc = pk2(p.scale_log2, p.scale_log2);
-    uint32_t g = 0, n_item = 0;
+    uint32_t g = 0, n_item = 0, n_got = 0;
     bool ok = true;
-    for (int w = 0, it; ok && (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
-      if (it >= p.n_work) continue;
-      const QItem x = load_qitem(p, seqs, it);
-      if (x.n == 0) continue;
-      if (!warp_wait(bars + L::kOpReady + (n_item & 1), (n_item >> 1) & 1, abort_flag, p.status)) break;
-      const float nl = rowv[(n_item & 1) * 256 + row], nd = -rowv[(n_item & 1) * 256 + 128 + row];
-      const uint64_t nl2 = pk2(nl, nl), nd2 = pk2(nd, nd);
-      ++n_item;
+    QItem x;
+    while (ok && next(n_got, x)) {
+      if (!warp_wait(bars + L::kQReady + (n_item & 1), (n_item >> 1) & 1, abort_flag, p.status)) break;
+      const float nl = rowv[(n_item & 1) * 256 + row];
+      const uint64_t nl2 = pk2(nl, nl);
+      uint64_t nd2 = 0;
       const int limit = p.causal ? min(x.lim0 + row, x.kv_len) : x.kv_len;  // keys this row sees
       for (int j = 0; j < x.n; ++j, ++g) {
         if (!warp_wait(bars + L::kSFull, g & 1, abort_flag, p.status)) { ok = false; break; }
@@ -355,12 +427,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + L::kSFree);
+        const int rem = limit - 128 * j - 64 * half;
+        const bool masked = __any_sync(0xffffffffu, rem < 64);
+        auto probs = [&](auto mask) {
+          constexpr bool kMask = decltype(mask)::value;
+          if (kMask) {
+#pragma unroll
+            for (int e = 0; e < 64; ++e)
+              if (e >= rem) v[e] = __float_as_uint(-INFINITY);
+          }
 #pragma unroll
         for (int q = 0; q < 32; ++q) {
           const uint64_t e = ffma2(pk2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1])), cc, nl2);
           float a, b;
           upk2(e, a, b);
-          if ((q & 7) < DENSE_BWD_POLY8) {
+          if (!kMask && (q & 7) < DENSE_BWD_POLY8) {
             upk2(exp2_fma2_t<true>(a, b), a, b);
           } else {
             a = fast_exp2(a);
@@ -369,26 +450,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           v[2 * q] = __float_as_uint(a);
           v[2 * q + 1] = __float_as_uint(b);
         }
+        };
+        if (masked) probs(std::true_type{});
+        else probs(std::false_type{});
+        if (j == 0) {
+          if (!warp_wait(bars + L::kDReady + (n_item & 1), (n_item >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
+          const float nd = -rowv[(n_item & 1) * 256 + 128 + row];
+          nd2 = pk2(nd, nd);
+        }
         if (!warp_wait(bars + L::kDPFull, g & 1, abort_flag, p.status)) { ok = false; break; }
         tc_fence_after_sync();
-        const int rem = limit - 128 * j - 64 * half;
-        const bool masked = __any_sync(0xffffffffu, rem < 64);
 #pragma unroll
         for (int q0 = 0; q0 < 32; q0 += 16) {
-          uint32_t dp[32], pk[16];
+          uint32_t dp[32];
           tmem_ld32(t_lane + kQDP + 2 * q0, dp);
+          if (masked) {
+            // p = 0 there, but dP may be infinite
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (2 * q0 + e >= rem) dp[e] = 0u;
+          }
+          uint32_t pk[16];
 #pragma unroll
           for (int q = 0; q < 16; ++q) {
             const int e = 2 * (q0 + q);
             float a, b;
             upk2(fadd2(pk2(__uint_as_float(dp[2 * q]), __uint_as_float(dp[2 * q + 1])), nd2), a, b);
-            a *= __uint_as_float(v[e]);
-            b *= __uint_as_float(v[e + 1]);
-            if (masked) {
-              a = e < rem ? a : 0.f;
-              b = e + 1 < rem ? b : 0.f;
-            }
-            pk[q] = pack_bf16x2(a, b);
+            pk[q] = pack_bf16x2(a * __uint_as_float(v[e]), b * __uint_as_float(v[e + 1]));
           }
           // the first 32 words lie over columns that this thread has read
           VSA_TMEM_ST16(t_lane + kQDP + q0, pk, 0);
@@ -398,6 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + L::kDSFull);
       }
+      ++n_item;
     }
   } else {
     regs_dec<kRegsEpilogue>();
@@ -434,72 +523,69 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return true;
     };
-    for (int w = 0, it; ok && (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
-      if (it >= p.n_work) continue;
-      const QItem x = load_qitem(p, seqs, it);
+    uint32_t n_got = 0;
+    QItem x;
+    while (ok && next(n_got, x)) {
       const bool real = row < x.rows;
-      if (x.n == 0) {
-        // rows that see no key
-        if (real) {
-          __nv_bfloat16* to = p.dq + x.head * p.dq_st.h + (long long)(x.row0 + row) * p.dq_st.s;
-#pragma unroll
-          for (int e = 0; e < D; e += 8) *reinterpret_cast<uint4*>(to + e) = make_uint4(0u, 0u, 0u, 0u);
-          p.delta[x.head * p.lse_seq + x.row0 + row] = 0.f;
-        }
-        continue;
-      }
-      const uint32_t sq = g % NST, sd = (g + 1) % NST;
-      if (!warp_wait(bars + L::kOpFull + (int)(n_item % L::NOP), (n_item / L::NOP) & 1, abort_flag, p.status)) break;
+      const float lse = real ? p.lse[x.head * p.lse_seq + x.row0 + row] : 0.f;
+      const uint32_t sq = g % NST, sd = (g + 1) % NST, so = (g + 2) % NST;
       const uint8_t* qt = smem + L::kRingOff + sq * L::kTile;
       const uint8_t* dt = smem + L::kRingOff + sd * L::kTile;
-      // delta, from the dO tile and the out row
-      float delta = 0.f, lse = 0.f;
-      if (real) {
-        const __nv_bfloat16* orow = p.out + x.head * p.out_st.h + (long long)(x.row0 + row) * p.out_st.s;
-        lse = p.lse[x.head * p.lse_seq + x.row0 + row];
-#pragma unroll 4
-        for (int ch = 0; ch < D / 8; ++ch) {
-          const uint4 o4 = *reinterpret_cast<const uint4*>(orow + 8 * ch);
-          const uint4 d4 = *reinterpret_cast<const uint4*>(dt + (ch >> 3) * 16384 + sw128(row, ch & 7));
-          const __nv_bfloat162* o2 = reinterpret_cast<const __nv_bfloat162*>(&o4);
-          const __nv_bfloat162* d2 = reinterpret_cast<const __nv_bfloat162*>(&d4);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 a = __bfloat1622float2(o2[e]), c = __bfloat1622float2(d2[e]);
-            delta = fmaf(a.x, c.x, delta);
-            delta = fmaf(a.y, c.y, delta);
-          }
-        }
-        if (lse == -INFINITY) lse = delta = 0.f;  // a row that sees no key: all of it is masked
-        p.delta[x.head * p.lse_seq + x.row0 + row] = delta;
-      }
-      rowv[(n_item & 1) * 256 + row] = -lse * kLog2;
-      rowv[(n_item & 1) * 256 + 128 + row] = delta;
-      // the previous item's last product with Q and dO is complete
-      if (n_item >= 1 && !warp_wait(bars + L::kOpFree, (n_item - 1) & 1, abort_flag, p.status)) break;
-      tc_fence_after_sync();
+      const uint8_t* ot = smem + L::kRingOff + so * L::kTile;
+      const bool sees = lse != -INFINITY;  // else all of the row is masked
+      rowv[(n_item & 1) * 256 + row] = sees ? -lse * kLog2 : 0.f;
+      // this thread's row of a tile -> bf16 A operand in TMEM
+      auto copy_row = [&](const uint8_t* tile, uint32_t col) {
 #pragma unroll 1
-      for (int c0 = 0; c0 < D / 8; c0 += 4) {
-        uint32_t a[16], b[16];
+        for (int c0 = 0; c0 < D / 8; c0 += 8) {
+          uint32_t a[32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int ch = c0 + c;
-          const uint32_t off = (ch >> 3) * 16384 + sw128(row, ch & 7);
-          const uint4 x4 = *reinterpret_cast<const uint4*>(qt + off);
-          const uint4 y4 = *reinterpret_cast<const uint4*>(dt + off);
-          a[4 * c] = x4.x, a[4 * c + 1] = x4.y, a[4 * c + 2] = x4.z, a[4 * c + 3] = x4.w;
-          b[4 * c] = y4.x, b[4 * c + 1] = y4.y, b[4 * c + 2] = y4.z, b[4 * c + 3] = y4.w;
+          for (int c = 0; c < 8; ++c) {
+            const uint4 x4 = *reinterpret_cast<const uint4*>(tile + (c0 >> 3) * 16384 + sw128(row, c));
+            a[4 * c] = x4.x, a[4 * c + 1] = x4.y, a[4 * c + 2] = x4.z, a[4 * c + 3] = x4.w;
+          }
+          VSA_TMEM_ST16(t_lane + col + 4 * c0, a, 0);
+          VSA_TMEM_ST16(t_lane + col + 4 * c0 + 16, a, 16);
         }
-        VSA_TMEM_ST16(t_lane + kQQ + 4 * c0, a, 0);
-        VSA_TMEM_ST16(t_lane + kQDO + 4 * c0, b, 0);
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before_sync();
+        __syncwarp();
+      };
+      // Q, once the previous item's last S is complete
+      if (!warp_wait(bars + L::kQFull + (int)(n_item % L::NOP), (n_item / L::NOP) & 1, abort_flag, p.status) ||
+          (n_item >= 1 && !warp_wait(bars + L::kQFree, (n_item - 1) & 1, abort_flag, p.status))) break;
+      tc_fence_after_sync();
+      copy_row(qt, kQQ);
+      if (lane == 0) mbar_arrive(bars + L::kQReady + (n_item & 1));
+      // dO, once its last dP is
+      if (!warp_wait(bars + L::kGFull + (int)(n_item % L::NOP), (n_item / L::NOP) & 1, abort_flag, p.status) ||
+          (n_item >= 1 && !warp_wait(bars + L::kGFree, (n_item - 1) & 1, abort_flag, p.status))) break;
+      tc_fence_after_sync();
+      copy_row(dt, kQDO);
+      if (lane == 0) mbar_arrive(bars + L::kGReady);
+      float delta = 0.f;
+#pragma unroll 4
+      for (int ch = 0; ch < D / 8; ++ch) {
+        const uint32_t off = (ch >> 3) * 16384 + sw128(row, ch & 7);
+        const uint4 o4 = *reinterpret_cast<const uint4*>(ot + off);
+        const uint4 d4 = *reinterpret_cast<const uint4*>(dt + off);
+        const __nv_bfloat162* o2 = reinterpret_cast<const __nv_bfloat162*>(&o4);
+        const __nv_bfloat162* d2 = reinterpret_cast<const __nv_bfloat162*>(&d4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 a = __bfloat1622float2(o2[e]), c = __bfloat1622float2(d2[e]);
+          delta = fmaf(a.x, c.x, delta);
+          delta = fmaf(a.y, c.y, delta);
+        }
       }
-      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-      tc_fence_before_sync();
+      if (!sees) delta = 0.f;
+      rowv[(n_item & 1) * 256 + 128 + row] = delta;
+      if (real) p.delta[x.head * p.lse_seq + x.row0 + row] = delta;
       __syncwarp();
-      if (lane == 0) mbar_arrive(bars + L::kOpReady + (n_item & 1));
+      if (lane == 0) mbar_arrive(bars + L::kDReady + (n_item & 1));
       if (n_item >= 1 && !read_out(prev, n_item - 1)) { ok = false; break; }
       prev = x;
-      g += 2 * x.n + 2;
+      g += 2 * x.n + 3;
       ++n_item;
     }
     if (ok && !*abort_flag && n_item >= 1) read_out(prev, n_item - 1);
@@ -517,6 +603,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------
 // dk and dv
 // ---------------------------------------------------------------------------
+struct KItem {
+  int hk;
+  int key0, keys;  // rows of k
+  int q0, q_len;   // first row of q that sees the tile, and the rows from there on
+  int diag;        // causal: tile key i is seen by rows q0 + r with r + diag >= i
+  int tiles;       // query tiles of one head
+  int n;           // query tiles of all heads of the group
+};
+
 template <int D>
 struct KLayout {
   static constexpr int DH = D / 64;
@@ -526,26 +621,19 @@ struct KLayout {
   static constexpr uint32_t kKOff = 0, kVOff = kTile;
   static constexpr uint32_t kRingOff = 2 * kTile;
   static constexpr uint32_t kRowOff = kRingOff + NST * kTile;  // [NROW][2][128] f32
-  static constexpr uint32_t kBarOff = kRowOff + NROW * 1024u;
+  static constexpr uint32_t kItemOff = kRowOff + NROW * 1024u;
+  static constexpr uint32_t kBarOff = kItemOff + (uint32_t)sizeof(ItemRing<KItem>);
   static constexpr int kFull = 0, kEmpty = NST, kPre = 2 * NST, kRowFull = 3 * NST,
-                       kRowEmpty = kRowFull + NROW, kKVFull = kRowEmpty + NROW, kKVEmpty = kKVFull + 1,
-                       kSFull = kKVEmpty + 1, kPFull = kSFull + 1, kDPFull = kPFull + 1,
-                       kDSFull = kDPFull + 1, kOFull = kDSFull + 1, kOEmpty = kOFull + 1,
-                       kNumBars = kOEmpty + 1;
+                       kRowEmpty = kRowFull + NROW, kKFull = kRowEmpty + NROW, kKEmpty = kKFull + 1,
+                       kVFull = kKEmpty + 1, kVEmpty = kVFull + 1, kSFull = kVEmpty + 1, kPFull = kSFull + 1, kDPFull = kPFull + 1,
+                       kDSFull = kDPFull + 1, kDVFull = kDSFull + 1, kDKFull = kDVFull + 1,
+                       kDVEmpty = kDKFull + 1, kDKEmpty = kDVEmpty + 1, kItFull = kDKEmpty + 1, kItEmpty = kItFull + kItemSlots,
+                       kNumBars = kItEmpty + kItemSlots;
   static constexpr uint32_t kMiscOff = kBarOff + 8u * kNumBars;
   static constexpr uint32_t kAlloc = kMiscOff + 16u + 1024u;
   static_assert(kAlloc <= 227u * 1024u, "shared memory");
 };
 constexpr uint32_t kKS = 0, kKDP = 128, kKDV = 256, kKDK = 384;
-
-struct KItem {
-  int hk;
-  int key0, keys;  // rows of k
-  int q0, q_len;   // first row of q that sees the tile, and the rows from there on
-  int diag;        // causal: tile key i is seen by rows q0 + r with r + diag >= i
-  int tiles;       // query tiles of one head
-  int n;           // query tiles of all heads of the group
-};
 
 __device__ __forceinline__ KItem load_kitem(const DenseBwdParams& p, const DenseSeqs& t, int w) {
   KItem x;
@@ -578,6 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   float* rowv = reinterpret_cast<float*>(smem + L::kRowOff);
+  ItemRing<KItem>* items = reinterpret_cast<ItemRing<KItem>*>(smem + L::kItemOff);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
@@ -588,9 +677,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < L::kNumBars; ++i) {
-      const uint32_t count = i == L::kOEmpty ? 4u
+      const uint32_t count = (i == L::kDVEmpty || i == L::kDKEmpty) ? 4u
                              : (i == L::kPFull || i == L::kDSFull ||
                                 (i >= L::kRowEmpty && i < L::kRowEmpty + NROW)) ? 8u
+                             : (i >= L::kItEmpty)                              ? 15u  // all warps but one
                                                                                : 1u;
       mbar_init(bars + i, count);
     }
@@ -608,18 +698,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
+  auto next = [&](uint32_t& w, KItem& x) {
+    return get_item(items, bars + L::kItFull, bars + L::kItEmpty, w, x, lane, abort_flag, p.status);
+  };
 
   if (warp < 4) {
     regs_dec<kRegsProducer>();
     if (warp == 0) {
       // ===================== Q and dO tiles =====================
-      if (lane == 0) {
-        const uint64_t keep = l2_policy_evict_last();
-        uint32_t g = 0;
-        bool ok = true;
-        for (int w = 0, it; ok && (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
-          if (it >= p.n_work) continue;
-          const KItem x = load_kitem(p, seqs, it);
+      const uint64_t keep = l2_policy_evict_last();
+      uint32_t g = 0, n_item = 0;
+      bool ok = true;
+      KItem x;
+      while (ok && next(n_item, x)) {
+        if (lane == 0) {
           for (int h = 0; ok && h < p.group; ++h)
             for (int t = 0; ok && t < 2 * x.tiles; ++t, ++g) {
               const int st = (int)(g % NST);
@@ -638,40 +730,64 @@ __global__ void __launch_bounds__(kThreads, 1)
                           x.q0 + r, x.hk * p.group + h, 0, keep);
             }
         }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      }
+      if (lane == 0)
         for (uint32_t t = (g > (uint32_t)NST ? g - NST : 0u); ok && t < g; ++t)
           ok = mbar_wait(bars + L::kEmpty + (int)(t % NST), (t / NST) & 1, abort_flag, p.status);
-      }
       __syncwarp();
     } else if (warp == 2) {
-      // ===================== K and V tiles =====================
-      if (lane == 0) {
-        const uint64_t once = l2_policy_evict_first();
-        uint32_t n_item = 0;
-        bool ok = true;
-        for (int w = 0, it; ok && (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
-          if (it >= p.n_work) continue;
-          const KItem x = load_kitem(p, seqs, it);
-          if (x.n == 0) continue;
-          if (n_item >= 1) ok = mbar_wait(bars + L::kKVEmpty, (n_item - 1) & 1, abort_flag, p.status);
-          if (!ok) break;
-          ++n_item;
-          mbar_arrive_expect_tx(bars + L::kKVFull, 2 * L::kTile);
+      // ===================== work items, their K and V tiles; keys that no row sees =====================
+      const uint64_t once = l2_policy_evict_first();
+      uint32_t n_item = 0;
+      bool ok = true;
+      KItem x;
+      for (int w = 0, it; ok && (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
+        if (it >= p.n_work) continue;
+        x = load_kitem(p, seqs, it);
+        if (x.n == 0) {
+          for (int r = lane; r < x.keys; r += 32) {
+            __nv_bfloat16* tk = p.dk + x.hk * p.dk_st.h + (long long)(x.key0 + r) * p.dk_st.s;
+            __nv_bfloat16* tv = p.dv + x.hk * p.dv_st.h + (long long)(x.key0 + r) * p.dv_st.s;
+            for (int e = 0; e < D; e += 8) {
+              *reinterpret_cast<uint4*>(tk + e) = make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(tv + e) = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+          continue;
+        }
+        if (!put_item(items, bars + L::kItFull, bars + L::kItEmpty, n_item, x, lane, abort_flag, p.status)) { ok = false; break; }
+        if (lane == 0) {
+          // K, once the previous item's last S is complete; V, once its last dP is
+          if (n_item >= 1) ok = mbar_wait(bars + L::kKEmpty, (n_item - 1) & 1, abort_flag, p.status);
+          if (ok) {
+            mbar_arrive_expect_tx(bars + L::kKFull, L::kTile);
 #pragma unroll
-          for (int dh = 0; dh < L::DH; ++dh) {
-            load_rows(smem + L::kKOff + dh * 16384, &tm_k, p.k_ax, bars + L::kKVFull, dh * 64, x.key0, x.hk, 0, once);
-            load_rows(smem + L::kVOff + dh * 16384, &tm_v, p.v_ax, bars + L::kKVFull, dh * 64, x.key0, x.hk, 0, once);
+            for (int dh = 0; dh < L::DH; ++dh)
+              load_rows(smem + L::kKOff + dh * 16384, &tm_k, p.k_ax, bars + L::kKFull, dh * 64, x.key0, x.hk, 0, once);
+            if (n_item >= 1) ok = mbar_wait(bars + L::kVEmpty, (n_item - 1) & 1, abort_flag, p.status);
+          }
+          if (ok) {
+            mbar_arrive_expect_tx(bars + L::kVFull, L::kTile);
+#pragma unroll
+            for (int dh = 0; dh < L::DH; ++dh)
+              load_rows(smem + L::kVOff + dh * 16384, &tm_v, p.v_ax, bars + L::kVFull, dh * 64, x.key0, x.hk, 0, once);
           }
         }
-        if (ok && n_item >= 1) mbar_wait(bars + L::kKVEmpty, (n_item - 1) & 1, abort_flag, p.status);
+        ++n_item;
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       }
+      x.n = -1;
+      if (ok) ok = put_item(items, bars + L::kItFull, bars + L::kItEmpty, n_item, x, lane, abort_flag, p.status);
+      // every copy has been consumed before exit
+      if (ok && lane == 0 && n_item >= 1) mbar_wait(bars + L::kVEmpty, (n_item - 1) & 1, abort_flag, p.status);
       __syncwarp();
     } else if (warp == 3) {
       // ============ -lse and delta rows; zero Q and dO rows past a sequence ============
-      uint32_t g = 0, pre = 0;  // query tiles so far; phase bit per ring stage
+      uint32_t g = 0, pre = 0, n_item = 0;  // query tiles so far; phase bit per ring stage; items
       bool ok = true;
-      for (int w = 0, it; ok && (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
-        if (it >= p.n_work) continue;
-        const KItem x = load_kitem(p, seqs, it);
+      KItem x;
+      while (ok && next(n_item, x)) {
         for (int h = 0; ok && h < p.group; ++h) {
           const long long at = (x.hk * p.group + h) * p.lse_seq + x.q0;
           for (int t = 0; ok && t < x.tiles; ++t, ++g) {
@@ -711,28 +827,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
       // ===================== MMA issue =====================
-      uint32_t g = 0, n_item = 0;  // query tiles, items so far
+      uint32_t g = 0;    // query tiles so far
+      uint32_t n_s = 0;  // items whose first S was issued
       bool ok = true;
       auto full = [&](uint32_t at) {
         const bool r = warp_wait(bars + L::kFull + (int)(at % NST), (at / NST) & 1, abort_flag, p.status);
         tc_fence_after_sync();
         return r;
       };
-      auto do_s = [&](uint32_t i) {
-        const uint32_t at = 2 * i;
+      // S of query tile number t (its i-th of item x)
+      auto do_s = [&](const KItem& x, int i, uint32_t t) {
+        if (i == 0) {
+          if (!warp_wait(bars + L::kKFull, n_s & 1, abort_flag, p.status)) { ok = false; return; }
+          ++n_s;
+        }
+        const uint32_t at = 2 * t;
         if (!full(at)) { ok = false; return; }
         if (elect_one()) {
           issue_s<D>(tmem_base + kKS, sbase + L::kKOff, sbase + L::kRingOff + (at % NST) * L::kTile);
           umma_commit(bars + L::kSFull);
+          if (i == x.n - 1) umma_commit(bars + L::kKEmpty);
         }
         __syncwarp();
       };
-      for (int w = 0, it; ok && (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
-        if (it >= p.n_work) continue;
-        const KItem x = load_kitem(p, seqs, it);
-        if (x.n == 0) continue;
-        if (!warp_wait(bars + L::kKVFull, n_item & 1, abort_flag, p.status)) break;
-        do_s(g);
+      uint32_t n_got = 0, n_item = 0;
+      KItem x, y;
+      bool have = next(n_got, x);
+      if (have) do_s(x, 0, 0);
+      while (ok && have) {
+        const bool more = next(n_got, y);
+        if (!warp_wait(bars + L::kVFull, n_item & 1, abort_flag, p.status)) break;
         int t = 0;  // query tile of the head
         for (int i = 0; ok && i < x.n; ++i, ++g) {
           const int left = x.q_len - 128 * t;
@@ -743,116 +867,141 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (elect_one()) {
             issue_s<D>(tmem_base + kKDP, sbase + L::kVOff, sbase + L::kRingOff + st_do * L::kTile);
             umma_commit(bars + L::kDPFull);
-            if (i == x.n - 1) umma_commit(bars + L::kKVEmpty);
+            if (i == x.n - 1) umma_commit(bars + L::kVEmpty);
           }
           __syncwarp();
-          // the epilogue has taken the previous item's dK and dV
+          // the epilogue has taken the previous item's dV
           if (i == 0 && n_item >= 1 &&
-              !warp_wait(bars + L::kOEmpty, (n_item - 1) & 1, abort_flag, p.status)) { ok = false; break; }
+              !warp_wait(bars + L::kDVEmpty, (n_item - 1) & 1, abort_flag, p.status)) { ok = false; break; }
           if (!warp_wait(bars + L::kPFull, g & 1, abort_flag, p.status)) { ok = false; break; }
           tc_fence_after_sync();
           if (elect_one()) {
             issue_halves<D>(tmem_base + kKDV, tmem_base + kKS, sbase + L::kRingOff + st_do * L::kTile, steps, i > 0);
             umma_commit(bars + L::kEmpty + (int)st_do);
+            if (i == x.n - 1) umma_commit(bars + L::kDVFull);
           }
           __syncwarp();
-          if (i + 1 < x.n) do_s(g + 1);
+          if (i + 1 < x.n) do_s(x, i + 1, g + 1);
+          else if (more) do_s(y, 0, g + 1);
           if (!ok) break;
+          if (i == 0 && n_item >= 1 &&
+              !warp_wait(bars + L::kDKEmpty, (n_item - 1) & 1, abort_flag, p.status)) { ok = false; break; }
           if (!warp_wait(bars + L::kDSFull, g & 1, abort_flag, p.status)) { ok = false; break; }
           tc_fence_after_sync();
           if (elect_one()) {
             issue_halves<D>(tmem_base + kKDK, tmem_base + kKDP, sbase + L::kRingOff + st_q * L::kTile, steps, i > 0);
             umma_commit(bars + L::kEmpty + (int)st_q);
-            if (i == x.n - 1) umma_commit(bars + L::kOFull);
+            if (i == x.n - 1) umma_commit(bars + L::kDKFull);
           }
           __syncwarp();
         }
+        x = y;
+        have = more;
         ++n_item;
       }
     }
   } else if (warp < 12) {
     regs_inc<kRegsSoftmax>();
-    // ===================== p and ds: one thread per key and 64 query rows =====================
+    // ===================== p and ds =====================
+    // A warp has 32 keys (TMEM lanes) and 64 query rows (columns).  -lse and
+    // delta go with the columns, so they come from shared memory; a thread
+    // that held a key's whole row would read 64 of each, and a warp's reads of
+    // one address cost as much as reads of 32.  In the 16x256b form a thread
+    // holds four keys (lane / 4 + 8 k) and the columns 8 i + 2 (lane % 4) + {0, 1}
+    // and reads a quarter of that (measured: 1950 -> @A@ cycles for p, 760 -> @B@ for ds).
     const int half = (warp - 4) >> 2;
-    const int row = (warp & 3) * 32 + lane;
     const uint32_t t_lane = tmem_base + (uint32_t((warp & 3) * 32) << 16) + 64u * half;
+    constexpr uint32_t kUpper = 16u << 16;  // lanes 16-31 of the warp
+    const int row0 = (warp & 3) * 32 + lane / 4, col0 = 2 * (lane & 3);
     const uint64_t cc = pk2(p.scale_log2, p.scale_log2);
-    uint32_t g = 0;
+    uint32_t g = 0, n_got = 0;
     bool ok = true;
-    for (int w = 0, it; ok && (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
-      if (it >= p.n_work) continue;
-      const KItem x = load_kitem(p, seqs, it);
+    KItem x;
+    while (ok && next(n_got, x)) {
       int t = 0;
       for (int i = 0; i < x.n; ++i, ++g) {
-        // rows of this half from `first` on see the key
-        const int first = p.causal ? row - x.diag - 128 * t - 64 * half : 0;
+        // column c of this half sees key row r where c >= r - shift
+        const int shift = x.diag + 128 * t + 64 * half;
         if (++t == x.tiles) t = 0;
-        const bool masked = __any_sync(0xffffffffu, first > 0);
+        const bool masked = p.causal && (warp & 3) * 32 + 31 > shift;
         const int slot = (int)(g % NROW);
-        const float* nl = rowv + slot * 256 + 64 * half;
+        const float* nl = rowv + slot * 256 + 64 * half + col0;
         if (!warp_wait(bars + L::kRowFull + slot, (g / NROW) & 1, abort_flag, p.status) ||
             !warp_wait(bars + L::kSFull, g & 1, abort_flag, p.status)) { ok = false; break; }
         tc_fence_after_sync();
+        // v[32 u + 4 i + 2 b + e]: key row0 + 16 u + 8 b, column 8 i + col0 + e
         uint32_t v[64];
-        tmem_ld64(t_lane + kKS, v);
+        tmem_ld_16x256(t_lane + kKS, v, 0);
+        tmem_ld_16x256(t_lane + kKS + kUpper, v, 32);
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+        const int under = row0 - col0 - shift;  // element (u, i, b, e) is masked where 8 i + e - 16 u - 8 b < under
+        auto probs = [&](auto mk) {
+          constexpr bool kMask = decltype(mk)::value;
+          uint64_t ll[8];
 #pragma unroll
-        for (int q0 = 0; q0 < 32; q0 += 16) {
-          uint32_t pk[16];
+          for (int i8 = 0; i8 < 8; ++i8) {
+            const float2 l2 = *reinterpret_cast<const float2*>(nl + 8 * i8);
+            ll[i8] = pk2(l2.x, l2.y);
+          }
 #pragma unroll
-          for (int q1 = 0; q1 < 16; q1 += 2) {
-            const float4 l4 = *reinterpret_cast<const float4*>(nl + 2 * (q0 + q1));
+          for (int u = 0; u < 2; ++u) {
+            uint32_t pk[16];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int q = q1 + u, e = 2 * (q0 + q);
+            for (int k = 0; k < 16; ++k) {
+              const int e = 32 * u + 2 * k;
               float a, b;
-              upk2(ffma2(pk2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), cc,
-                         u ? pk2(l4.z, l4.w) : pk2(l4.x, l4.y)), a, b);
-              if ((q & 7) < DENSE_BWD_POLY8) {
+              upk2(ffma2(pk2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), cc, ll[k >> 1]), a, b);
+              if (kMask) {
+                const int at = 8 * (k >> 1) - 16 * u - 8 * (k & 1);
+                if (at < under) a = -INFINITY;
+                if (at + 1 < under) b = -INFINITY;
+              }
+              if (!kMask && (k & 7) < DENSE_BWD_POLY8) {
                 upk2(exp2_fma2_t<true>(a, b), a, b);
               } else {
                 a = fast_exp2(a);
                 b = fast_exp2(b);
               }
-              if (masked) {
-                a = e >= first ? a : 0.f;
-                b = e + 1 >= first ? b : 0.f;
-              }
               v[e] = __float_as_uint(a);
               v[e + 1] = __float_as_uint(b);
-              pk[q] = pack_bf16x2(a, b);
+              pk[k] = pack_bf16x2(a, b);
             }
+            tmem_st_16x128(t_lane + kKS + u * kUpper, pk);
           }
-          VSA_TMEM_ST16(t_lane + kKS + q0, pk, 0);
-        }
+        };
+        if (masked) probs(std::true_type{});
+        else probs(std::false_type{});
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + L::kPFull);
         if (!warp_wait(bars + L::kDPFull, g & 1, abort_flag, p.status)) { ok = false; break; }
         tc_fence_after_sync();
+        uint64_t dd[8];
 #pragma unroll
-        for (int q0 = 0; q0 < 32; q0 += 16) {
+        for (int i8 = 0; i8 < 8; ++i8) {
+          const float2 d2 = *reinterpret_cast<const float2*>(nl + 128 + 8 * i8);
+          dd[i8] = pk2(d2.x, d2.y);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
           uint32_t dp[32], pk[16];
-          tmem_ld32(t_lane + kKDP + 2 * q0, dp);
+          tmem_ld_16x256(t_lane + kKDP + u * kUpper, dp, 0);
+          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+          if (masked) {
+            // p = 0 there, but dP may be infinite
 #pragma unroll
-          for (int q1 = 0; q1 < 16; q1 += 2) {
-            const float4 d4 = *reinterpret_cast<const float4*>(nl + 128 + 2 * (q0 + q1));
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int q = q1 + u, e = 2 * (q0 + q);
-              float a, b;
-              upk2(fadd2(pk2(__uint_as_float(dp[2 * q]), __uint_as_float(dp[2 * q + 1])),
-                         u ? pk2(d4.z, d4.w) : pk2(d4.x, d4.y)), a, b);
-              a *= __uint_as_float(v[e]);
-              b *= __uint_as_float(v[e + 1]);
-              if (masked) {
-                a = e >= first ? a : 0.f;
-                b = e + 1 >= first ? b : 0.f;
-              }
-              pk[q] = pack_bf16x2(a, b);
-            }
+            for (int k = 0; k < 32; ++k)
+              if (8 * (k >> 2) + (k & 1) - 16 * u - 8 * ((k >> 1) & 1) < under) dp[k] = 0u;
           }
-          VSA_TMEM_ST16(t_lane + kKDP + q0, pk, 0);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int e = 32 * u + 2 * k;
+            float a, b;
+            upk2(fadd2(pk2(__uint_as_float(dp[2 * k]), __uint_as_float(dp[2 * k + 1])), dd[k >> 1]), a, b);
+            pk[k] = pack_bf16x2(a * __uint_as_float(v[e]), b * __uint_as_float(v[e + 1]));
+          }
+          tmem_st_16x128(t_lane + kKDP + u * kUpper, pk);
         }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before_sync();
@@ -868,50 +1017,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ===================== results: one thread per key =====================
     const int row = (warp - 12) * 32 + lane;
     const uint32_t t_lane = tmem_base + (uint32_t((warp - 12) * 32) << 16);
-    uint32_t n_item = 0;
-    for (int w = 0, it; (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
-      if (it >= p.n_work) continue;
-      const KItem x = load_kitem(p, seqs, it);
+    uint32_t n_item = 0, n_got = 0;
+    KItem x;
+    while (next(n_got, x)) {
       const bool real = row < x.keys;
       __nv_bfloat16* tk = p.dk + x.hk * p.dk_st.h + (long long)(x.key0 + row) * p.dk_st.s;
       __nv_bfloat16* tv = p.dv + x.hk * p.dv_st.h + (long long)(x.key0 + row) * p.dv_st.s;
-      if (x.n == 0) {
-        // keys that no row sees
-        if (real) {
-#pragma unroll
-          for (int e = 0; e < D; e += 8) {
-            *reinterpret_cast<uint4*>(tk + e) = make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4*>(tv + e) = make_uint4(0u, 0u, 0u, 0u);
-          }
-        }
-        continue;
-      }
-      if (!warp_wait(bars + L::kOFull, n_item & 1, abort_flag, p.status)) break;
-      ++n_item;
-      tc_fence_after_sync();
+      bool ok = true;
 #pragma unroll 1
-      for (int q0 = 0; q0 < 2 * D; q0 += 32) {
-        const bool is_k = q0 >= D;
-        uint32_t ov[32];
-        tmem_ld32(t_lane + (is_k ? kKDK + q0 - D : kKDV + q0), ov);
-        if (q0 + 32 == 2 * D) {
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bars + L::kOEmpty);
-        }
-        const float m = is_k ? p.scale : 1.f;
-        if (real) {
-          __nv_bfloat16* to = is_k ? tk + q0 - D : tv + q0;
+      for (int k = 0; ok && k < 2; ++k) {  // dV, then dK
+        ok = warp_wait(bars + (k ? L::kDKFull : L::kDVFull), n_item & 1, abort_flag, p.status);
+        if (!ok) break;
+        tc_fence_after_sync();
+        __nv_bfloat16* to = k ? tk : tv;
+        const float m = k ? p.scale : 1.f;
+#pragma unroll 1
+        for (int q0 = 0; q0 < D; q0 += 32) {
+          uint32_t ov[32];
+          tmem_ld32(t_lane + (k ? kKDK : kKDV) + q0, ov);
+          if (q0 + 32 == D) {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars + (k ? L::kDKEmpty : L::kDVEmpty));
+          }
+          if (real) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint32_t o[4];
+            for (int e = 0; e < 32; e += 8) {
+              uint32_t o[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              o[q] = pack_bf16x2(__uint_as_float(ov[e + 2 * q]) * m, __uint_as_float(ov[e + 2 * q + 1]) * m);
-            *reinterpret_cast<uint4*>(to + e) = make_uint4(o[0], o[1], o[2], o[3]);
+              for (int q = 0; q < 4; ++q)
+                o[q] = pack_bf16x2(__uint_as_float(ov[e + 2 * q]) * m, __uint_as_float(ov[e + 2 * q + 1]) * m);
+              *reinterpret_cast<uint4*>(to + q0 + e) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
           }
         }
       }
+      if (!ok) break;
+      ++n_item;
     }
   }
 
@@ -954,7 +1096,7 @@ static int launch_dense_bwd_t(DenseBwdParams p, const CUtensorMap* m, const int4
     fill_dense_seqs(&table, seqs, units, n);
     p.n_work = table.n_items * p.Hkv;
     kq<<<(unsigned)(p.n_work < sms ? p.n_work : sms), dense::kThreads, dense::QLayout<D>::kAlloc, stream>>>(
-        m[0], m[1], m[2], m[3], p, table);
+        m[0], m[1], m[2], m[3], m[4], p, table);
   }
   if (k_units > 0) {
     for (int i = 0; i < n; ++i) units[i] = (seqs[i].w + 127) / 128;
@@ -966,8 +1108,8 @@ static int launch_dense_bwd_t(DenseBwdParams p, const CUtensorMap* m, const int4
   return cudaGetLastError() == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
 }
 
-int launch_dense_bwd(const DenseBwdParams& p_in, const DenseTensors& t, const void* dout, Strides3 do_st,
-                     const DenseBatch& b, int D, cudaStream_t stream) {
+int launch_dense_bwd(const DenseBwdParams& p_in, const DenseTensors& t, const void* out, Strides3 out_st,
+                     const void* dout, Strides3 do_st, const DenseBatch& b, int D, cudaStream_t stream) {
   DenseBwdParams p = p_in;
   // without rows or keys no tile is loaded; the maps only have to be valid
   const bool rows = t.q_seq > 0, keys = t.kv_seq > 0;
@@ -975,7 +1117,7 @@ int launch_dense_bwd(const DenseBwdParams& p_in, const DenseTensors& t, const vo
   const long long any_seq = rows ? t.q_seq : t.kv_seq;
   const int any_h = rows ? p.Hq : p.Hkv;
   const Strides3 any_st = rows ? t.q_st : t.k_st;
-  CUtensorMap m[4];
+  CUtensorMap m[5];
   auto map = [&](CUtensorMap* to, TmaAxes* ax, bool have, const void* base, long long seq, int H, Strides3 st) {
     return have ? make_view_map_rows(to, ax, base, D, seq, H, 1, st, 128)
                 : make_view_map_rows(to, ax, any, D, any_seq, any_h, 1, any_st, 128);
@@ -983,7 +1125,8 @@ int launch_dense_bwd(const DenseBwdParams& p_in, const DenseTensors& t, const vo
   if (!map(&m[0], &p.q_ax, rows, t.q, t.q_seq, p.Hq, t.q_st) ||
       !map(&m[1], &p.k_ax, keys, t.k, t.kv_seq, p.Hkv, t.k_st) ||
       !map(&m[2], &p.v_ax, keys, t.v, t.kv_seq, p.Hkv, t.v_st) ||
-      !map(&m[3], &p.do_ax, rows, dout, t.q_seq, p.Hq, do_st))
+      !map(&m[3], &p.do_ax, rows, dout, t.q_seq, p.Hq, do_st) ||
+      !map(&m[4], &p.o_ax, rows, out, t.q_seq, p.Hq, out_st))
     return VSA_ERR_CUDA;
   for (int i0 = 0; i0 < b.n; i0 += kDenseMaxSeqs) {
     int4 seqs[kDenseMaxSeqs];

@@ -154,11 +154,9 @@ int dense_attn_varlen_backward(const void* q, const void* k, const void* v, cons
     return VSA_ERR_WORKSPACE;
   DenseBwdParams p;
   memset(&p, 0, sizeof(p));
-  p.out = static_cast<const __nv_bfloat16*>(out);
   p.dq = static_cast<__nv_bfloat16*>(dq);
   p.dk = static_cast<__nv_bfloat16*>(dk);
   p.dv = static_cast<__nv_bfloat16*>(dv);
-  p.out_st = to3(L.out);
   p.dq_st = to3(L.dq);
   p.dk_st = to3(L.dk);
   p.dv_st = to3(L.dv);
@@ -175,7 +173,7 @@ int dense_attn_varlen_backward(const void* q, const void* k, const void* v, cons
   if (!p.status) return VSA_ERR_CUDA;
   const DenseTensors t{q, k, v, to3(L.q), to3(L.k), to3(L.v), rows ? q_rows : 0, keys ? kv_rows : 0};
   const DenseBatch b{cu_seqlens_q, cu_seqlens_kv, n_seqs};
-  return launch_dense_bwd(p, t, dout, to3(L.dout), b, D, static_cast<cudaStream_t>(stream));
+  return launch_dense_bwd(p, t, out, to3(L.out), dout, to3(L.dout), b, D, static_cast<cudaStream_t>(stream));
 }
 
 size_t shared_prefix_attn_workspace_size(int B, int Hq, int Hkv, int T, int D, int64_t prefix_len,

@@ -72,21 +72,20 @@ int launch_dense_fwd(const DenseParams& p, const DenseTensors& t, const DenseBat
 
 // Gradients (dense_bwd.cu): one launch for dq (and delta), one for dk and dv.
 struct DenseBwdParams {
-  const __nv_bfloat16* out;
   __nv_bfloat16 *dq, *dk, *dv;
-  Strides3 out_st, dq_st, dk_st, dv_st;
+  Strides3 dq_st, dk_st, dv_st;
   const float* lse;                 // [Hq, lse_seq]
   float* delta;                     // [Hq, lse_seq] workspace
   long long lse_seq;
-  TmaAxes q_ax, k_ax, v_ax, do_ax;
+  TmaAxes q_ax, k_ax, v_ax, do_ax, o_ax;
   int Hq, Hkv, group;
   int causal;
   int n_work;
   float scale, scale_log2;
   int* status;
 };
-int launch_dense_bwd(const DenseBwdParams& p, const DenseTensors& t, const void* dout, Strides3 do_st,
-                     const DenseBatch& b, int D, cudaStream_t stream);
+int launch_dense_bwd(const DenseBwdParams& p, const DenseTensors& t, const void* out, Strides3 out_st,
+                     const void* dout, Strides3 do_st, const DenseBatch& b, int D, cudaStream_t stream);
 
 // Shared-prefix decoding (prefix_attn.cu).  CTAs of its attention kernel: one
 // per SM, and a constant, so that the workspace and the split of the work (and
