@@ -80,6 +80,18 @@ __device__ __forceinline__ bool get_item(const ItemRing<Item>* ring, uint64_t* f
   return x.n >= 0;
 }
 
+// The same for a role that one thread plays.
+template <typename Item>
+__device__ __forceinline__ bool get_item_one(const ItemRing<Item>* ring, uint64_t* full, uint64_t* empty,
+                                             uint32_t& w, Item& x, volatile int* abort_flag, int* status) {
+  const int slot = (int)(w % kItemSlots);
+  if (!mbar_wait(full + slot, (w / kItemSlots) & 1, abort_flag, status)) return false;
+  x = ring->item[slot];
+  mbar_arrive(empty + slot);
+  ++w;
+  return x.n >= 0;
+}
+
 // 64 head dims x box rows of a [H, S, D] view through its tile map.
 __device__ __forceinline__ void load_rows(void* dst, const CUtensorMap* map, TmaAxes ax,
                                           uint64_t* bar, int d0, int s, int h, int b,

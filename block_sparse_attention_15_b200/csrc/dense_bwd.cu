@@ -50,11 +50,8 @@ namespace vsa {
 namespace dense {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr uint32_t kRegsProducer = 104, kRegsSoftmax = 168, kRegsEpilogue = 72;
-constexpr uint32_t kLaunchRegs = 128;  // 512 x 128 = 65536
-static_assert(128u * (kRegsProducer + 2u * kRegsSoftmax + kRegsEpilogue) <= 512u * kLaunchRegs,
-              "register split exceeds the launch's registers");
+constexpr int kThreads = 768;
+constexpr int kSoftmaxWarps = 16;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2 = 1.4426950408889634f;
 #ifndef DENSE_BWD_POLY8
@@ -77,52 +74,44 @@ __device__ __forceinline__ void issue_ta(uint32_t tmem_d, uint32_t tmem_a, uint3
 }
 
 // D (+)= A B over the first 16 * steps rows of the tile B [D / 64][128][128 B];
-// A [128][128] bf16 in TMEM: columns 0-63 at tmem_a, 64-127 at tmem_a + 64
-// (each half over the fp32 columns of the softmax warpgroup that wrote it).
+// A [128][128] bf16 in TMEM: 32 columns at each of tmem_a + 0, 32, 64, 96 (over
+// the fp32 columns of the softmax warpgroup that wrote them).
 template <int D>
-__device__ __forceinline__ void issue_halves(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_base,
+__device__ __forceinline__ void issue_quarters(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_base,
                                              int steps, bool accumulate) {
   constexpr uint32_t idesc = make_idesc_bf16(128, D, false, true);
   const uint64_t b0 = make_sdesc_sw128(b_base, 16384u, 1024u);
   if (steps == 8) {
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
-      umma_bf16_tmem_a(tmem_d, tmem_a + 64u * (kk / 4) + 8u * (kk % 4), b0 + (uint64_t)((kk * 2048) >> 4),
+      umma_bf16_tmem_a(tmem_d, tmem_a + 32u * (kk / 2) + 8u * (kk % 2), b0 + (uint64_t)((kk * 2048) >> 4),
                        idesc, (accumulate || kk > 0) ? 1u : 0u);
   } else {
     for (int kk = 0; kk < steps; ++kk)
-      umma_bf16_tmem_a(tmem_d, tmem_a + 64u * (kk / 4) + 8u * (kk % 4), b0 + (uint64_t)((kk * 2048) >> 4),
+      umma_bf16_tmem_a(tmem_d, tmem_a + 32u * (kk / 2) + 8u * (kk % 2), b0 + (uint64_t)((kk * 2048) >> 4),
                        idesc, (accumulate || kk > 0) ? 1u : 0u);
   }
 }
 
-// 16 TMEM lanes x 64 fp32 columns: register 4 i + 2 b + e holds lane
+// 16 TMEM lanes x 32 fp32 columns: register 4 i + 2 b + e holds lane
 // threadIdx / 4 + 8 b, column 8 i + 2 (threadIdx % 4) + e.
 template <int N>
 __device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, uint32_t (&r)[N], int o) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(r[o + 0]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]),
         "=r"(r[o + 6]), "=r"(r[o + 7]), "=r"(r[o + 8]), "=r"(r[o + 9]), "=r"(r[o + 10]), "=r"(r[o + 11]),
-        "=r"(r[o + 12]), "=r"(r[o + 13]), "=r"(r[o + 14]), "=r"(r[o + 15]), "=r"(r[o + 16]), "=r"(r[o + 17]),
-        "=r"(r[o + 18]), "=r"(r[o + 19]), "=r"(r[o + 20]), "=r"(r[o + 21]), "=r"(r[o + 22]), "=r"(r[o + 23]),
-        "=r"(r[o + 24]), "=r"(r[o + 25]), "=r"(r[o + 26]), "=r"(r[o + 27]), "=r"(r[o + 28]), "=r"(r[o + 29]),
-        "=r"(r[o + 30]), "=r"(r[o + 31])
+        "=r"(r[o + 12]), "=r"(r[o + 13]), "=r"(r[o + 14]), "=r"(r[o + 15])
       : "r"(taddr));
 }
 
-// 16 TMEM lanes x 32 columns of 32 bits: register 2 i + b holds lane
+// 16 TMEM lanes x 16 columns of 32 bits: register 2 i + b holds lane
 // threadIdx / 4 + 8 b, column 4 i + threadIdx % 4.
-__device__ __forceinline__ void tmem_st_16x128(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
-      "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
-      "r"(r[14]), "r"(r[15])
-      : "memory");
+__device__ __forceinline__ void tmem_st_16x128(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -141,7 +130,7 @@ template <int D>
 struct QLayout {
   static constexpr int DH = D / 64;
   static constexpr uint32_t kTile = 128u * D * 2u;
-  static constexpr int NST = D == 128 ? 6 : 10;  // ring: Q, dO, out, K(0), V(0), K(1), ...
+  static constexpr int NST = D == 128 ? 7 : 12;  // ring: Q, dO, out, K(0), V(0), K(1), ...
   static constexpr uint32_t kRingOff = 0;
   static constexpr uint32_t kRowOff = kRingOff + NST * kTile;  // [2][2][128] f32: -lse, delta
   static constexpr uint32_t kItemOff = kRowOff + 2048u;
@@ -159,7 +148,7 @@ struct QLayout {
                        kOEmpty = kOFull + 1, kItFull = kOEmpty + 1, kItEmpty = kItFull + kItemSlots,
                        kNumBars = kItEmpty + kItemSlots;
   static constexpr uint32_t kMiscOff = kBarOff + 8u * kNumBars;
-  static constexpr uint32_t kAlloc = kMiscOff + 16u + 1024u;
+  static constexpr uint32_t kAlloc = kMiscOff + 16u;
   static_assert(kAlloc <= 227u * 1024u, "shared memory");
 };
 // TMEM columns
@@ -189,10 +178,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ DenseBwdParams p, const __grid_constant__ DenseSeqs seqs) {
   using L = QLayout<D>;
   constexpr int NST = L::NST;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
+  if (sbase & 1023u) {  // the tiles' swizzle needs it; there is no room to align by hand
+    set_status(p.status, VSA_ERR_UNSUPPORTED);
+    return;
+  }
   float* rowv = reinterpret_cast<float*>(smem + L::kRowOff);
   ItemRing<QItem>* items = reinterpret_cast<ItemRing<QItem>*>(smem + L::kItemOff);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
@@ -208,8 +199,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a TMA transaction, a commit or one thread's arrival, except where the
       // epilogue's four or the softmax's eight warps arrive
       const uint32_t count = ((i >= L::kQReady && i < L::kQFree) || i == L::kOEmpty) ? 4u
-                             : (i == L::kSFree || i == L::kDSFull)                    ? 8u
-                             : (i >= L::kItEmpty)                                     ? 15u  // all warps but one
+                             : (i == L::kSFree || i == L::kDSFull)                    ? (uint32_t)kSoftmaxWarps
+                             : (i >= L::kItEmpty)                                     ? kThreads / 32 - 1u  // all warps but one
                                                                                       : 1u;
       mbar_init(bars + i, count);
     }
@@ -232,7 +223,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp < 4) {
-    regs_dec<kRegsProducer>();
     if (warp == 0) {
       // ===================== tile loads =====================
       const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
@@ -266,10 +256,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       }
-      // every stage's release lands before exit
-      if (lane == 0)
-        for (uint32_t t = (g > (uint32_t)NST ? g - NST : 0u); ok && t < g; ++t)
-          ok = mbar_wait(bars + L::kEmpty + (int)(t % NST), (t / NST) & 1, abort_flag, p.status);
       __syncwarp();
     } else if (warp == 3) {
       // ===================== work items; rows that see no key =====================
@@ -309,108 +295,107 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bars + L::kFull + st);
       }
     } else if (warp == 1) {
-      // ===================== MMA issue =====================
-      uint32_t ts = 0, tq = 0;     // S and dQ products so far
-      uint32_t n_s = 0, n_dp = 0;  // items whose first S, first dP was issued
-      uint32_t phase = 0;          // phase bit per ring stage
-      bool ok = true;
-      auto full = [&](uint32_t at) {
-        const int st = (int)(at % NST);
-        const bool r = warp_wait(bars + L::kFull + st, (phase >> st) & 1, abort_flag, p.status);
-        phase ^= 1u << st;
-        tc_fence_after_sync();
-        return r;
-      };
-      auto release = [&](uint32_t at) { mbar_arrive(bars + L::kEmpty + (int)(at % NST)); };
-      // S(j) and dP(j) of item x, whose ring tiles start at g
-      auto do_s = [&](const QItem& x, int j, uint32_t g) {
-        if (j == 0) {
-          // Q is in TMEM, its ring stage free again
-          if (!warp_wait(bars + L::kQReady + (n_s & 1), (n_s >> 1) & 1, abort_flag, p.status)) { ok = false; return; }
-          ++n_s;
-          if (elect_one()) release(g);
-          __syncwarp();
-        }
-        const uint32_t at = g + 3 + 2 * j;
-        if (!full(at)) { ok = false; return; }
-        if (ts >= 1 && !warp_wait(bars + L::kSFree, (ts - 1) & 1, abort_flag, p.status)) { ok = false; return; }
-        ++ts;
-        tc_fence_after_sync();
-        if (elect_one()) {
-          issue_ta<D>(tmem_base + kQS, tmem_base + kQQ, sbase + L::kRingOff + (at % NST) * L::kTile);
+      // ===================== MMA issue: one thread =====================
+      if (elect_one()) {
+        uint32_t phase = 0;          // phase bit per ring stage
+        uint32_t ts = 0, tq = 0;     // S and dQ products so far
+        uint32_t n_s = 0, n_dp = 0;  // items whose first S, first dP was issued
+        uint32_t g = 0, n_got = 0, n_item = 0;
+        bool ok = true;
+        auto wait = [&](int bar, uint32_t ph) {
+          if (!mbar_wait(bars + bar, ph & 1, abort_flag, p.status)) ok = false;
+        };
+        auto wait_stage = [&](uint32_t at) {
+          const uint32_t st = at % NST;
+          wait(L::kFull + (int)st, phase >> st);
+          phase ^= 1u << st;
+        };
+        auto tile = [&](uint32_t at) { return sbase + L::kRingOff + (at % NST) * L::kTile; };
+        auto release = [&](uint32_t at) { mbar_arrive(bars + L::kEmpty + (int)(at % NST)); };
+        // S(j) of item x, whose ring tiles start at gx
+        auto do_s = [&](const QItem& x, int j, uint32_t gx) {
+          if (j == 0) {
+            // Q is in TMEM, its ring stage free again
+            wait(L::kQReady + (int)(n_s & 1), n_s >> 1);
+            ++n_s;
+            release(gx);
+          }
+          wait_stage(gx + 3 + 2 * j);
+          if (ts >= 1) wait(L::kSFree, ts - 1);
+          if (!ok) return;
+          ++ts;
+          tc_fence_after_sync();
+          issue_ta<D>(tmem_base + kQS, tmem_base + kQQ, tile(gx + 3 + 2 * j));
           umma_commit(bars + L::kSFull);
           if (j == x.n - 1) umma_commit(bars + L::kQFree);
-        }
-        __syncwarp();
-      };
-      auto do_dp = [&](const QItem& x, int j, uint32_t g) {
-        if (j == 0) {
-          if (!warp_wait(bars + L::kGReady, n_dp & 1, abort_flag, p.status)) { ok = false; return; }
-          ++n_dp;
-        }
-        const uint32_t at = g + 4 + 2 * j;
-        if (!full(at)) { ok = false; return; }
-        if (elect_one()) {
-          issue_ta<D>(tmem_base + kQDP, tmem_base + kQDO, sbase + L::kRingOff + (at % NST) * L::kTile);
+        };
+        // what dP(j) waits for, and dP(j)
+        auto before_dp = [&](int j, uint32_t gx) {
+          if (j == 0) wait(L::kGReady, n_dp++);
+          wait_stage(gx + 4 + 2 * j);
+        };
+        auto do_dp = [&](const QItem& x, int j, uint32_t gx) {
+          issue_ta<D>(tmem_base + kQDP, tmem_base + kQDO, tile(gx + 4 + 2 * j));
           umma_commit(bars + L::kDPFull);
-          umma_commit(bars + L::kEmpty + (int)(at % NST));
           if (j == x.n - 1) umma_commit(bars + L::kGFree);
+        };
+        auto next_one = [&](QItem& x) {
+          return get_item_one(items, bars + L::kItFull, bars + L::kItEmpty, n_got, x, abort_flag, p.status);
+        };
+        QItem x, y;
+        bool have = next_one(x);
+        if (have) {
+          do_s(x, 0, 0);
+          before_dp(0, 0);
+          tc_fence_after_sync();
+          if (ok) do_dp(x, 0, 0);
         }
-        __syncwarp();
-      };
-      uint32_t g = 0, n_got = 0, n_item = 0;
-      QItem x, y;
-      bool have = next(n_got, x);
-      if (have) do_s(x, 0, g);
-      if (ok && have) do_dp(x, 0, g);
-      while (ok && have) {
-        const bool more = next(n_got, y);
-        const uint32_t g_next = g + 2 * x.n + 3;
-        // delta is formed: dO and out are read.  Released here, before the next
-        // item's first S: with one key tile the ring cannot take that item's K
-        // until then.
-        if (!warp_wait(bars + L::kDReady + (n_item & 1), (n_item >> 1) & 1, abort_flag, p.status)) break;
-        if (elect_one()) {
+        while (ok && have) {
+          const bool more = next_one(y);
+          const uint32_t g_next = g + 2 * x.n + 3;
+          // delta is formed: dO and out are read.  Released here, before the next
+          // item's first S: with one key tile the ring cannot take that item's K
+          // until then.
+          wait(L::kDReady + (int)(n_item & 1), n_item >> 1);
+          if (!ok) break;
           release(g + 1);
           release(g + 2);
-        }
-        __syncwarp();
-        for (int j = 0; ok && j < x.n; ++j) {
-          if (j + 1 < x.n) do_s(x, j + 1, g);
-          else if (more) do_s(y, 0, g_next);
-          if (!ok) break;
-          // the epilogue has taken the previous item's dQ
-          if (j == 0 && n_item >= 1 &&
-              !warp_wait(bars + L::kOEmpty, (n_item - 1) & 1, abort_flag, p.status)) { ok = false; break; }
-          if (!warp_wait(bars + L::kDSFull, tq & 1, abort_flag, p.status)) { ok = false; break; }
-          ++tq;
-          tc_fence_after_sync();
-          if (elect_one()) {
-            const uint32_t st = (g + 3 + 2 * j) % NST;
+          for (int j = 0; ok && j < x.n; ++j) {
+            const bool last = j + 1 == x.n;
+            if (!last) do_s(x, j + 1, g);
+            else if (more) do_s(y, 0, g_next);
+            // everything that dP will need first, so that it follows dQ at once
+            if (!last) before_dp(j + 1, g);
+            else if (more) before_dp(0, g_next);
+            // the epilogue has taken the previous item's dQ
+            if (j == 0 && n_item >= 1) wait(L::kOEmpty, n_item - 1);
+            wait(L::kDSFull, tq);
+            ++tq;
+            if (!ok) break;
+            tc_fence_after_sync();
             const int keys = x.last - 128 * j;
-            issue_halves<D>(tmem_base + kQDQ, tmem_base + kQDP, sbase + L::kRingOff + st * L::kTile,
-                            keys >= 128 ? 8 : (keys + 15) >> 4, j > 0);
-            umma_commit(bars + L::kEmpty + (int)st);
-            if (j == x.n - 1) umma_commit(bars + L::kOFull);
+            issue_quarters<D>(tmem_base + kQDQ, tmem_base + kQDP, tile(g + 3 + 2 * j),
+                              keys >= 128 ? 8 : (keys + 15) >> 4, j > 0);
+            if (last) umma_commit(bars + L::kOFull);
+            if (!last) do_dp(x, j + 1, g);
+            else if (more) do_dp(y, 0, g_next);
           }
-          __syncwarp();
-          if (j + 1 < x.n) do_dp(x, j + 1, g);
-          else if (more) do_dp(y, 0, g_next);
+          g = g_next;
+          x = y;
+          have = more;
+          ++n_item;
         }
-        g = g_next;
-        x = y;
-        have = more;
-        ++n_item;
       }
+      __syncwarp();
     }
-  } else if (warp < 12) {
-    regs_inc<kRegsSoftmax>();
-    // ===================== p and ds: one thread per query row and 64 keys =====================
-    const int half = (warp - 4) >> 2;
+  } else if (warp < 4 + kSoftmaxWarps) {
+    // ===================== p and ds: one thread per query row and 32 keys =====================
+    const int quarter = (warp - 4) >> 2;
     const int row = (warp & 3) * 32 + lane;
-    const uint32_t t_lane = tmem_base + (uint32_t((warp & 3) * 32) << 16) + 64u * half;
+    const uint32_t t_lane = tmem_base + (uint32_t((warp & 3) * 32) << 16) + 32u * quarter;
     const uint64_t cc = pk2(p.scale_log2, p.scale_log2);
     uint32_t g = 0, n_item = 0, n_got = 0;
+    uint32_t at = 0, last_k = 0;  // ring tiles before the item; the previous key tile's K
     bool ok = true;
     QItem x;
     while (ok && next(n_got, x)) {
@@ -422,22 +407,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < x.n; ++j, ++g) {
         if (!warp_wait(bars + L::kSFull, g & 1, abort_flag, p.status)) { ok = false; break; }
         tc_fence_after_sync();
-        uint32_t v[64];
-        tmem_ld64(t_lane + kQS, v);
+        uint32_t v[32];
+        tmem_ld32(t_lane + kQS, v);
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + L::kSFree);
-        const int rem = limit - 128 * j - 64 * half;
-        const bool masked = __any_sync(0xffffffffu, rem < 64);
+        const int rem = limit - 128 * j - 32 * quarter;
+        const bool masked = __any_sync(0xffffffffu, rem < 32);
         auto probs = [&](auto mask) {
           constexpr bool kMask = decltype(mask)::value;
           if (kMask) {
 #pragma unroll
-            for (int e = 0; e < 64; ++e)
+            for (int e = 0; e < 32; ++e)
               if (e >= rem) v[e] = __float_as_uint(-INFINITY);
           }
 #pragma unroll
-        for (int q = 0; q < 32; ++q) {
+        for (int q = 0; q < 16; ++q) {
           const uint64_t e = ffma2(pk2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1])), cc, nl2);
           float a, b;
           upk2(e, a, b);
@@ -460,39 +445,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!warp_wait(bars + L::kDPFull, g & 1, abort_flag, p.status)) { ok = false; break; }
         tc_fence_after_sync();
-#pragma unroll
-        for (int q0 = 0; q0 < 32; q0 += 16) {
-          uint32_t dp[32];
-          tmem_ld32(t_lane + kQDP + 2 * q0, dp);
-          if (masked) {
-            // p = 0 there, but dP may be infinite
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (2 * q0 + e >= rem) dp[e] = 0u;
-          }
-          uint32_t pk[16];
-#pragma unroll
-          for (int q = 0; q < 16; ++q) {
-            const int e = 2 * (q0 + q);
-            float a, b;
-            upk2(fadd2(pk2(__uint_as_float(dp[2 * q]), __uint_as_float(dp[2 * q + 1])), nd2), a, b);
-            pk[q] = pack_bf16x2(a * __uint_as_float(v[e]), b * __uint_as_float(v[e + 1]));
-          }
-          // the first 32 words lie over columns that this thread has read
-          VSA_TMEM_ST16(t_lane + kQDP + q0, pk, 0);
+        if (warp == 4 && lane == 0) {
+          // dP is complete, and with it the dQ issued before it: their V and K tiles are free
+          mbar_arrive(bars + L::kEmpty + (int)((at + 4 + 2 * j) % NST));
+          if (g > 0) mbar_arrive(bars + L::kEmpty + (int)(last_k % NST));
+          last_k = at + 3 + 2 * j;
         }
+        uint32_t dp[32], pk[16];
+        tmem_ld32(t_lane + kQDP, dp);
+        if (masked) {
+          // p = 0 there, but dP may be infinite
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (e >= rem) dp[e] = 0u;
+        }
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          float a, b;
+          upk2(fadd2(pk2(__uint_as_float(dp[2 * q]), __uint_as_float(dp[2 * q + 1])), nd2), a, b);
+          pk[q] = pack_bf16x2(a * __uint_as_float(v[2 * q]), b * __uint_as_float(v[2 * q + 1]));
+        }
+        // over columns that this thread has read
+        VSA_TMEM_ST16(t_lane + kQDP, pk, 0);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + L::kDSFull);
       }
       ++n_item;
+      at += 2 * x.n + 3;
     }
   } else {
-    regs_dec<kRegsEpilogue>();
     // ===================== operands, delta and results: one thread per query row =====================
-    const int row = (warp - 12) * 32 + lane;
-    const uint32_t t_lane = tmem_base + (uint32_t((warp - 12) * 32) << 16);
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t t_lane = tmem_base + (uint32_t((warp & 3) * 32) << 16);
     uint32_t g = 0, n_item = 0;
     bool ok = true;
     QItem prev = {};
@@ -616,8 +602,8 @@ template <int D>
 struct KLayout {
   static constexpr int DH = D / 64;
   static constexpr uint32_t kTile = 128u * D * 2u;
-  static constexpr int NST = D == 128 ? 4 : 8;  // ring: Q(0), dO(0), Q(1), ...
-  static constexpr int NROW = 4;                // ring of -lse and delta rows
+  static constexpr int NST = D == 128 ? 5 : 10;  // ring: Q(0), dO(0), Q(1), ...
+  static constexpr int NROW = 2;                // ring of -lse and delta rows
   static constexpr uint32_t kKOff = 0, kVOff = kTile;
   static constexpr uint32_t kRingOff = 2 * kTile;
   static constexpr uint32_t kRowOff = kRingOff + NST * kTile;  // [NROW][2][128] f32
@@ -630,7 +616,7 @@ struct KLayout {
                        kDVEmpty = kDKFull + 1, kDKEmpty = kDVEmpty + 1, kItFull = kDKEmpty + 1, kItEmpty = kItFull + kItemSlots,
                        kNumBars = kItEmpty + kItemSlots;
   static constexpr uint32_t kMiscOff = kBarOff + 8u * kNumBars;
-  static constexpr uint32_t kAlloc = kMiscOff + 16u + 1024u;
+  static constexpr uint32_t kAlloc = kMiscOff + 16u;
   static_assert(kAlloc <= 227u * 1024u, "shared memory");
 };
 constexpr uint32_t kKS = 0, kKDP = 128, kKDV = 256, kKDK = 384;
@@ -661,10 +647,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ DenseBwdParams p, const __grid_constant__ DenseSeqs seqs) {
   using L = KLayout<D>;
   constexpr int NST = L::NST, NROW = L::NROW;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
+  if (sbase & 1023u) {  // the tiles' swizzle needs it; there is no room to align by hand
+    set_status(p.status, VSA_ERR_UNSUPPORTED);
+    return;
+  }
   float* rowv = reinterpret_cast<float*>(smem + L::kRowOff);
   ItemRing<KItem>* items = reinterpret_cast<ItemRing<KItem>*>(smem + L::kItemOff);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
@@ -679,8 +667,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < L::kNumBars; ++i) {
       const uint32_t count = (i == L::kDVEmpty || i == L::kDKEmpty) ? 4u
                              : (i == L::kPFull || i == L::kDSFull ||
-                                (i >= L::kRowEmpty && i < L::kRowEmpty + NROW)) ? 8u
-                             : (i >= L::kItEmpty)                              ? 15u  // all warps but one
+                                (i >= L::kRowEmpty && i < L::kRowEmpty + NROW)) ? (uint32_t)kSoftmaxWarps
+                             : (i >= L::kItEmpty)                              ? kThreads / 32 - 1u  // all warps but one
                                                                                : 1u;
       mbar_init(bars + i, count);
     }
@@ -703,7 +691,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp < 4) {
-    regs_dec<kRegsProducer>();
     if (warp == 0) {
       // ===================== Q and dO tiles =====================
       const uint64_t keep = l2_policy_evict_last();
@@ -732,9 +719,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       }
-      if (lane == 0)
-        for (uint32_t t = (g > (uint32_t)NST ? g - NST : 0u); ok && t < g; ++t)
-          ok = mbar_wait(bars + L::kEmpty + (int)(t % NST), (t / NST) & 1, abort_flag, p.status);
       __syncwarp();
     } else if (warp == 2) {
       // ===================== work items, their K and V tiles; keys that no row sees =====================
@@ -826,91 +810,97 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else {
-      // ===================== MMA issue =====================
-      uint32_t g = 0;    // query tiles so far
-      uint32_t n_s = 0;  // items whose first S was issued
-      bool ok = true;
-      auto full = [&](uint32_t at) {
-        const bool r = warp_wait(bars + L::kFull + (int)(at % NST), (at / NST) & 1, abort_flag, p.status);
-        tc_fence_after_sync();
-        return r;
-      };
-      // S of query tile number t (its i-th of item x)
-      auto do_s = [&](const KItem& x, int i, uint32_t t) {
-        if (i == 0) {
-          if (!warp_wait(bars + L::kKFull, n_s & 1, abort_flag, p.status)) { ok = false; return; }
-          ++n_s;
-        }
-        const uint32_t at = 2 * t;
-        if (!full(at)) { ok = false; return; }
-        if (elect_one()) {
-          issue_s<D>(tmem_base + kKS, sbase + L::kKOff, sbase + L::kRingOff + (at % NST) * L::kTile);
+      // ===================== MMA issue: one thread =====================
+      if (elect_one()) {
+        uint32_t g = 0;    // query tiles so far
+        uint32_t n_s = 0, n_dp = 0;  // items whose first S, first dP was prepared
+        uint32_t n_got = 0, n_item = 0;
+        bool ok = true;
+        auto wait = [&](int bar, uint32_t ph) {
+          if (!mbar_wait(bars + bar, ph & 1, abort_flag, p.status)) ok = false;
+        };
+        auto wait_stage = [&](uint32_t at) { wait(L::kFull + (int)(at % NST), at / NST); };
+        auto tile = [&](uint32_t at) { return sbase + L::kRingOff + (at % NST) * L::kTile; };
+        // S of query tile number t and what it waits for (its i-th of item x)
+        auto before_s = [&](int i, uint32_t t) {
+          if (i == 0) wait(L::kKFull, n_s++);
+          wait_stage(2 * t);
+        };
+        auto do_s = [&](const KItem& x, int i, uint32_t t) {
+          issue_s<D>(tmem_base + kKS, sbase + L::kKOff, tile(2 * t));
           umma_commit(bars + L::kSFull);
           if (i == x.n - 1) umma_commit(bars + L::kKEmpty);
-        }
-        __syncwarp();
-      };
-      uint32_t n_got = 0, n_item = 0;
-      KItem x, y;
-      bool have = next(n_got, x);
-      if (have) do_s(x, 0, 0);
-      while (ok && have) {
-        const bool more = next(n_got, y);
-        if (!warp_wait(bars + L::kVFull, n_item & 1, abort_flag, p.status)) break;
-        int t = 0;  // query tile of the head
-        for (int i = 0; ok && i < x.n; ++i, ++g) {
-          const int left = x.q_len - 128 * t;
-          const int steps = left >= 128 ? 8 : (left + 15) >> 4;
-          if (++t == x.tiles) t = 0;
-          const uint32_t st_q = (2 * g) % NST, st_do = (2 * g + 1) % NST;
-          if (!full(2 * g + 1)) { ok = false; break; }
-          if (elect_one()) {
-            issue_s<D>(tmem_base + kKDP, sbase + L::kVOff, sbase + L::kRingOff + st_do * L::kTile);
-            umma_commit(bars + L::kDPFull);
-            if (i == x.n - 1) umma_commit(bars + L::kVEmpty);
-          }
-          __syncwarp();
-          // the epilogue has taken the previous item's dV
-          if (i == 0 && n_item >= 1 &&
-              !warp_wait(bars + L::kDVEmpty, (n_item - 1) & 1, abort_flag, p.status)) { ok = false; break; }
-          if (!warp_wait(bars + L::kPFull, g & 1, abort_flag, p.status)) { ok = false; break; }
+        };
+        auto before_dp = [&](int i, uint32_t t) {
+          if (i == 0) wait(L::kVFull, n_dp++);
+          wait_stage(2 * t + 1);
+        };
+        auto do_dp = [&](const KItem& x, int i, uint32_t t) {
+          issue_s<D>(tmem_base + kKDP, sbase + L::kVOff, tile(2 * t + 1));
+          umma_commit(bars + L::kDPFull);
+          if (i == x.n - 1) umma_commit(bars + L::kVEmpty);
+        };
+        auto next_one = [&](KItem& x) {
+          return get_item_one(items, bars + L::kItFull, bars + L::kItEmpty, n_got, x, abort_flag, p.status);
+        };
+        KItem x, y;
+        bool have = next_one(x);
+        if (have) {
+          before_s(0, 0);
           tc_fence_after_sync();
-          if (elect_one()) {
-            issue_halves<D>(tmem_base + kKDV, tmem_base + kKS, sbase + L::kRingOff + st_do * L::kTile, steps, i > 0);
-            umma_commit(bars + L::kEmpty + (int)st_do);
-            if (i == x.n - 1) umma_commit(bars + L::kDVFull);
-          }
-          __syncwarp();
-          if (i + 1 < x.n) do_s(x, i + 1, g + 1);
-          else if (more) do_s(y, 0, g + 1);
-          if (!ok) break;
-          if (i == 0 && n_item >= 1 &&
-              !warp_wait(bars + L::kDKEmpty, (n_item - 1) & 1, abort_flag, p.status)) { ok = false; break; }
-          if (!warp_wait(bars + L::kDSFull, g & 1, abort_flag, p.status)) { ok = false; break; }
+          if (ok) do_s(x, 0, 0);
+          before_dp(0, 0);
           tc_fence_after_sync();
-          if (elect_one()) {
-            issue_halves<D>(tmem_base + kKDK, tmem_base + kKDP, sbase + L::kRingOff + st_q * L::kTile, steps, i > 0);
-            umma_commit(bars + L::kEmpty + (int)st_q);
-            if (i == x.n - 1) umma_commit(bars + L::kDKFull);
-          }
-          __syncwarp();
+          if (ok) do_dp(x, 0, 0);
         }
-        x = y;
-        have = more;
-        ++n_item;
+        while (ok && have) {
+          const bool more = next_one(y);
+          int t = 0;  // query tile of the head
+          for (int i = 0; ok && i < x.n; ++i, ++g) {
+            const bool last = i + 1 == x.n;
+            const int left = x.q_len - 128 * t;
+            const int steps = left >= 128 ? 8 : (left + 15) >> 4;
+            if (++t == x.tiles) t = 0;
+            // dV, then the next S: everything that S will need first, so that it follows at once
+            if (!last || more) before_s(last ? 0 : i + 1, g + 1);
+            // the epilogue has taken the previous item's dV
+            if (i == 0 && n_item >= 1) wait(L::kDVEmpty, n_item - 1);
+            wait(L::kPFull, g);
+            if (!ok) break;
+            tc_fence_after_sync();
+            issue_quarters<D>(tmem_base + kKDV, tmem_base + kKS, tile(2 * g + 1), steps, i > 0);
+            if (last) umma_commit(bars + L::kDVFull);
+            if (!last) do_s(x, i + 1, g + 1);
+            else if (more) do_s(y, 0, g + 1);
+            // dK, then the next dP
+            if (!last || more) before_dp(last ? 0 : i + 1, g + 1);
+            if (i == 0 && n_item >= 1) wait(L::kDKEmpty, n_item - 1);
+            wait(L::kDSFull, g);
+            if (!ok) break;
+            tc_fence_after_sync();
+            issue_quarters<D>(tmem_base + kKDK, tmem_base + kKDP, tile(2 * g), steps, i > 0);
+            umma_commit(bars + L::kEmpty + (int)((2 * g) % NST));
+            if (last) umma_commit(bars + L::kDKFull);
+            if (!last) do_dp(x, i + 1, g + 1);
+            else if (more) do_dp(y, 0, g + 1);
+          }
+          x = y;
+          have = more;
+          ++n_item;
+        }
       }
+      __syncwarp();
     }
-  } else if (warp < 12) {
-    regs_inc<kRegsSoftmax>();
+  } else if (warp < 4 + kSoftmaxWarps) {
     // ===================== p and ds =====================
-    // A warp has 32 keys (TMEM lanes) and 64 query rows (columns).  -lse and
+    // A warp has 32 keys (TMEM lanes) and 32 query rows (columns).  -lse and
     // delta go with the columns, so they come from shared memory; a thread
-    // that held a key's whole row would read 64 of each, and a warp's reads of
+    // that held one key's part of S would read 32 of each, and a warp's reads of
     // one address cost as much as reads of 32.  In the 16x256b form a thread
     // holds four keys (lane / 4 + 8 k) and the columns 8 i + 2 (lane % 4) + {0, 1}
     // and reads a quarter of that (measured: 1950 -> @A@ cycles for p, 760 -> @B@ for ds).
-    const int half = (warp - 4) >> 2;
-    const uint32_t t_lane = tmem_base + (uint32_t((warp & 3) * 32) << 16) + 64u * half;
+    const int quarter = (warp - 4) >> 2;
+    const uint32_t t_lane = tmem_base + (uint32_t((warp & 3) * 32) << 16) + 32u * quarter;
     constexpr uint32_t kUpper = 16u << 16;  // lanes 16-31 of the warp
     const int row0 = (warp & 3) * 32 + lane / 4, col0 = 2 * (lane & 3);
     const uint64_t cc = pk2(p.scale_log2, p.scale_log2);
@@ -920,35 +910,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && next(n_got, x)) {
       int t = 0;
       for (int i = 0; i < x.n; ++i, ++g) {
-        // column c of this half sees key row r where c >= r - shift
-        const int shift = x.diag + 128 * t + 64 * half;
+        // column c of this quarter sees key row r where c >= r - shift
+        const int shift = x.diag + 128 * t + 32 * quarter;
         if (++t == x.tiles) t = 0;
         const bool masked = p.causal && (warp & 3) * 32 + 31 > shift;
         const int slot = (int)(g % NROW);
-        const float* nl = rowv + slot * 256 + 64 * half + col0;
+        const float* nl = rowv + slot * 256 + 32 * quarter + col0;
         if (!warp_wait(bars + L::kRowFull + slot, (g / NROW) & 1, abort_flag, p.status) ||
             !warp_wait(bars + L::kSFull, g & 1, abort_flag, p.status)) { ok = false; break; }
         tc_fence_after_sync();
-        // v[32 u + 4 i + 2 b + e]: key row0 + 16 u + 8 b, column 8 i + col0 + e
-        uint32_t v[64];
+        // S is complete, and with it the dV issued before it: its dO tile is free
+        if (warp == 4 && lane == 0 && g > 0) mbar_arrive(bars + L::kEmpty + (int)((2 * g - 1) % NST));
+        // v[16 u + 4 i + 2 b + e]: key row0 + 16 u + 8 b, column 8 i + col0 + e
+        uint32_t v[32];
         tmem_ld_16x256(t_lane + kKS, v, 0);
-        tmem_ld_16x256(t_lane + kKS + kUpper, v, 32);
+        tmem_ld_16x256(t_lane + kKS + kUpper, v, 16);
         asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
         const int under = row0 - col0 - shift;  // element (u, i, b, e) is masked where 8 i + e - 16 u - 8 b < under
         auto probs = [&](auto mk) {
           constexpr bool kMask = decltype(mk)::value;
-          uint64_t ll[8];
+          uint64_t ll[4];
 #pragma unroll
-          for (int i8 = 0; i8 < 8; ++i8) {
+          for (int i8 = 0; i8 < 4; ++i8) {
             const float2 l2 = *reinterpret_cast<const float2*>(nl + 8 * i8);
             ll[i8] = pk2(l2.x, l2.y);
           }
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            uint32_t pk[16];
+            uint32_t pk[8];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const int e = 32 * u + 2 * k;
+            for (int k = 0; k < 8; ++k) {
+              const int e = 16 * u + 2 * k;
               float a, b;
               upk2(ffma2(pk2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), cc, ll[k >> 1]), a, b);
               if (kMask) {
@@ -977,26 +969,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bars + L::kPFull);
         if (!warp_wait(bars + L::kDPFull, g & 1, abort_flag, p.status)) { ok = false; break; }
         tc_fence_after_sync();
-        uint64_t dd[8];
+        uint64_t dd[4];
 #pragma unroll
-        for (int i8 = 0; i8 < 8; ++i8) {
+        for (int i8 = 0; i8 < 4; ++i8) {
           const float2 d2 = *reinterpret_cast<const float2*>(nl + 128 + 8 * i8);
           dd[i8] = pk2(d2.x, d2.y);
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          uint32_t dp[32], pk[16];
+          uint32_t dp[16], pk[8];
           tmem_ld_16x256(t_lane + kKDP + u * kUpper, dp, 0);
           asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
           if (masked) {
             // p = 0 there, but dP may be infinite
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
+            for (int k = 0; k < 16; ++k)
               if (8 * (k >> 2) + (k & 1) - 16 * u - 8 * ((k >> 1) & 1) < under) dp[k] = 0u;
           }
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const int e = 32 * u + 2 * k;
+          for (int k = 0; k < 8; ++k) {
+            const int e = 16 * u + 2 * k;
             float a, b;
             upk2(fadd2(pk2(__uint_as_float(dp[2 * k]), __uint_as_float(dp[2 * k + 1])), dd[k >> 1]), a, b);
             pk[k] = pack_bf16x2(a * __uint_as_float(v[e]), b * __uint_as_float(v[e + 1]));
@@ -1013,10 +1005,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    regs_dec<kRegsEpilogue>();
     // ===================== results: one thread per key =====================
-    const int row = (warp - 12) * 32 + lane;
-    const uint32_t t_lane = tmem_base + (uint32_t((warp - 12) * 32) << 16);
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t t_lane = tmem_base + (uint32_t((warp & 3) * 32) << 16);
     uint32_t n_item = 0, n_got = 0;
     KItem x;
     while (next(n_got, x)) {
@@ -1078,9 +1069,9 @@ static int launch_dense_bwd_t(DenseBwdParams p, const CUtensorMap* m, const int4
   static KernelReady ready_q, ready_k;
   auto kq = dense::dense_dq_kernel<D>;
   auto kk = dense::dense_dkv_kernel<D>;
-  int rc = ready_q.check(reinterpret_cast<const void*>(kq), (int)dense::kLaunchRegs, (int)dense::QLayout<D>::kAlloc);
+  int rc = ready_q.check(reinterpret_cast<const void*>(kq), 0, (int)dense::QLayout<D>::kAlloc);
   if (rc == VSA_OK)
-    rc = ready_k.check(reinterpret_cast<const void*>(kk), (int)dense::kLaunchRegs, (int)dense::KLayout<D>::kAlloc);
+    rc = ready_k.check(reinterpret_cast<const void*>(kk), 0, (int)dense::KLayout<D>::kAlloc);
   if (rc != VSA_OK) return rc;
   const int sms = device_sm_count();
   int units[kDenseMaxSeqs];
