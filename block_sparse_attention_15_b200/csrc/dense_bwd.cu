@@ -62,6 +62,12 @@ __device__ __forceinline__ uint32_t sw128(uint32_t row, uint32_t chunk) {
   return row * 128u + ((chunk ^ (row & 7u)) << 4);
 }
 
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // D = A B^T: A [128][D] bf16 in TMEM, B a tile [D / 64][128 rows][128 B].
 template <int D>
 __device__ __forceinline__ void issue_ta(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_base) {
@@ -462,8 +468,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
           float a, b;
-          upk2(fadd2(pk2(__uint_as_float(dp[2 * q]), __uint_as_float(dp[2 * q + 1])), nd2), a, b);
-          pk[q] = pack_bf16x2(a * __uint_as_float(v[2 * q]), b * __uint_as_float(v[2 * q + 1]));
+          upk2(fmul2(fadd2(pk2(__uint_as_float(dp[2 * q]), __uint_as_float(dp[2 * q + 1])), nd2),
+                     pk2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1]))), a, b);
+          pk[q] = pack_bf16x2(a, b);
         }
         // over columns that this thread has read
         VSA_TMEM_ST16(t_lane + kQDP, pk, 0);
@@ -990,8 +997,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 8; ++k) {
             const int e = 16 * u + 2 * k;
             float a, b;
-            upk2(fadd2(pk2(__uint_as_float(dp[2 * k]), __uint_as_float(dp[2 * k + 1])), dd[k >> 1]), a, b);
-            pk[k] = pack_bf16x2(a * __uint_as_float(v[e]), b * __uint_as_float(v[e + 1]));
+            upk2(fmul2(fadd2(pk2(__uint_as_float(dp[2 * k]), __uint_as_float(dp[2 * k + 1])), dd[k >> 1]),
+                       pk2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]))), a, b);
+            pk[k] = pack_bf16x2(a, b);
           }
           tmem_st_16x128(t_lane + kKDP + u * kUpper, pk);
         }
