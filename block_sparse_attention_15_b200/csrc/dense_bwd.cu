@@ -99,19 +99,6 @@ __device__ __forceinline__ void issue_quarters(uint32_t tmem_d, uint32_t tmem_a,
   }
 }
 
-// 16 TMEM lanes x 32 fp32 columns: register 4 i + 2 b + e holds lane
-// threadIdx / 4 + 8 b, column 8 i + 2 (threadIdx % 4) + e.
-template <int N>
-__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, uint32_t (&r)[N], int o) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[o + 0]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]),
-        "=r"(r[o + 6]), "=r"(r[o + 7]), "=r"(r[o + 8]), "=r"(r[o + 9]), "=r"(r[o + 10]), "=r"(r[o + 11]),
-        "=r"(r[o + 12]), "=r"(r[o + 13]), "=r"(r[o + 14]), "=r"(r[o + 15])
-      : "r"(taddr));
-}
-
 // 16 TMEM lanes x 16 columns of 32 bits: register 2 i + b holds lane
 // threadIdx / 4 + 8 b, column 4 i + threadIdx % 4.
 __device__ __forceinline__ void tmem_st_16x128(uint32_t taddr, const uint32_t (&r)[8]) {

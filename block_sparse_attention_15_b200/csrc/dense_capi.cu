@@ -55,14 +55,14 @@ int check_prefix(PrefixParams* p, int B, int Hq, int Hkv, int T, int D, int64_t 
   if (B < 0 || Hq <= 0 || Hkv <= 0 || T < 0 || prefix_len < 0 || suffix_cap < 0) return VSA_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return VSA_ERR_UNSUPPORTED;
   if (Hq % Hkv) return VSA_ERR_SHAPE;
-  // rows, and the key tiles of one key head, are counted in 32 bits
+  // rows, and the key tiles of all key heads, are counted in 32 bits
   const long long per_req = (long long)(Hq / Hkv) * T;
   if (prefix_len > kMaxRows || suffix_cap > kMaxRows || Hq > 65535 || per_req > (1 << 24) ||
       B * per_req > (1 << 28) || (long long)B * Hq * T > (1 << 30))
     return VSA_ERR_UNSUPPORTED;
   const long long tiles = (B * per_req + 255) / 256 * ((prefix_len + 127) / 128) +
                           (long long)B * ((per_req + 255) / 256) * ((suffix_cap + 127) / 128);
-  if (tiles > (1 << 30)) return VSA_ERR_UNSUPPORTED;
+  if (tiles > (1 << 30) / Hkv || (per_req + 15) / 16 > 65535) return VSA_ERR_UNSUPPORTED;
   p->B = B;
   p->Hq = Hq;
   p->Hkv = Hkv;

@@ -103,7 +103,7 @@ struct PrefixParams {
   // filled by prefix_shape
   int group, rows_per_req;          // Hq / Hkv, group * T
   int pfx_blocks, sfx_blocks;       // row blocks of 256 of a prefix / suffix segment
-  int pfx_rows, sfx_rows;           // rows of a slot's partial result
+  int pfx_rows, sfx_rows;           // rows of a partial result
   // workspace
   float *part_p, *part_s, *part_lse_p, *part_lse_s;
   TmaAxes kp_ax, vp_ax, ks_ax, vs_ax;

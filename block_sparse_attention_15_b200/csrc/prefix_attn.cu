@@ -8,12 +8,12 @@
 // key gives 0.
 //
 // How (sm_100a).  The rows of all requests that read a key head, B * G * T of
-// them, are stacked into 128-row tiles against the prefix, so its keys come
-// from HBM once; the G * T rows of one request are a (mostly empty) tile
-// against its suffix.  Both are the forward kernel's products (S = Q K^T, P in
-// TMEM, O += P V); a 128-row tile with few real rows wastes tensor cycles, not
-// time: 1024 cycles per 64 KB of K and V are 2.5 times what HBM feeds an SM.
-// Rows without a query are skipped by the softmax.
+// them, are stacked into row blocks of 256 against the prefix, so its keys come
+// from HBM once (and from L2 for further blocks); the G * T rows of one request
+// are a (mostly empty) block against its suffix.  Both are the forward kernel's
+// products (S = Q K^T, P in TMEM, O += P V); a 128-row tile with few real rows
+// wastes tensor cycles, not time: the two products take 1460 cycles per 64 KB
+// of K and V, for which an SM's share of HBM takes 2600.
 //
 // Work split: all (key head, segment, key tile) triples form one line (a
 // segment is a row block of the prefix, or a request's suffix), cut into equal
@@ -23,10 +23,16 @@
 // line.  A second kernel joins each row's partials.
 // Within a CTA the two slots share the key tiles: with more than 128 rows each
 // slot takes half of the rows, otherwise both have the same rows and take
-// alternate key tiles, two chains of product, softmax, product in flight.
+// alternate key tiles, two chains of product, softmax, product in flight, and
+// their results are joined on the way out.
 //
-// Warp roles as in the forward kernel; Q rows are gathered by the softmax
-// warps themselves (they come from many requests), under the K/V prefetch.
+// 512 threads: warp 0 loads K and V tiles, warp 1 (one thread) issues products,
+// warp 2 zeroes what a segment's last V tile holds past its keys, warp 3 walks
+// the line, warps 4-7 and 8-11 are the slots' softmax (one thread per row; warps
+// without rows pass), warps 12-15 gather the next piece's Q rows and write the
+// last one's results.  Loops are kept short: the first pass through each line of
+// code costs an instruction fetch that waits behind the K/V stream (a softmax
+// unrolled over its 128 columns spent 25 us of a call on that).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -50,6 +56,17 @@ static_assert(128u * (kRegsProducer + 2u * kRegsSoftmax + kRegsEpilogue) <= 512u
               "register split exceeds the launch's registers");
 constexpr float kRefresh = 8.f;
 
+// One CTA's part of one segment.
+struct Piece {
+  int h;          // key head
+  int b;          // request, -1: the prefix
+  int blk;        // row block of 256
+  int tile0, n;   // key tiles
+  int kv_len;     // keys of the segment
+  int rows;       // rows of the block
+  long long part; // partial-result number within its kind
+};
+
 template <int D>
 struct Layout {
   static constexpr int DH = D / 64;
@@ -57,14 +74,16 @@ struct Layout {
   static constexpr int NST = D == 128 ? 5 : 10;
   static constexpr uint32_t kQOff = 0;  // [2]
   static constexpr uint32_t kRingOff = kQOff + 2 * kTile;
-  static constexpr uint32_t kInvLOff = kRingOff + NST * kTile;  // [2][128] f32
-  static constexpr uint32_t kBarOff = kInvLOff + 2u * 128u * 4u;
-  static constexpr int kQFull = 0, kFull = 2, kEmpty = kFull + NST, kPre = kEmpty + NST,
+  static constexpr uint32_t kMLOff = kRingOff + NST * kTile;  // [2 slots][m, l][128] f32
+  static constexpr uint32_t kItemOff = kMLOff + 2048u;
+  static constexpr uint32_t kBarOff = kItemOff + (uint32_t)sizeof(dense::ItemRing<Piece>);
+  // kQFull and kQFree alternate between pieces: one piece may be ahead of a waiter
+  static constexpr int kQFull = 0, kQFree = 2, kFull = 4, kEmpty = kFull + NST, kPre = kEmpty + NST,
                        kSFull = kPre + NST, kPFull = kSFull + 2, kOFull = kPFull + 2,
-                       kOEmpty = kOFull + 2, kLFull = kOEmpty + 2, kNumBars = kLFull + 2;
+                       kOEmpty = kOFull + 2, kLFull = kOEmpty + 2, kItFull = kLFull + 2,
+                       kItEmpty = kItFull + dense::kItemSlots, kNumBars = kItEmpty + dense::kItemSlots;
   static constexpr uint32_t kMiscOff = kBarOff + 8u * kNumBars;
-  static constexpr uint32_t kBytes = kMiscOff + 16u;
-  static constexpr uint32_t kAlloc = kBytes + 1024u;
+  static constexpr uint32_t kAlloc = kMiscOff + 16u;
   static_assert(kAlloc <= 227u * 1024u, "shared memory");
 };
 
@@ -82,9 +101,8 @@ __device__ __forceinline__ int key_tiles(int keys) { return (keys + 127) >> 7; }
 // The line of key tiles (see the header comment).  Whole-warp functions: every
 // lane gets the same answer.
 struct Line {
-  int per_head;     // tiles of one key head
-  long long total;  // tiles of all key heads
-  int ctas;         // CTAs that share them: with fewer tiles than CTAs, the first ones take one each
+  int per_head;    // tiles of one key head
+  int each, more;  // a CTA has `each` tiles, the first `more` CTAs one more
 };
 
 // Tiles of the suffixes of requests [0, b_end).
@@ -99,48 +117,36 @@ __device__ __forceinline__ int suffix_tiles_before(const PrefixParams& p, int b_
 __device__ __forceinline__ Line make_line(const PrefixParams& p, int lane, int grid) {
   Line l;
   l.per_head = p.pfx_blocks * key_tiles(p.prefix_len) + suffix_tiles_before(p, p.B, lane);
-  l.total = (long long)l.per_head * p.Hkv;
-  l.ctas = l.total < grid ? (int)l.total : grid;
+  const int total = l.per_head * p.Hkv;
+  l.each = total / grid;
+  l.more = total - l.each * grid;
   return l;
 }
 
 // CTA whose piece of the line holds tile x.
-__device__ __forceinline__ int cta_of(const Line& l, long long x) {
-  return (int)(((x + 1) * l.ctas + l.total - 1) / l.total) - 1;
+__device__ __forceinline__ int cta_of(const Line& l, int x) {
+  const int first = l.more * (l.each + 1);
+  return x < first ? x / (l.each + 1) : l.more + (x - first) / l.each;
 }
-
-// One CTA's part of one segment.
-struct Piece {
-  int h;          // key head
-  int b;          // request, -1: the prefix
-  int blk;        // row block of 256
-  int tile0, nt;  // key tiles
-  int kv_len;     // keys of the segment
-  int rows;       // rows of the block
-  long long part; // partial-result number within its kind
-};
 
 // The CTA's pieces in order.
 struct Walk {
   const PrefixParams& p;
   Line line;
-  long long at, end;  // tiles [at, end) are still to do
+  int at, end;  // tiles [at, end) are still to do
   int h, b, blk, tile;  // where `at` lies (b = -1: the prefix)
 
   __device__ __forceinline__ Walk(const PrefixParams& pp, int lane) : p(pp) {
     line = make_line(p, lane, gridDim.x);
-    const long long c = blockIdx.x;
-    at = end = 0;
-    if (c < line.ctas) {
-      at = line.total * c / line.ctas;
-      end = line.total * (c + 1) / line.ctas;
-    }
+    const int c = blockIdx.x;
+    at = line.each * c + min(c, line.more);
+    end = at + line.each + (c < line.more ? 1 : 0);
     h = 0;
     b = -1;
     blk = tile = 0;
     if (at >= end) return;
-    h = (int)(at / line.per_head);
-    int r = (int)(at - (long long)h * line.per_head);
+    h = at / line.per_head;
+    int r = at - h * line.per_head;
     const int tp = key_tiles(p.prefix_len);
     if (r < p.pfx_blocks * tp) {
       blk = r / tp;
@@ -195,15 +201,13 @@ struct Walk {
     x.b = b;
     x.blk = blk;
     x.tile0 = tile;
-    const long long left = end - at;
-    const int here = key_tiles(x.kv_len) - tile;
-    x.nt = left < here ? (int)left : here;
+    x.n = min(end - at, key_tiles(x.kv_len) - tile);
     const int rows = b < 0 ? p.B * p.rows_per_req : p.rows_per_req;
     x.rows = min(256, rows - 256 * blk);
     x.part = (b < 0 ? (long long)h * p.pfx_blocks + blk
                     : ((long long)h * p.B + b) * p.sfx_blocks + blk) + blockIdx.x;
-    at += x.nt;
-    tile += x.nt;
+    at += x.n;
+    tile += x.n;
     return true;
   }
 };
@@ -211,7 +215,7 @@ struct Walk {
 // Key tiles of a slot and which they are.
 __device__ __forceinline__ bool split_rows(const Piece& x) { return x.rows > 128; }
 __device__ __forceinline__ int slot_tiles(const Piece& x, int s) {
-  return split_rows(x) ? x.nt : (x.nt + 1 - s) >> 1;
+  return split_rows(x) ? x.n : (x.n + 1 - s) >> 1;
 }
 __device__ __forceinline__ int slot_tile(const Piece& x, int s, int j) {
   return split_rows(x) ? j : 2 * j + s;
@@ -221,24 +225,6 @@ __device__ __forceinline__ int slot_rows(const Piece& x, int s) {
   return split_rows(x) ? min(128, x.rows - 128 * s) : x.rows;
 }
 
-// Row r of the piece's row block: request, head and token.
-struct Row {
-  int b, head, t;
-};
-__device__ __forceinline__ Row find_row(const PrefixParams& p, const Piece& x, int r) {
-  int i = 256 * x.blk + r;
-  Row o;
-  o.b = x.b;
-  if (x.b < 0) {
-    o.b = i / p.rows_per_req;
-    i -= o.b * p.rows_per_req;
-  }
-  const int g = i / p.T;
-  o.head = x.h * p.group + g;
-  o.t = i - g * p.T;
-  return o;
-}
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_kp, const __grid_constant__ CUtensorMap tm_vp,
@@ -246,11 +232,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ PrefixParams p) {
   using L = Layout<D>;
   constexpr int NST = L::NST;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
-  float* inv_l = reinterpret_cast<float*>(smem + L::kInvLOff);
+  if (sbase & 1023u) {  // the tiles' swizzle needs it; there is no room to align by hand
+    set_status(p.status, VSA_ERR_UNSUPPORTED);
+    return;
+  }
+  // the joining kernel may be set up while this one runs
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  float* ml = reinterpret_cast<float*>(smem + L::kMLOff);
+  dense::ItemRing<Piece>* items = reinterpret_cast<dense::ItemRing<Piece>*>(smem + L::kItemOff);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
@@ -260,8 +251,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < L::kNumBars; ++i) {
-      const bool four = i < L::kFull || (i >= L::kPFull && i < L::kPFull + 2) || i >= L::kOEmpty;
-      mbar_init(bars + i, four ? 4u : 1u);
+      const uint32_t count = (i < L::kQFree || (i >= L::kPFull && i < L::kPFull + 2) ||
+                              (i >= L::kOEmpty && i < L::kItFull)) ? 4u
+                             : i >= L::kItEmpty                     ? 15u  // all warps but one
+                                                                    : 1u;
+      mbar_init(bars + i, count);
     }
     *abort_flag = 0;
     mbar_fence_init();
@@ -277,24 +271,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
+  auto next = [&](uint32_t& w, Piece& x) {
+    return dense::get_item(items, bars + L::kItFull, bars + L::kItEmpty, w, x, lane, abort_flag, p.status);
+  };
 
   if (warp < 4) {
     regs_dec<kRegsProducer>();
     if (warp == 0) {
       // ===================== K and V tiles =====================
-      if (blockIdx.x == 0)
-        for (int b = lane; b < p.B; b += 32)
-          if (p.lens[b] < 0 || p.lens[b] > p.suffix_cap) set_status(p.status, VSA_ERR_INDEX_RANGE);
       const uint64_t pol_p = l2_policy_evict_last(), pol_s = l2_policy_evict_first();
-      Walk walk(p, lane);
       Piece x;
-      uint32_t g = 0;
+      uint32_t g = 0, n_got = 0;
       bool ok = true;
-      while (ok && walk.next(x)) {
+      while (ok && next(n_got, x)) {
         if (lane == 0) {
           const bool own = x.b >= 0;
           const int b = own ? x.b : 0;
-          for (int j = 0; ok && j < 2 * x.nt; ++j, ++g) {
+          for (int j = 0; ok && j < 2 * x.n; ++j, ++g) {
             const int st = (int)(g % NST);
             const uint32_t u = g / NST;
             if (u >= 1) ok = mbar_wait(bars + L::kEmpty + st, (u - 1) & 1, abort_flag, p.status);
@@ -311,21 +304,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               dense::load_rows(dst + dh * 16384, map, ax, full, dh * 64, key, x.h, b, own ? pol_s : pol_p);
           }
         }
-        g = __shfl_sync(0xffffffffu, g, 0);
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       }
-      if (lane == 0)
-        for (uint32_t t = (g > (uint32_t)NST ? g - NST : 0u); ok && t < g; ++t)
-          ok = mbar_wait(bars + L::kEmpty + (int)(t % NST), (t / NST) & 1, abort_flag, p.status);
       __syncwarp();
     } else if (warp == 2) {
       // ============ zero V rows past a segment's keys (what a cache holds there) ============
-      Walk walk(p, lane);
       Piece x;
-      uint32_t g = 0, pre = 0;
-      while (walk.next(x)) {
-        g += 2 * x.nt;
-        const int len = x.kv_len - 128 * (x.tile0 + x.nt - 1);
+      uint32_t g = 0, pre = 0, n_got = 0;
+      while (next(n_got, x)) {
+        g += 2 * x.n;
+        const int len = x.kv_len - 128 * (x.tile0 + x.n - 1);
         if (len >= 128) continue;
         const int st = (int)((g - 1) % NST);
         if (!warp_wait(bars + L::kPre + st, (pre >> st) & 1, abort_flag, p.status)) break;
@@ -335,66 +323,100 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + L::kFull + st);
       }
-    } else if (warp == 1) {
-      // ===================== MMA issue =====================
-      uint32_t cs[2] = {0, 0};  // pieces of the slot that have started
-      uint32_t gs[2] = {0, 0};  // key tiles of the slot whose P has been consumed
-      uint32_t g = 0;
-      bool ok = true;
-      auto do_s = [&](const Piece& x, int s, int j, uint32_t g_piece) {
-        const int tile = slot_tile(x, s, j);
-        const uint32_t gk = g_piece + 2 * tile;
-        const int st = (int)(gk % NST);
-        if (j == 0) {
-          if (!warp_wait(bars + L::kQFull + s, cs[s] & 1, abort_flag, p.status)) { ok = false; return; }
-          ++cs[s];
-        }
-        if (!warp_wait(bars + L::kFull + st, (gk / NST) & 1, abort_flag, p.status)) { ok = false; return; }
-        tc_fence_after_sync();
-        if (elect_one()) {
-          issue_s<D>(tmem_base + 128u * s, sbase + L::kQOff + s * L::kTile, sbase + L::kRingOff + st * L::kTile);
-          umma_commit(bars + L::kSFull + s);
-          if (s == 1 || !split_rows(x)) umma_commit(bars + L::kEmpty + st);
-        }
-        __syncwarp();
-      };
+    } else if (warp == 3) {
+      // ===================== the line =====================
+      if (blockIdx.x == 0)
+        for (int b = lane; b < p.B; b += 32)
+          if (p.lens[b] < 0 || p.lens[b] > p.suffix_cap) set_status(p.status, VSA_ERR_INDEX_RANGE);
       Walk walk(p, lane);
       Piece x;
-      while (ok && walk.next(x)) {
-        const int n0 = slot_tiles(x, 0), n1 = slot_tiles(x, 1);
-        do_s(x, 0, 0, g);
-        if (ok && n1 > 0) do_s(x, 1, 0, g);
-        for (int j = 0; ok && j < n0; ++j) {
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const int ns = s ? n1 : n0;
-            if (!ok || j >= ns) continue;
-            const int tile = slot_tile(x, s, j);
-            const uint32_t gv = g + 2 * tile + 1;
-            const int st = (int)(gv % NST);
-            if (j == 0 && cs[s] >= 2 &&
-                !warp_wait(bars + L::kOEmpty + s, (cs[s] - 2) & 1, abort_flag, p.status)) { ok = false; continue; }
-            if (!warp_wait(bars + L::kFull + st, (gv / NST) & 1, abort_flag, p.status)) { ok = false; continue; }
-            if (!warp_wait(bars + L::kPFull + s, gs[s] & 1, abort_flag, p.status)) { ok = false; continue; }
-            ++gs[s];
-            tc_fence_after_sync();
-            if (elect_one()) {
+      uint32_t n = 0;
+      bool ok = true;
+      while (ok && walk.next(x))
+        ok = dense::put_item(items, bars + L::kItFull, bars + L::kItEmpty, n++, x, lane, abort_flag, p.status);
+      x.n = -1;
+      if (ok) dense::put_item(items, bars + L::kItFull, bars + L::kItEmpty, n, x, lane, abort_flag, p.status);
+    } else {
+      // ===================== MMA issue: one thread =====================
+      if (elect_one()) {
+        uint32_t cs[2] = {0, 0};  // pieces of the slot that have started
+        uint32_t gs[2] = {0, 0};  // key tiles of the slot whose P has been consumed
+        uint32_t g = 0, n_got = 0, n_q = 0;
+        bool ok = true;
+        auto wait = [&](int bar, uint32_t ph) {
+          if (!mbar_wait(bars + bar, ph & 1, abort_flag, p.status)) ok = false;
+        };
+        // S(j) of slot s of the piece numbered n, whose ring tiles start at gx
+        auto do_s = [&](const Piece& x, uint32_t n, int s, int j, uint32_t gx) {
+          const int tile = slot_tile(x, s, j);
+          const bool split = split_rows(x);
+          const uint32_t gk = gx + 2 * tile;
+          if (j == 0) {
+            if (n_q == n) {  // the piece's first product
+              wait(L::kQFull + (int)(n & 1), n >> 1);
+              ++n_q;
+            }
+            ++cs[s];
+          }
+          wait(L::kFull + (int)(gk % NST), gk / NST);
+          if (!ok) return;
+          tc_fence_after_sync();
+          issue_s<D>(tmem_base + 128u * s, sbase + L::kQOff + (split ? s : (int)(n & 1)) * L::kTile,
+                     sbase + L::kRingOff + (gk % NST) * L::kTile);
+          umma_commit(bars + L::kSFull + s);
+          if (s == 1 || !split) umma_commit(bars + L::kEmpty + (int)(gk % NST));
+          if (tile == x.n - 1 && (s == 1 || !split)) umma_commit(bars + L::kQFree + (int)(n & 1));  // the piece's last S
+        };
+        Piece x, y;
+        auto next_one = [&](Piece& z) {
+          return dense::get_item_one(items, bars + L::kItFull, bars + L::kItEmpty, n_got, z, abort_flag, p.status);
+        };
+        bool have = next_one(x);
+        uint32_t n = 0;
+        if (have) {
+          do_s(x, 0, 0, 0, 0);
+          if (ok && slot_tiles(x, 1) > 0) do_s(x, 0, 1, 0, 0);
+        }
+        while (ok && have) {
+          const bool more = next_one(y);
+          const uint32_t g_next = g + 2 * x.n;
+          const int n0 = slot_tiles(x, 0), n1 = slot_tiles(x, 1);
+          for (int j = 0; ok && j < n0; ++j) {
+#pragma unroll 1
+            for (int s = 0; s < 2; ++s) {
+              const int ns = s ? n1 : n0;
+              if (!ok || j >= ns) continue;
+              const int tile = slot_tile(x, s, j);
+              const uint32_t gv = g + 2 * tile + 1;
+              const int st = (int)(gv % NST);
+              wait(L::kFull + st, gv / NST);
+              // the epilogue has emptied this slot's O
+              if (j == 0 && cs[s] >= 2) wait(L::kOEmpty + s, cs[s] - 2);
+              wait(L::kPFull + s, gs[s]);
+              ++gs[s];
+              if (!ok) continue;
+              tc_fence_after_sync();
               const int keys = x.kv_len - 128 * (x.tile0 + tile);
               issue_pv<D>(tmem_base + kTmemO + D * s, tmem_base + 128u * s,
                           sbase + L::kRingOff + st * L::kTile, keys >= 128 ? 8 : (keys + 15) >> 4, j > 0);
               if (s == 1 || !split_rows(x)) umma_commit(bars + L::kEmpty + st);
               if (j == ns - 1) umma_commit(bars + L::kOFull + s);
+              if (j + 1 < ns) do_s(x, n, s, j + 1, g);
+              else if (s == 0 && more) do_s(y, n + 1, 0, 0, g_next);
             }
-            __syncwarp();
-            if (j + 1 < ns) do_s(x, s, j + 1, g);
           }
+          if (ok && more && slot_tiles(y, 1) > 0) do_s(y, n + 1, 1, 0, g_next);
+          g = g_next;
+          x = y;
+          have = more;
+          ++n;
         }
-        g += 2 * x.nt;
       }
+      __syncwarp();
     }
   } else if (warp < 12) {
     regs_inc<kRegsSoftmax>();
-    // ===================== Q gather and softmax: one thread per row =====================
+    // ===================== softmax: one thread per row =====================
     const int s = (warp - 4) >> 2;
     const int wq = warp & 3;
     const int row = wq * 32 + lane;
@@ -402,66 +424,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t_o = tmem_base + (uint32_t(wq * 32) << 16) + kTmemO + D * s;
     const float c = p.scale_log2;
     const uint64_t cc = pk2(c, c);
-    uint8_t* qt = smem + L::kQOff + s * L::kTile;
-    uint32_t g = 0, n = 0;
+    uint32_t g = 0, n = 0, n_got = 0;
     bool ok = true;
-    Walk walk(p, lane);
     Piece x;
-    while (ok && walk.next(x)) {
+    while (ok && next(n_got, x)) {
       const int nt = slot_tiles(x, s);
-      const int rows = slot_rows(x, s);
-      const int first = split_rows(x) ? 128 * s : 0;  // the slot's first row in the block
-      float* lse_out = (x.b < 0 ? p.part_lse_p + x.part * (2 * p.pfx_rows) + s * p.pfx_rows
-                                : p.part_lse_s + x.part * (2 * p.sfx_rows) + s * p.sfx_rows);
-      if (nt == 0) {
-        // a piece of one key tile leaves slot 1 nothing
-        if (row < rows) lse_out[row] = -INFINITY;
-        continue;
-      }
-      // The slot's score products up to here are complete (their results were
-      // waited for), so its Q tile may be overwritten.  Each warp fetches its
-      // own 32 rows: 16-byte chunks, consecutive lanes along a row, into the
-      // 128-byte swizzle.  Rows past the block keep what the tile held; only
-      // their own (unused) results depend on it.
-      constexpr int CH = D / 8;
-      const int my_rows = min(32, max(0, rows - 32 * wq));
-#pragma unroll 8
-      for (int i = lane; i < my_rows * CH; i += 32) {
-        const int r = 32 * wq + i / CH, ch = i % CH;
-        const Row o = find_row(p, x, first + r);
-        const uint4 v = *reinterpret_cast<const uint4*>(p.q + o.b * p.q_st.b + o.head * p.q_st.h +
-                                                        (long long)o.t * p.q_st.s + ch * 8);
-        *reinterpret_cast<uint4*>(qt + (ch >> 3) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + L::kQFull + s);
-      const bool any = 32 * wq < rows;  // this warp has rows
-      int limit = x.kv_len;             // keys the row sees
-      if (x.b >= 0 && row < rows) limit = x.kv_len - p.T + 1 + find_row(p, x, first + row).t;
+      if (nt == 0) continue;  // a piece of one key tile leaves slot 1 nothing
+      const bool any = 32 * wq < slot_rows(x, s);  // this warp has rows
+      int limit = x.kv_len;                        // keys the row sees
+      if (x.b >= 0) limit += 1 - p.T + (256 * x.blk + (split_rows(x) ? 128 * s : 0) + row) % p.T;
       float m = -INFINITY;
       uint64_t l2 = pk2(0.f, 0.f);
       for (int j = 0; j < nt; ++j, ++g) {
         if (!warp_wait(bars + L::kSFull + s, g & 1, abort_flag, p.status)) { ok = false; break; }
         tc_fence_after_sync();
         if (any) {
-          uint32_t v[128];
-#pragma unroll
-          for (int q = 0; q < 8; ++q) VSA_TMEM_LD16(t_s + 16u * q, v, 16 * q);
-          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-          const int rem = limit - 128 * (x.tile0 + slot_tile(x, s, j));
+          const int rem = min(limit, x.kv_len) - 128 * (x.tile0 + slot_tile(x, s, j));
           const bool masked = __any_sync(0xffffffffu, rem < 128);
-          if (masked) {
-#pragma unroll
-            for (int q = 0; q < 128; ++q)
-              if (q >= rem) v[q] = __float_as_uint(-INFINITY);
-          }
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int q0 = 0; q0 < 128; q0 += 32) {
+            uint32_t v[32];
+            tmem_ld32(t_s + q0, v);
+            if (masked) {
 #pragma unroll
-          for (int q = 0; q < 128; q += 8) {
+              for (int q = 0; q < 32; ++q)
+                if (q >= rem - q0) v[q] = __float_as_uint(-INFINITY);
+            }
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mx[e] = fmax3(mx[e], __uint_as_float(v[q + 2 * e]), __uint_as_float(v[q + 2 * e + 1]));
+            for (int q = 0; q < 32; q += 8) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                mx[e] = fmax3(mx[e], __uint_as_float(v[q + 2 * e]), __uint_as_float(v[q + 2 * e + 1]));
+            }
           }
           const float top = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c;
           const bool move = top > m + kRefresh;
@@ -474,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (j > 0) {
               // PV(j - 1) is complete: the thread that issued S(j) issued it before
               const float a = move ? alpha : 1.f;
-#pragma unroll
+#pragma unroll 1
               for (int q0 = 0; q0 < D; q0 += 16) {
                 uint32_t ov[16];
                 VSA_TMEM_LD16(t_o + q0, ov, 0);
@@ -488,19 +483,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float ref = (m == -INFINITY) ? 0.f : -m;
           const uint64_t nm2 = pk2(ref, ref);
+          // P's 16 columns of 32 bits lie over columns of S that were read before
+#pragma unroll 1
+          for (int q0 = 0; q0 < 128; q0 += 32) {
+            uint32_t v[32], pk[16];
+            tmem_ld32(t_s + q0, v);
+            if (masked) {
 #pragma unroll
-          for (int q0 = 0; q0 < 64; q0 += 16) {
-            uint32_t pk[16];
+              for (int q = 0; q < 32; ++q)
+                if (q >= rem - q0) v[q] = __float_as_uint(-INFINITY);
+            }
 #pragma unroll
             for (int q = 0; q < 16; ++q) {
-              const int e = 2 * (q0 + q);
               float a, b;
-              upk2(ffma2(pk2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), cc, nm2), a, b);
+              upk2(ffma2(pk2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1])), cc, nm2), a, b);
               const float p0 = fast_exp2(a), p1 = fast_exp2(b);
               l2 = fadd2(l2, pk2(p0, p1));
               pk[q] = pack_bf16x2(p0, p1);
             }
-            VSA_TMEM_ST16(t_s + q0, pk, 0);
+            VSA_TMEM_ST16(t_s + q0 / 2, pk, 0);
           }
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         }
@@ -509,57 +510,151 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bars + L::kPFull + s);
       }
       if (!ok) break;
+      // the epilogue has read the slot's previous maxima and sums
       if (n >= 1 && !warp_wait(bars + L::kOEmpty + s, (n - 1) & 1, abort_flag, p.status)) { ok = false; break; }
       ++n;
       float la, lb;
       upk2(l2, la, lb);
-      const float l = la + lb;
-      inv_l[s * 128 + row] = l == 0.f ? 0.f : 1.f / l;
-      if (row < rows) lse_out[row] = l == 0.f ? -INFINITY : m + __log2f(l);
+      ml[s * 256 + row] = m;
+      ml[s * 256 + 128 + row] = la + lb;
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + L::kLFull + s);
     }
   } else {
     regs_dec<kRegsEpilogue>();
-    // ===================== epilogue: partial rows in fp32 =====================
+    // ===================== Q rows in, partial rows out (fp32) =====================
     const int wq = warp - 12;
-    const int row = wq * 32 + lane;
     const uint32_t t_lane = tmem_base + (uint32_t(wq * 32) << 16) + kTmemO;
     uint32_t cs[2] = {0, 0};
+    uint32_t n_got = 0, freed = 0;  // pieces whose Q tiles are known to be free
     bool ok = true;
-    Walk walk(p, lane);
-    Piece x;
-    while (ok && walk.next(x)) {
+    // Rows of piece x (number n) into its Q tile or tiles: 16-byte chunks,
+    // consecutive lanes along a row, into the 128-byte swizzle.  Rows past the
+    // block keep what the tile held; only their own (unused) results depend on it.
+    auto gather = [&](const Piece& x, uint32_t n, bool after_split) {
+      const bool split = split_rows(x);
+      // the tile's last reader: the piece before the previous one, or, where either
+      // of this and the previous piece has both tiles, the previous one
+      const uint32_t need = n == 0 ? 0u : (split || after_split) ? n : n - 1;
+      for (; freed < need; ++freed)
+        if (!warp_wait(bars + L::kQFree + (int)(freed & 1), (freed >> 1) & 1, abort_flag, p.status)) return false;
+      constexpr int CH = D / 8, RPI = 32 / CH;  // chunks of a row, rows per access of the warp
+      for (int r0 = 32 * wq; r0 < x.rows; r0 += 128) {
+        // this lane's row
+        int i = 256 * x.blk + r0 + lane, b = x.b;
+        if (b < 0) {
+          b = i / p.rows_per_req;
+          i -= b * p.rows_per_req;
+        }
+        const int gi = i / p.T;
+        const long long off = b * p.q_st.b + (long long)(x.h * p.group + gi) * p.q_st.h + (long long)(i - gi * p.T) * p.q_st.s;
+        uint8_t* qt = smem + L::kQOff + (split ? r0 >> 7 : (int)(n & 1)) * L::kTile;
+        const int rows = min(32, x.rows - r0), ch = lane % CH;
+#pragma unroll 4
+        for (int r = 0; r < rows; r += RPI) {
+          const int mine = r + lane / CH;
+          const long long from = __shfl_sync(0xffffffffu, off, mine & 31);
+          if (mine < rows) {
+            const int at = (r0 & 127) + mine;
+            const uint4 v = *reinterpret_cast<const uint4*>(p.q + from + ch * 8);
+            *reinterpret_cast<uint4*>(qt + (ch >> 3) * 16384 + at * 128 + (((ch & 7) ^ (at & 7)) << 4)) = v;
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + L::kQFull + (int)(n & 1));
+      return true;
+    };
+    Piece x, y;
+    uint32_t n = 0;
+    bool have = next(n_got, x);
+    if (have) ok = gather(x, 0, false);
+    while (ok && have) {
+      const bool more = next(n_got, y);
+      if (more && !gather(y, n + 1, split_rows(x))) break;
+      const bool split = split_rows(x);
+      const bool two = slot_tiles(x, 1) > 0;
 #pragma unroll 1
-      for (int s = 0; s < 2; ++s) {
-        if (slot_tiles(x, s) == 0) continue;
-        const uint32_t ph = cs[s] & 1;
-        ++cs[s];
-        if (!warp_wait(bars + L::kLFull + s, ph, abort_flag, p.status) ||
-            !warp_wait(bars + L::kOFull + s, ph, abort_flag, p.status)) { ok = false; break; }
+      for (int s = 0; ok && s < 2; ++s) {
+        if (s == 0 || two) {
+          ok = warp_wait(bars + L::kLFull + s, cs[s] & 1, abort_flag, p.status) &&
+               warp_wait(bars + L::kOFull + s, cs[s] & 1, abort_flag, p.status);
+          if (!ok) break;
+          ++cs[s];
+        }
+        if (!split && s == 0) continue;  // both slots are written together
         tc_fence_after_sync();
         const int rows = slot_rows(x, s);
         if (32 * wq < rows) {
-          const float il = inv_l[s * 128 + row];
-          float* o = (x.b < 0 ? p.part_p + (x.part * (2 * p.pfx_rows) + s * p.pfx_rows + row) * D
-                              : p.part_s + (x.part * (2 * p.sfx_rows) + s * p.sfx_rows + row) * D);
+          // weights of the slots' sums for this lane's row: split, one slot at a
+          // time; else both together
+          const int s0 = split ? s : 0;
+          const bool both = !split && two;
+          float w0 = 1.f, w1 = 0.f;
+          const int row = 32 * wq + lane;
+          const float m0 = ml[s0 * 256 + row], l0 = ml[s0 * 256 + 128 + row];
+          float top = m0, sum = l0;
+          if (both) {
+            const float m1 = ml[256 + row], l1 = ml[384 + row];
+            top = fmaxf(m0, m1);
+            const float ref = top == -INFINITY ? 0.f : top;
+            w0 = fast_exp2(m0 - ref);
+            w1 = fast_exp2(m1 - ref);
+            sum = l0 * w0 + l1 * w1;
+          }
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          w0 *= inv;
+          w1 *= inv;
+          const int first = split ? 128 * s : 0;
+          const long long at = x.part * (x.b < 0 ? p.pfx_rows : p.sfx_rows) + first;
+          if (row < rows) (x.b < 0 ? p.part_lse_p : p.part_lse_s)[at + row] = sum == 0.f ? -INFINITY : top + __log2f(sum);
+          float* o = (x.b < 0 ? p.part_p : p.part_s) + at * D;
+          // four lanes to a row's 32 bytes
+#pragma unroll 1
+          for (int u = 0; u < 2; ++u) {
+            float a0[2], a1[2];
 #pragma unroll
-          for (int q0 = 0; q0 < D; q0 += 32) {
-            uint32_t ov[32];
-            tmem_ld32(t_lane + D * s + q0, ov);
-            if (row < rows) {
+            for (int b = 0; b < 2; ++b) {
+              a0[b] = __shfl_sync(0xffffffffu, w0, 16 * u + 8 * b + lane / 4);
+              a1[b] = __shfl_sync(0xffffffffu, w1, 16 * u + 8 * b + lane / 4);
+            }
+            if (32 * wq + 16 * u >= rows) break;
+            const uint32_t t_u = t_lane + ((uint32_t)(16 * u) << 16) + D * s0;
+#pragma unroll 1
+            for (int q0 = 0; q0 < D; q0 += 32) {
+              uint32_t va[16], vb[16];
+              dense::tmem_ld_16x256(t_u + q0, va, 0);
+              if (both) dense::tmem_ld_16x256(t_u + D + q0, vb, 0);
+              asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<float4*>(o + q0 + e) =
-                    make_float4(__uint_as_float(ov[e]) * il, __uint_as_float(ov[e + 1]) * il,
-                                __uint_as_float(ov[e + 2]) * il, __uint_as_float(ov[e + 3]) * il);
+              for (int k = 0; k < 8; ++k) {
+                const int b = k & 1, r = 32 * wq + 16 * u + 8 * b + lane / 4;
+                float2 f = make_float2(__uint_as_float(va[2 * k]) * a0[b], __uint_as_float(va[2 * k + 1]) * a0[b]);
+                if (both) {
+                  f.x = fmaf(__uint_as_float(vb[2 * k]), a1[b], f.x);
+                  f.y = fmaf(__uint_as_float(vb[2 * k + 1]), a1[b], f.y);
+                }
+                if (r < rows)
+                  *reinterpret_cast<float2*>(o + (long long)r * D + q0 + 8 * (k >> 1) + 2 * (lane & 3)) = f;
+              }
             }
           }
         }
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bars + L::kOEmpty + s);
+        if (lane == 0) {
+          if (!split) {
+            mbar_arrive(bars + L::kOEmpty);
+            if (two) mbar_arrive(bars + L::kOEmpty + 1);
+          } else {
+            mbar_arrive(bars + L::kOEmpty + s);
+          }
+        }
       }
+      x = y;
+      have = more;
+      ++n;
     }
   }
 
@@ -572,85 +667,76 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins a row's partials: weights 2^(lse_i - max), fp32.  One block per row,
-// its warps taking partials in turn.
-constexpr int kJoinWarps = 4;
+// Joins the rows' partials: weights 2^(lse_i - max), fp32, in the order of the
+// line.  A block has up to kJoinRows rows of one request and key head, a warp
+// one row at a time.
+constexpr int kJoinWarps = 4, kJoinRows = 16;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps)
     prefix_join_kernel(const __grid_constant__ PrefixParams p, int grid) {
   constexpr int E = D / 32;  // elements per lane
-  __shared__ float sm_m[kJoinWarps], sm_l[kJoinWarps];
-  __shared__ float sm_o[kJoinWarps][D];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int row = blockIdx.x % p.rows_per_req;  // (head of the group, token)
-  const int bh = blockIdx.x / p.rows_per_req;
-  const int h = bh % p.Hkv, b = bh / p.Hkv;
+  const int h = blockIdx.x % p.Hkv, b = blockIdx.x / p.Hkv;
   const Line line = make_line(p, lane, grid);
-  float m = -INFINITY, l = 0.f, o[E] = {};
-  // partials [first, first + count), `copies` rows each `pitch` apart
-  auto take = [&](const float* part, const float* lse, long long first, int count, int rows, int slot0,
-                  int copies, int r) {
-    for (int i = warp; i < count * copies; i += kJoinWarps) {
-      const long long at = (first + i / copies) * (2 * rows) + (slot0 + i % copies) * rows + r;
-      const float x = lse[at];
-      if (x == -INFINITY) continue;
-      const float nm = fmaxf(m, x);
-      const float a = fast_exp2(m - nm), w = fast_exp2(x - nm);
-      m = nm;
-      l = l * a + w;
-      const float* src = part + at * D + lane * E;
+  const int tp = key_tiles(p.prefix_len), tb = key_tiles(suffix_len(p, b));
+  const int before = suffix_tiles_before(p, b, lane);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial results are there
+  const int row_end = min(p.rows_per_req, (int)(blockIdx.y + 1) * kJoinRows);
+  for (int row = blockIdx.y * kJoinRows + warp; row < row_end; row += kJoinWarps) {
+    float m = -INFINITY, l = 0.f, o[E] = {};
+#pragma unroll 1
+    for (int kind = 0; kind < 2; ++kind) {
+      // the segment's tiles, its first partial and the row in it
+      const int tiles = kind ? tb : tp;
+      if (tiles == 0) continue;
+      const int r = kind ? row : b * p.rows_per_req + row;
+      const int blk = r >> 8;
+      const int t0 = h * line.per_head + (kind ? p.pfx_blocks * tp + before : 0) + blk * tiles;
+      const int c0 = cta_of(line, t0), count = cta_of(line, t0 + tiles - 1) - c0 + 1;
+      const long long seg = kind ? ((long long)h * p.B + b) * p.sfx_blocks + blk : (long long)h * p.pfx_blocks + blk;
+      const int rows = kind ? p.sfx_rows : p.pfx_rows;
+      const long long first = (seg + c0) * rows + (r & 255);
+      const float* lse = kind ? p.part_lse_s : p.part_lse_p;
+      const float* part = (kind ? p.part_s : p.part_p) + lane * E;
+      for (int i0 = 0; i0 < count; i0 += 32) {
+        const float mine = i0 + lane < count ? lse[first + (long long)(i0 + lane) * rows] : -INFINITY;
+        float top = mine;
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = o[e] * a + w * src[e];
+        for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+        if (top == -INFINITY) continue;
+        const float nm = fmaxf(m, top), a = fast_exp2(m - nm);
+        m = nm;
+        l *= a;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] *= a;
+        const int here = min(32, count - i0);
+#pragma unroll 4
+        for (int i = 0; i < here; ++i) {
+          const float x = __shfl_sync(0xffffffffu, mine, i);
+          const float w = fast_exp2(x - nm);
+          const float* src = part + (first + (long long)(i0 + i) * rows) * D;
+          float v[E];
+          if (E == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
+          else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+          l += w;
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] = fmaf(w, v[e], o[e]);
+        }
+      }
     }
-  };
-  const int tp = key_tiles(p.prefix_len);
-  if (tp > 0) {
-    const int gr = b * p.rows_per_req + row, blk = gr >> 8, r = gr & 255;
-    const bool split = min(256, p.B * p.rows_per_req - 256 * blk) > 128;
-    const long long t0 = (long long)h * line.per_head + (long long)blk * tp;
-    const int c0 = cta_of(line, t0), c1 = cta_of(line, t0 + tp - 1);
-    take(p.part_p, p.part_lse_p, (long long)h * p.pfx_blocks + blk + c0, c1 - c0 + 1, p.pfx_rows,
-         split ? r >> 7 : 0, split ? 1 : 2, split ? r & 127 : r);
-  }
-  const int tb = key_tiles(suffix_len(p, b));
-  if (tb > 0) {
-    const int blk = row >> 8, r = row & 255;
-    const bool split = min(256, p.rows_per_req - 256 * blk) > 128;
-    const long long t0 = (long long)h * line.per_head + (long long)p.pfx_blocks * tp +
-                         suffix_tiles_before(p, b, lane) + (long long)blk * tb;
-    const int c0 = cta_of(line, t0), c1 = cta_of(line, t0 + tb - 1);
-    take(p.part_s, p.part_lse_s, ((long long)h * p.B + b) * p.sfx_blocks + blk + c0, c1 - c0 + 1,
-         p.sfx_rows, split ? r >> 7 : 0, split ? 1 : 2, split ? r & 127 : r);
-  }
-  if (lane == 0) {
-    sm_m[warp] = m;
-    sm_l[warp] = l;
-  }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int g = row / p.T, t = row - g * p.T;
+    const int head = h * p.group + g;
+    __nv_bfloat16* out = p.out + b * p.out_st.b + head * p.out_st.h + (long long)t * p.out_st.s + lane * E;
+    uint32_t pk[E / 2];
 #pragma unroll
-  for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = o[e];
-  __syncthreads();
-  float top = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kJoinWarps; ++i) top = fmaxf(top, sm_m[i]);
-  float sum = 0.f, w[kJoinWarps];
-#pragma unroll
-  for (int i = 0; i < kJoinWarps; ++i) {
-    w[i] = sm_m[i] == -INFINITY ? 0.f : fast_exp2(sm_m[i] - top);
-    sum += sm_l[i] * w[i];
+    for (int e = 0; e < E / 2; ++e) pk[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+    if (E == 4) *reinterpret_cast<uint2*>(out) = make_uint2(pk[0], pk[1]);
+    else *reinterpret_cast<uint32_t*>(out) = pk[0];
+    if (p.lse && lane == 0)
+      p.lse[((long long)b * p.Hq + head) * p.T + t] =
+          l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int g = row / p.T, t = row - g * p.T;
-  const int head = h * p.group + g;
-  __nv_bfloat16* out = p.out + b * p.out_st.b + head * p.out_st.h + (long long)t * p.out_st.s;
-  for (int d = threadIdx.x; d < D; d += 32 * kJoinWarps) {
-    float v = 0.f;
-#pragma unroll
-    for (int i = 0; i < kJoinWarps; ++i) v += w[i] * sm_o[i][d];
-    out[d] = __float2bfloat16(v * inv);
-  }
-  if (p.lse && threadIdx.x == 0)
-    p.lse[((long long)b * p.Hq + head) * p.T + t] =
-        sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994531f;
 }
 
 }  // namespace prefix
@@ -664,13 +750,13 @@ void prefix_shape(PrefixParams* p) {
   const int all = p->B * p->rows_per_req;
   p->pfx_blocks = (all + 255) / 256;
   p->sfx_blocks = (p->rows_per_req + 255) / 256;
-  p->pfx_rows = all < 128 ? all : 128;
-  p->sfx_rows = p->rows_per_req < 128 ? p->rows_per_req : 128;
+  p->pfx_rows = all < 256 ? all : 256;
+  p->sfx_rows = p->rows_per_req < 256 ? p->rows_per_req : 256;
 }
 
-// Partial results of each kind: segments + CTAs, two slots of rows each.
+// Partial results of each kind: segments + CTAs, of a block's rows each.
 static size_t parts_of(long long segments, int rows) {
-  return (size_t)(segments + kPrefixGrid) * 2 * rows;
+  return (size_t)(segments + kPrefixGrid) * rows;
 }
 static size_t a256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -705,8 +791,18 @@ static int launch_prefix_t(const PrefixParams& p, const CUtensorMap* m, cudaStre
                                             (long long)p.B * p.sfx_blocks * ((p.suffix_cap + 127LL) / 128));
   const int grid = cap < kPrefixGrid ? (int)(cap > 0 ? cap : 1) : kPrefixGrid;
   kern<<<grid, prefix::kThreads, L::kAlloc, stream>>>(m[0], m[1], m[2], m[3], p);
-  prefix::prefix_join_kernel<D><<<(unsigned)(p.B * p.Hkv * p.rows_per_req), 32 * prefix::kJoinWarps, 0, stream>>>(p, grid);
-  return cudaGetLastError() == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
+  if (cudaGetLastError() != cudaSuccess) return VSA_ERR_CUDA;
+  // set up while the attention kernel runs; waits for it before it reads partial results
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.B * p.Hkv), (unsigned)((p.rows_per_req + prefix::kJoinRows - 1) / prefix::kJoinRows));
+  cfg.blockDim = dim3(32 * prefix::kJoinWarps);
+  cfg.stream = stream;
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prefix::prefix_join_kernel<D>, p, grid) == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
 }
 
 int launch_prefix(const PrefixParams& p_in, const PrefixTensors& t, int D, cudaStream_t stream) {
