@@ -136,14 +136,15 @@ struct Walk {
   int at, end;  // tiles [at, end) are still to do
   int h, b, blk, tile;  // where `at` lies (b = -1: the prefix)
 
-  __device__ __forceinline__ Walk(const PrefixParams& pp, int lane) : p(pp) {
+  // (only the warp that walks looks anything up)
+  __device__ __forceinline__ Walk(const PrefixParams& pp, int lane, bool mine) : p(pp) {
+    at = end = h = blk = tile = 0;
+    b = -1;
+    if (!mine) return;
     line = make_line(p, lane, gridDim.x);
     const int c = blockIdx.x;
     at = line.each * c + min(c, line.more);
     end = at + line.each + (c < line.more ? 1 : 0);
-    h = 0;
-    b = -1;
-    blk = tile = 0;
     if (at >= end) return;
     h = at / line.per_head;
     int r = at - h * line.per_head;
@@ -249,6 +250,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x;
   const int warp = tid / 32, lane = tid % 32;
 
+  // the line needs the lengths from memory: first of all
+  Walk walk(p, lane, warp == 3);
+
   if (tid == 0) {
     for (int i = 0; i < L::kNumBars; ++i) {
       const uint32_t count = (i < L::kQFree || (i >= L::kPFull && i < L::kPFull + 2) ||
@@ -328,7 +332,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (blockIdx.x == 0)
         for (int b = lane; b < p.B; b += 32)
           if (p.lens[b] < 0 || p.lens[b] > p.suffix_cap) set_status(p.status, VSA_ERR_INDEX_RANGE);
-      Walk walk(p, lane);
       Piece x;
       uint32_t n = 0;
       bool ok = true;
@@ -554,13 +557,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int r = 0; r < rows; r += RPI) {
           const int mine = r + lane / CH;
           const long long from = __shfl_sync(0xffffffffu, off, mine & 31);
-          if (mine < rows) {
-            const int at = (r0 & 127) + mine;
-            const uint4 v = *reinterpret_cast<const uint4*>(p.q + from + ch * 8);
-            *reinterpret_cast<uint4*>(qt + (ch >> 3) * 16384 + at * 128 + (((ch & 7) ^ (at & 7)) << 4)) = v;
-          }
+          const int at = (r0 & 127) + mine;
+          // all rows in flight at once, none of them in registers
+          if (mine < rows)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                             smem_u32(qt + (ch >> 3) * 16384 + at * 128 + (((ch & 7) ^ (at & 7)) << 4))),
+                         "l"(p.q + from + ch * 8)
+                         : "memory");
         }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + L::kQFull + (int)(n & 1));
@@ -610,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const long long at = x.part * (x.b < 0 ? p.pfx_rows : p.sfx_rows) + first;
           if (row < rows) (x.b < 0 ? p.part_lse_p : p.part_lse_s)[at + row] = sum == 0.f ? -INFINITY : top + __log2f(sum);
           float* o = (x.b < 0 ? p.part_p : p.part_s) + at * D;
-          // four lanes to a row's 32 bytes
+          // four lanes to a row's 64 bytes
 #pragma unroll 1
           for (int u = 0; u < 2; ++u) {
             float a0[2], a1[2];
@@ -629,14 +635,25 @@ __global__ void __launch_bounds__(kThreads, 1)
               asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
-                const int b = k & 1, r = 32 * wq + 16 * u + 8 * b + lane / 4;
-                float2 f = make_float2(__uint_as_float(va[2 * k]) * a0[b], __uint_as_float(va[2 * k + 1]) * a0[b]);
+                float2 f = make_float2(__uint_as_float(va[2 * k]) * a0[k & 1], __uint_as_float(va[2 * k + 1]) * a0[k & 1]);
                 if (both) {
-                  f.x = fmaf(__uint_as_float(vb[2 * k]), a1[b], f.x);
-                  f.y = fmaf(__uint_as_float(vb[2 * k + 1]), a1[b], f.y);
+                  f.x = fmaf(__uint_as_float(vb[2 * k]), a1[k & 1], f.x);
+                  f.y = fmaf(__uint_as_float(vb[2 * k + 1]), a1[k & 1], f.y);
                 }
+                va[2 * k] = __float_as_uint(f.x);
+                va[2 * k + 1] = __float_as_uint(f.y);
+              }
+              // pairs of lanes exchange halves of two column groups: 16 bytes each
+              const bool odd = lane & 1;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int b = k & 1, lo = 8 * (k >> 1) + 2 * b, hi = lo + 4;  // registers of groups 2 (k / 2), + 1
+                const int r = 32 * wq + 16 * u + 8 * b + lane / 4;
+                const uint32_t sx = odd ? va[lo] : va[hi], sy = odd ? va[lo + 1] : va[hi + 1];
+                const uint32_t rx = __shfl_xor_sync(0xffffffffu, sx, 1), ry = __shfl_xor_sync(0xffffffffu, sy, 1);
+                const uint4 f = odd ? make_uint4(rx, ry, va[hi], va[hi + 1]) : make_uint4(va[lo], va[lo + 1], rx, ry);
                 if (r < rows)
-                  *reinterpret_cast<float2*>(o + (long long)r * D + q0 + 8 * (k >> 1) + 2 * (lane & 3)) = f;
+                  *reinterpret_cast<uint4*>(o + (long long)r * D + q0 + 16 * (k >> 1) + (odd ? 8 : 0) + 2 * (lane & 2)) = f;
               }
             }
           }
@@ -668,9 +685,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the rows' partials: weights 2^(lse_i - max), fp32, in the order of the
-// line.  A block has up to kJoinRows rows of one request and key head, a warp
-// one row at a time.
-constexpr int kJoinWarps = 4, kJoinRows = 16;
+// line.  A block has kJoinRows rows of one request and key head, one per warp.
+constexpr int kJoinWarps = 4, kJoinRows = 4;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps)
     prefix_join_kernel(const __grid_constant__ PrefixParams p, int grid) {
