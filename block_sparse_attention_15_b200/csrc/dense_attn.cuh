@@ -12,6 +12,29 @@
 namespace vsa {
 namespace dense {
 
+// The waits of vsa_device.cuh with their polling out of line: a kernel waits in
+// dozens of places, and with the polling inlined its code (90-115 KB) did not
+// stay in the instruction caches.  (A kernel that moves registers between its
+// warpgroups cannot call functions and keeps the inlined form.)
+namespace slim {
+static __device__ __noinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                              int* status) {
+  return vsa::mbar_wait(bar, parity, abort_flag, status);
+}
+static __device__ __noinline__ bool warp_poll(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                              int* status) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = vsa::mbar_wait(bar, parity, abort_flag, status) ? 1 : 0;
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  return mbar_try_wait(bar, parity) || mbar_poll(bar, parity, abort_flag, status);
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || warp_poll(bar, parity, abort_flag, status);
+}
+}  // namespace slim
+
 // Work item i of a launch: one tile unit of one sequence.  Sequences are sorted
 // by their unit counts n_0 >= n_1 >= ..., and units are taken by descending
 // rank t (unit t of a causal sequence costs about t + 1 key tiles), every
@@ -57,7 +80,7 @@ template <typename Item>
 __device__ __forceinline__ bool put_item(ItemRing<Item>* ring, uint64_t* full, uint64_t* empty, uint32_t w,
                                          const Item& x, int lane, volatile int* abort_flag, int* status) {
   const int slot = (int)(w % kItemSlots);
-  if (w >= (uint32_t)kItemSlots && !warp_wait(empty + slot, (w / kItemSlots - 1) & 1, abort_flag, status))
+  if (w >= (uint32_t)kItemSlots && !slim::warp_wait(empty + slot, (w / kItemSlots - 1) & 1, abort_flag, status))
     return false;
   if (lane == 0) {
     ring->item[slot] = x;
@@ -72,7 +95,7 @@ template <typename Item>
 __device__ __forceinline__ bool get_item(const ItemRing<Item>* ring, uint64_t* full, uint64_t* empty, uint32_t& w,
                                          Item& x, int lane, volatile int* abort_flag, int* status) {
   const int slot = (int)(w % kItemSlots);
-  if (!warp_wait(full + slot, (w / kItemSlots) & 1, abort_flag, status)) return false;
+  if (!slim::warp_wait(full + slot, (w / kItemSlots) & 1, abort_flag, status)) return false;
   x = ring->item[slot];
   __syncwarp();
   if (lane == 0) mbar_arrive(empty + slot);
@@ -85,7 +108,7 @@ template <typename Item>
 __device__ __forceinline__ bool get_item_one(const ItemRing<Item>* ring, uint64_t* full, uint64_t* empty,
                                              uint32_t& w, Item& x, volatile int* abort_flag, int* status) {
   const int slot = (int)(w % kItemSlots);
-  if (!mbar_wait(full + slot, (w / kItemSlots) & 1, abort_flag, status)) return false;
+  if (!slim::mbar_wait(full + slot, (w / kItemSlots) & 1, abort_flag, status)) return false;
   x = ring->item[slot];
   mbar_arrive(empty + slot);
   ++w;

@@ -50,6 +50,9 @@ namespace vsa {
 namespace dense {
 namespace {
 
+using slim::mbar_wait;
+using slim::warp_wait;
+
 constexpr int kThreads = 768;
 constexpr int kSoftmaxWarps = 16;
 constexpr uint32_t kTmemCols = 512;

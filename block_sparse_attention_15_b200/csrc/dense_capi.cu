@@ -62,7 +62,7 @@ int check_prefix(PrefixParams* p, int B, int Hq, int Hkv, int T, int D, int64_t 
     return VSA_ERR_UNSUPPORTED;
   const long long tiles = (B * per_req + 255) / 256 * ((prefix_len + 127) / 128) +
                           (long long)B * ((per_req + 255) / 256) * ((suffix_cap + 127) / 128);
-  if (tiles > (1 << 30) / Hkv || (per_req + 3) / 4 > 65535) return VSA_ERR_UNSUPPORTED;
+  if (tiles > (1 << 29) / Hkv || (per_req + 3) / 4 > 65535) return VSA_ERR_UNSUPPORTED;
   p->B = B;
   p->Hq = Hq;
   p->Hkv = Hkv;

@@ -46,14 +46,10 @@
 namespace vsa {
 namespace prefix {
 
-using dense::issue_pv;
-using dense::issue_s;
+using dense::slim::mbar_wait;
+using dense::slim::warp_wait;
 
 constexpr int kThreads = 512;
-constexpr uint32_t kRegsProducer = 80, kRegsSoftmax = 184, kRegsEpilogue = 64;
-constexpr uint32_t kLaunchRegs = 128;
-static_assert(128u * (kRegsProducer + 2u * kRegsSoftmax + kRegsEpilogue) <= 512u * kLaunchRegs,
-              "register split exceeds the launch's registers");
 constexpr float kRefresh = 8.f;
 
 // One CTA's part of one segment.
@@ -64,6 +60,7 @@ struct Piece {
   int tile0, n;   // key tiles
   int kv_len;     // keys of the segment
   int rows;       // rows of the block
+  int turn;       // slot that takes the first tile (of a block of up to 128 rows)
   long long part; // partial-result number within its kind
 };
 
@@ -98,32 +95,55 @@ __device__ __forceinline__ int suffix_len(const PrefixParams& p, int b) {
 
 __device__ __forceinline__ int key_tiles(int keys) { return (keys + 127) >> 7; }
 
-// The line of key tiles (see the header comment).  Whole-warp functions: every
-// lane gets the same answer.
+// The line of key tiles (see the header comment), measured in units: a tile of a
+// block of more than 128 rows costs both slots a pass (3700 cycles against 1950
+// measured) and counts 2, others 1.  A tile belongs to the CTA that holds its
+// first unit.  With fewer than two units to a CTA every tile counts 1: a CTA
+// must not fall between the two units of a tile, where it would leave no partial
+// result.  Whole-warp functions: every lane gets the same answer.
 struct Line {
-  int per_head;    // tiles of one key head
-  int each, more;  // a CTA has `each` tiles, the first `more` CTAs one more
+  int heavy;       // units of a tile of a block of more than 128 rows
+  int pfx, sfx;    // units of one key tile over all row blocks of a prefix / suffix segment
+  int per_head;    // units of one key head
+  int each, more;  // a CTA has `each` units, the first `more` CTAs one more
 };
 
-// Tiles of the suffixes of requests [0, b_end).
+// Sum of the key tiles of requests [0, b_end).
 __device__ __forceinline__ int suffix_tiles_before(const PrefixParams& p, int b_end, int lane) {
   int sum = 0;
   for (int b = lane; b < b_end; b += 32) sum += key_tiles(suffix_len(p, b));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return sum * p.sfx_blocks;
+  return sum;
+}
+
+// Units of a tile of row block `blk` of a segment of `rows` rows, and of a tile
+// over all its blocks.
+__device__ __forceinline__ int tile_units(const Line& l, int rows, int blk) {
+  return rows - 256 * blk > 128 ? l.heavy : 1;
+}
+__device__ __forceinline__ int all_units(const Line& l, int rows, int blocks) {
+  return (blocks - 1) * l.heavy + tile_units(l, rows, blocks - 1);
 }
 
 __device__ __forceinline__ Line make_line(const PrefixParams& p, int lane, int grid) {
   Line l;
-  l.per_head = p.pfx_blocks * key_tiles(p.prefix_len) + suffix_tiles_before(p, p.B, lane);
-  const int total = l.per_head * p.Hkv;
+  const int tp = key_tiles(p.prefix_len), ts = suffix_tiles_before(p, p.B, lane);
+  int total = 0;
+#pragma unroll 1
+  for (l.heavy = 2;; l.heavy = 1) {
+    l.pfx = all_units(l, p.B * p.rows_per_req, p.pfx_blocks);
+    l.sfx = all_units(l, p.rows_per_req, p.sfx_blocks);
+    l.per_head = l.pfx * tp + l.sfx * ts;
+    total = l.per_head * p.Hkv;
+    if (l.heavy == 1 || total >= 2 * grid) break;
+  }
   l.each = total / grid;
   l.more = total - l.each * grid;
   return l;
 }
 
-// CTA whose piece of the line holds tile x.
+// CTA whose piece of the line holds unit x.
 __device__ __forceinline__ int cta_of(const Line& l, int x) {
   const int first = l.more * (l.each + 1);
   return x < first ? x / (l.each + 1) : l.more + (x - first) / l.each;
@@ -133,12 +153,13 @@ __device__ __forceinline__ int cta_of(const Line& l, int x) {
 struct Walk {
   const PrefixParams& p;
   Line line;
-  int at, end;  // tiles [at, end) are still to do
-  int h, b, blk, tile;  // where `at` lies (b = -1: the prefix)
+  int at, end;          // the next tile's first unit; the CTA's units end here
+  int h, b, blk, tile;  // the next tile (b = -1: the prefix)
+  int turn;             // slot whose turn it is
 
   // (only the warp that walks looks anything up)
   __device__ __forceinline__ Walk(const PrefixParams& pp, int lane, bool mine) : p(pp) {
-    at = end = h = blk = tile = 0;
+    at = end = h = blk = tile = turn = 0;
     b = -1;
     if (!mine) return;
     line = make_line(p, lane, gridDim.x);
@@ -148,41 +169,43 @@ struct Walk {
     if (at >= end) return;
     h = at / line.per_head;
     int r = at - h * line.per_head;
-    const int tp = key_tiles(p.prefix_len);
-    if (r < p.pfx_blocks * tp) {
-      blk = r / tp;
-      tile = r - blk * tp;
-      return;
-    }
-    r -= p.pfx_blocks * tp;
-    // the request whose suffix holds tile r: 32 requests at a time
-    for (int b0 = 0;; b0 += 32) {
-      const int mine = b0 + lane < p.B ? key_tiles(suffix_len(p, b0 + lane)) * p.sfx_blocks : 0;
-      int sum = mine;
+    int tiles = key_tiles(p.prefix_len), rows = p.B * p.rows_per_req, blocks = p.pfx_blocks;
+    if (r >= line.pfx * tiles) {
+      r -= line.pfx * tiles;
+      // the request whose suffix holds unit r: 32 requests at a time
+      for (int b0 = 0;; b0 += 32) {
+        const int mine_u = b0 + lane < p.B ? key_tiles(suffix_len(p, b0 + lane)) * line.sfx : 0;
+        int sum = mine_u;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += v;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += v;
+        }
+        const int all = __shfl_sync(0xffffffffu, sum, 31);
+        if (r >= all && b0 + 32 < p.B) {
+          r -= all;
+          continue;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, sum > r);
+        const int i = past ? __ffs(past) - 1 : 31;
+        r -= __shfl_sync(0xffffffffu, sum - mine_u, i);
+        b = b0 + i;
+        break;
       }
-      const int all = __shfl_sync(0xffffffffu, sum, 31);
-      if (r >= all && b0 + 32 < p.B) {
-        r -= all;
-        continue;
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, sum > r);
-      const int i = past ? __ffs(past) - 1 : 31;
-      r -= __shfl_sync(0xffffffffu, sum - mine, i);
-      b = b0 + i;
-      break;
+      tiles = max(1, key_tiles(suffix_len(p, b)));
+      rows = p.rows_per_req;
+      blocks = p.sfx_blocks;
     }
-    const int tb = max(1, key_tiles(suffix_len(p, b)));
-    blk = r / tb;
-    tile = r - blk * tb;
+    blk = min(r / (line.heavy * tiles), blocks - 1);
+    r -= blk * line.heavy * tiles;
+    const int w = tile_units(line, rows, blk);
+    tile = (r + w - 1) / w;  // a tile that began before `at` is the previous CTA's
+    at += tile * w - r;
   }
 
   __device__ __forceinline__ bool next(Piece& x) {
     if (at >= end) return false;
-    // step over what holds no tile
+    // step over what holds no (further) tile
     for (;;) {
       const int len = b < 0 ? p.prefix_len : suffix_len(p, b);
       const int blocks = b < 0 ? p.pfx_blocks : p.sfx_blocks;
@@ -198,16 +221,21 @@ struct Walk {
         if (++h >= p.Hkv) return false;  // not reached while at < end
       }
     }
+    const int rows = b < 0 ? p.B * p.rows_per_req : p.rows_per_req;
+    const int w = tile_units(line, rows, blk);
     x.h = h;
     x.b = b;
     x.blk = blk;
     x.tile0 = tile;
-    x.n = min(end - at, key_tiles(x.kv_len) - tile);
-    const int rows = b < 0 ? p.B * p.rows_per_req : p.rows_per_req;
+    x.n = min((end - at + w - 1) / w, key_tiles(x.kv_len) - tile);
     x.rows = min(256, rows - 256 * blk);
     x.part = (b < 0 ? (long long)h * p.pfx_blocks + blk
                     : ((long long)h * p.B + b) * p.sfx_blocks + blk) + blockIdx.x;
-    at += x.n;
+    // short pieces take turns, so that one slot's product, softmax, product
+    // runs under the other's
+    x.turn = x.rows > 128 ? 0 : turn;
+    turn ^= x.n & 1;
+    at += x.n * w;
     tile += x.n;
     return true;
   }
@@ -216,14 +244,69 @@ struct Walk {
 // Key tiles of a slot and which they are.
 __device__ __forceinline__ bool split_rows(const Piece& x) { return x.rows > 128; }
 __device__ __forceinline__ int slot_tiles(const Piece& x, int s) {
-  return split_rows(x) ? x.n : (x.n + 1 - s) >> 1;
+  return split_rows(x) ? x.n : (x.n + 1 - (s ^ x.turn)) >> 1;
 }
 __device__ __forceinline__ int slot_tile(const Piece& x, int s, int j) {
-  return split_rows(x) ? j : 2 * j + s;
+  return split_rows(x) ? j : 2 * j + (s ^ x.turn);
 }
 // Real rows of a slot.
 __device__ __forceinline__ int slot_rows(const Piece& x, int s) {
   return split_rows(x) ? min(128, x.rows - 128 * s) : x.rows;
+}
+
+// The products, out of line: they are issued from several places.
+template <int D>
+static __device__ __noinline__ void s_product(uint32_t tmem_d, uint32_t q_base, uint32_t k_base) {
+  dense::issue_s<D>(tmem_d, q_base, k_base);
+}
+template <int D>
+static __device__ __noinline__ void pv_product(uint32_t tmem_o, uint32_t tmem_p, uint32_t v_base, int steps,
+                                               bool accumulate) {
+  dense::issue_pv<D>(tmem_o, tmem_p, v_base, steps, accumulate);
+}
+
+// This warp's rows of a partial result: O (or both slots' O, D columns apart)
+// from TMEM times the row's weight, which lane r has for the warp's row r.  Four
+// lanes write 64 bytes of a row.
+template <int D>
+static __device__ __noinline__ void write_part(float* o, int rows, int wq, int lane, uint32_t t_o, bool both,
+                                           float w0, float w1) {
+#pragma unroll 1
+  for (int u = 0; u < 2; ++u) {
+    if (32 * wq + 16 * u >= rows) break;
+    float a0[2], a1[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      a0[b] = __shfl_sync(0xffffffffu, w0, 16 * u + 8 * b + lane / 4);
+      a1[b] = __shfl_sync(0xffffffffu, w1, 16 * u + 8 * b + lane / 4);
+    }
+    const uint32_t t_u = t_o + ((uint32_t)(16 * u) << 16);
+#pragma unroll 1
+    for (int q0 = 0; q0 < D; q0 += 32) {
+      uint32_t va[16], vb[16];
+      dense::tmem_ld_16x256(t_u + q0, va, 0);
+      if (both) dense::tmem_ld_16x256(t_u + D + q0, vb, 0);
+      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        float f = __uint_as_float(va[k]) * a0[(k >> 1) & 1];
+        if (both) f = fmaf(__uint_as_float(vb[k]), a1[(k >> 1) & 1], f);
+        va[k] = __float_as_uint(f);
+      }
+      // pairs of lanes exchange halves of two column groups: 16 bytes each
+      const bool odd = lane & 1;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int b = k & 1, lo = 8 * (k >> 1) + 2 * b, hi = lo + 4;  // registers of groups 2 (k / 2), + 1
+        const int r = 32 * wq + 16 * u + 8 * b + lane / 4;
+        const uint32_t sx = odd ? va[lo] : va[hi], sy = odd ? va[lo + 1] : va[hi + 1];
+        const uint32_t rx = __shfl_xor_sync(0xffffffffu, sx, 1), ry = __shfl_xor_sync(0xffffffffu, sy, 1);
+        const uint4 f = odd ? make_uint4(rx, ry, va[hi], va[hi + 1]) : make_uint4(va[lo], va[lo + 1], rx, ry);
+        if (r < rows)
+          *reinterpret_cast<uint4*>(o + (long long)r * D + q0 + 16 * (k >> 1) + (odd ? 8 : 0) + 2 * (lane & 2)) = f;
+      }
+    }
+  }
 }
 
 template <int D>
@@ -256,9 +339,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < L::kNumBars; ++i) {
       const uint32_t count = (i < L::kQFree || (i >= L::kPFull && i < L::kPFull + 2) ||
-                              (i >= L::kOEmpty && i < L::kItFull)) ? 4u
-                             : i >= L::kItEmpty                     ? 15u  // all warps but one
-                                                                    : 1u;
+                              (i >= L::kLFull && i < L::kItFull))     ? 4u
+                             : (i >= L::kOEmpty && i < L::kLFull)      ? 8u
+                             : i >= L::kItEmpty                        ? 15u  // all warps but one
+                                                                       : 1u;
       mbar_init(bars + i, count);
     }
     *abort_flag = 0;
@@ -280,7 +364,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp < 4) {
-    regs_dec<kRegsProducer>();
     if (warp == 0) {
       // ===================== K and V tiles =====================
       const uint64_t pol_p = l2_policy_evict_last(), pol_s = l2_policy_evict_first();
@@ -342,8 +425,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       // ===================== MMA issue: one thread =====================
       if (elect_one()) {
-        uint32_t cs[2] = {0, 0};  // pieces of the slot that have started
-        uint32_t gs[2] = {0, 0};  // key tiles of the slot whose P has been consumed
+        // per slot: pieces whose products are issued, key tiles whose P has been
+        // consumed.  (Scalars: an array indexed by the slot would live in memory.)
+        uint32_t done0 = 0, done1 = 0, gs0 = 0, gs1 = 0;
         uint32_t g = 0, n_got = 0, n_q = 0;
         bool ok = true;
         auto wait = [&](int bar, uint32_t ph) {
@@ -354,17 +438,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int tile = slot_tile(x, s, j);
           const bool split = split_rows(x);
           const uint32_t gk = gx + 2 * tile;
-          if (j == 0) {
-            if (n_q == n) {  // the piece's first product
-              wait(L::kQFull + (int)(n & 1), n >> 1);
-              ++n_q;
-            }
-            ++cs[s];
+          if (n_q == n) {  // the piece's first product
+            wait(L::kQFull + (int)(n & 1), n >> 1);
+            ++n_q;
           }
           wait(L::kFull + (int)(gk % NST), gk / NST);
           if (!ok) return;
           tc_fence_after_sync();
-          issue_s<D>(tmem_base + 128u * s, sbase + L::kQOff + (split ? s : (int)(n & 1)) * L::kTile,
+          s_product<D>(tmem_base + 128u * s, sbase + L::kQOff + (split ? s : (int)(n & 1)) * L::kTile,
                      sbase + L::kRingOff + (gk % NST) * L::kTile);
           umma_commit(bars + L::kSFull + s);
           if (s == 1 || !split) umma_commit(bars + L::kEmpty + (int)(gk % NST));
@@ -376,39 +457,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         bool have = next_one(x);
         uint32_t n = 0;
-        if (have) {
-          do_s(x, 0, 0, 0, 0);
-          if (ok && slot_tiles(x, 1) > 0) do_s(x, 0, 1, 0, 0);
-        }
+        // the first S of slots 0, 1
+        auto begin = [&](const Piece& z, uint32_t nz, int s, uint32_t gz) {
+          if (ok && slot_tiles(z, s) > 0) do_s(z, nz, s, 0, gz);
+        };
+        // in the order of their tiles
+        if (have) begin(x, 0, x.turn, 0);
+        if (have) begin(x, 0, x.turn ^ 1, 0);
         while (ok && have) {
           const bool more = next_one(y);
           const uint32_t g_next = g + 2 * x.n;
-          const int n0 = slot_tiles(x, 0), n1 = slot_tiles(x, 1);
-          for (int j = 0; ok && j < n0; ++j) {
-#pragma unroll 1
-            for (int s = 0; s < 2; ++s) {
-              const int ns = s ? n1 : n0;
-              if (!ok || j >= ns) continue;
-              const int tile = slot_tile(x, s, j);
-              const uint32_t gv = g + 2 * tile + 1;
-              const int st = (int)(gv % NST);
-              wait(L::kFull + st, gv / NST);
-              // the epilogue has emptied this slot's O
-              if (j == 0 && cs[s] >= 2) wait(L::kOEmpty + s, cs[s] - 2);
-              wait(L::kPFull + s, gs[s]);
-              ++gs[s];
-              if (!ok) continue;
-              tc_fence_after_sync();
-              const int keys = x.kv_len - 128 * (x.tile0 + tile);
-              issue_pv<D>(tmem_base + kTmemO + D * s, tmem_base + 128u * s,
-                          sbase + L::kRingOff + st * L::kTile, keys >= 128 ? 8 : (keys + 15) >> 4, j > 0);
-              if (s == 1 || !split_rows(x)) umma_commit(bars + L::kEmpty + st);
-              if (j == ns - 1) umma_commit(bars + L::kOFull + s);
-              if (j + 1 < ns) do_s(x, n, s, j + 1, g);
-              else if (s == 0 && more) do_s(y, n + 1, 0, 0, g_next);
+          // a slot that is through with its tiles (or has none) goes on with the next
+          // piece; where both slots read the same tiles, together and slot 0 first
+          // (slot 1 releases the tile)
+          const bool early = more && !split_rows(y);
+          if (early && !split_rows(x) && x.n == 1) begin(y, n + 1, x.turn ^ 1, g_next);
+          for (int i = 0; ok && i < x.n * (split_rows(x) ? 2 : 1); ++i) {
+            // the slots in turn
+            const int s = (i & 1) ^ x.turn, j = i >> 1, ns = slot_tiles(x, s);
+            const int tile = slot_tile(x, s, j);
+            const uint32_t gv = g + 2 * tile + 1;
+            const int st = (int)(gv % NST);
+            wait(L::kFull + st, gv / NST);
+            // the epilogue has emptied this slot's O
+            const uint32_t done = s ? done1 : done0;
+            if (j == 0 && done >= 1) wait(L::kOEmpty + s, done - 1);
+            wait(L::kPFull + s, s ? gs1 : gs0);
+            gs0 += s ^ 1;
+            gs1 += s;
+            if (!ok) break;
+            tc_fence_after_sync();
+            const int keys = x.kv_len - 128 * (x.tile0 + tile);
+            pv_product<D>(tmem_base + kTmemO + D * s, tmem_base + 128u * s,
+                        sbase + L::kRingOff + st * L::kTile, keys >= 128 ? 8 : (keys + 15) >> 4, j > 0);
+            if (s == 1 || !split_rows(x)) umma_commit(bars + L::kEmpty + st);
+            if (j + 1 < ns) {
+              do_s(x, n, s, j + 1, g);
+            } else {
+              umma_commit(bars + L::kOFull + s);
+              done0 += s ^ 1;
+              done1 += s;
+              if (early) begin(y, n + 1, s, g_next);
             }
           }
-          if (ok && more && slot_tiles(y, 1) > 0) do_s(y, n + 1, 1, 0, g_next);
+          if (more && !early) begin(y, n + 1, 0, g_next);
+          if (more && !early) begin(y, n + 1, 1, g_next);
           g = g_next;
           x = y;
           have = more;
@@ -418,7 +511,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
   } else if (warp < 12) {
-    regs_inc<kRegsSoftmax>();
     // ===================== softmax: one thread per row =====================
     const int s = (warp - 4) >> 2;
     const int wq = warp & 3;
@@ -432,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Piece x;
     while (ok && next(n_got, x)) {
       const int nt = slot_tiles(x, s);
-      if (nt == 0) continue;  // a piece of one key tile leaves slot 1 nothing
+      if (nt == 0) continue;  // a piece of one key tile leaves one slot nothing
       const bool any = 32 * wq < slot_rows(x, s);  // this warp has rows
       int limit = x.kv_len;                        // keys the row sees
       if (x.b >= 0) limit += 1 - p.T + (256 * x.blk + (split_rows(x) ? 128 * s : 0) + row) % p.T;
@@ -442,14 +534,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!warp_wait(bars + L::kSFull + s, g & 1, abort_flag, p.status)) { ok = false; break; }
         tc_fence_after_sync();
         if (any) {
-          const int rem = min(limit, x.kv_len) - 128 * (x.tile0 + slot_tile(x, s, j));
-          const bool masked = __any_sync(0xffffffffu, rem < 128);
+          // columns before `whole` are seen by all of the warp's rows, from `none` on by none
+          const int rem = min(128, limit - 128 * (x.tile0 + slot_tile(x, s, j)));
+          const int whole = __reduce_min_sync(0xffffffffu, rem), none = __reduce_max_sync(0xffffffffu, rem);
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-          for (int q0 = 0; q0 < 128; q0 += 32) {
+          for (int q0 = 0; q0 < none; q0 += 32) {
             uint32_t v[32];
             tmem_ld32(t_s + q0, v);
-            if (masked) {
+            if (q0 + 32 > whole) {
 #pragma unroll
               for (int q = 0; q < 32; ++q)
                 if (q >= rem - q0) v[q] = __float_as_uint(-INFINITY);
@@ -490,8 +583,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int q0 = 0; q0 < 128; q0 += 32) {
             uint32_t v[32], pk[16];
+            if (q0 >= none) {
+#pragma unroll
+              for (int q = 0; q < 16; ++q) pk[q] = 0u;
+              VSA_TMEM_ST16(t_s + q0 / 2, pk, 0);
+              continue;
+            }
             tmem_ld32(t_s + q0, v);
-            if (masked) {
+            if (q0 + 32 > whole) {
 #pragma unroll
               for (int q = 0; q < 32; ++q)
                 if (q >= rem - q0) v[q] = __float_as_uint(-INFINITY);
@@ -500,9 +599,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int q = 0; q < 16; ++q) {
               float a, b;
               upk2(ffma2(pk2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1])), cc, nm2), a, b);
-              const float p0 = fast_exp2(a), p1 = fast_exp2(b);
-              l2 = fadd2(l2, pk2(p0, p1));
-              pk[q] = pack_bf16x2(p0, p1);
+              a = fast_exp2(a);
+              b = fast_exp2(b);
+              l2 = fadd2(l2, pk2(a, b));
+              pk[q] = pack_bf16x2(a, b);
             }
             VSA_TMEM_ST16(t_s + q0 / 2, pk, 0);
           }
@@ -518,17 +618,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++n;
       float la, lb;
       upk2(l2, la, lb);
+      const float l = la + lb;
       ml[s * 256 + row] = m;
-      ml[s * 256 + 128 + row] = la + lb;
+      ml[s * 256 + 128 + row] = l;
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + L::kLFull + s);
+      if (split_rows(x)) {
+        // 256 rows to write: each slot's own warps, side by side
+        if (!warp_wait(bars + L::kOFull + s, (n - 1) & 1, abort_flag, p.status)) { ok = false; break; }
+        tc_fence_after_sync();
+        const int rows = slot_rows(x, s);
+        if (any) {
+          const long long at = x.part * (x.b < 0 ? p.pfx_rows : p.sfx_rows) + 128 * s;
+          if (row < rows) (x.b < 0 ? p.part_lse_p : p.part_lse_s)[at + row] = l == 0.f ? -INFINITY : m + __log2f(l);
+          write_part<D>((x.b < 0 ? p.part_p : p.part_s) + at * D, rows, wq, lane, t_o, false,
+                        l == 0.f ? 0.f : 1.f / l, 0.f);
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + L::kOEmpty + s);
+      }
     }
   } else {
-    regs_dec<kRegsEpilogue>();
     // ===================== Q rows in, partial rows out (fp32) =====================
     const int wq = warp - 12;
     const uint32_t t_lane = tmem_base + (uint32_t(wq * 32) << 16) + kTmemO;
-    uint32_t cs[2] = {0, 0};
+    uint32_t cs0 = 0, cs1 = 0;  // pieces of the slots
     uint32_t n_got = 0, freed = 0;  // pieces whose Q tiles are known to be free
     bool ok = true;
     // Rows of piece x (number n) into its Q tile or tiles: 16-byte chunks,
@@ -574,34 +689,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     Piece x, y;
     uint32_t n = 0;
-    bool have = next(n_got, x);
-    if (have) ok = gather(x, 0, false);
-    while (ok && have) {
+    x.n = -1;  // no piece yet
+    while (ok) {
+      // the next piece's Q before this one's results
       const bool more = next(n_got, y);
-      if (more && !gather(y, n + 1, split_rows(x))) break;
+      if (more && !gather(y, n, x.n > 0 && split_rows(x))) break;
+      ++n;
+      if (x.n < 0) {
+        x = y;
+        if (!more) break;
+        continue;
+      }
       const bool split = split_rows(x);
-      const bool two = slot_tiles(x, 1) > 0;
+      const bool has0 = slot_tiles(x, 0) > 0, has1 = slot_tiles(x, 1) > 0;
+      const bool two = has0 && has1;
 #pragma unroll 1
       for (int s = 0; ok && s < 2; ++s) {
-        if (s == 0 || two) {
-          ok = warp_wait(bars + L::kLFull + s, cs[s] & 1, abort_flag, p.status) &&
-               warp_wait(bars + L::kOFull + s, cs[s] & 1, abort_flag, p.status);
+        if (s ? has1 : has0) {
+          const uint32_t ph = (s ? cs1 : cs0) & 1;
+          ok = warp_wait(bars + L::kLFull + s, ph, abort_flag, p.status) &&
+               warp_wait(bars + L::kOFull + s, ph, abort_flag, p.status);
           if (!ok) break;
-          ++cs[s];
+          cs0 += s ^ 1;
+          cs1 += s;
         }
-        if (!split && s == 0) continue;  // both slots are written together
+        // both slots are written together; a split piece's by its softmax warps,
+        // but its maxima may be replaced only once these warps have passed here
+        if (split) {
+          if (lane == 0) mbar_arrive(bars + L::kOEmpty + s);
+          continue;
+        }
+        if (s == 0) continue;
         tc_fence_after_sync();
-        const int rows = slot_rows(x, s);
-        if (32 * wq < rows) {
-          // weights of the slots' sums for this lane's row: split, one slot at a
-          // time; else both together
-          const int s0 = split ? s : 0;
-          const bool both = !split && two;
+        if (32 * wq < x.rows) {
+          // weights of the slots' sums for this lane's row
           float w0 = 1.f, w1 = 0.f;
           const int row = 32 * wq + lane;
+          const int s0 = has0 ? 0 : 1;
           const float m0 = ml[s0 * 256 + row], l0 = ml[s0 * 256 + 128 + row];
           float top = m0, sum = l0;
-          if (both) {
+          if (two) {
             const float m1 = ml[256 + row], l1 = ml[384 + row];
             top = fmaxf(m0, m1);
             const float ref = top == -INFINITY ? 0.f : top;
@@ -610,68 +737,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum = l0 * w0 + l1 * w1;
           }
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          w0 *= inv;
-          w1 *= inv;
-          const int first = split ? 128 * s : 0;
-          const long long at = x.part * (x.b < 0 ? p.pfx_rows : p.sfx_rows) + first;
-          if (row < rows) (x.b < 0 ? p.part_lse_p : p.part_lse_s)[at + row] = sum == 0.f ? -INFINITY : top + __log2f(sum);
-          float* o = (x.b < 0 ? p.part_p : p.part_s) + at * D;
-          // four lanes to a row's 64 bytes
-#pragma unroll 1
-          for (int u = 0; u < 2; ++u) {
-            float a0[2], a1[2];
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              a0[b] = __shfl_sync(0xffffffffu, w0, 16 * u + 8 * b + lane / 4);
-              a1[b] = __shfl_sync(0xffffffffu, w1, 16 * u + 8 * b + lane / 4);
-            }
-            if (32 * wq + 16 * u >= rows) break;
-            const uint32_t t_u = t_lane + ((uint32_t)(16 * u) << 16) + D * s0;
-#pragma unroll 1
-            for (int q0 = 0; q0 < D; q0 += 32) {
-              uint32_t va[16], vb[16];
-              dense::tmem_ld_16x256(t_u + q0, va, 0);
-              if (both) dense::tmem_ld_16x256(t_u + D + q0, vb, 0);
-              asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                float2 f = make_float2(__uint_as_float(va[2 * k]) * a0[k & 1], __uint_as_float(va[2 * k + 1]) * a0[k & 1]);
-                if (both) {
-                  f.x = fmaf(__uint_as_float(vb[2 * k]), a1[k & 1], f.x);
-                  f.y = fmaf(__uint_as_float(vb[2 * k + 1]), a1[k & 1], f.y);
-                }
-                va[2 * k] = __float_as_uint(f.x);
-                va[2 * k + 1] = __float_as_uint(f.y);
-              }
-              // pairs of lanes exchange halves of two column groups: 16 bytes each
-              const bool odd = lane & 1;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int b = k & 1, lo = 8 * (k >> 1) + 2 * b, hi = lo + 4;  // registers of groups 2 (k / 2), + 1
-                const int r = 32 * wq + 16 * u + 8 * b + lane / 4;
-                const uint32_t sx = odd ? va[lo] : va[hi], sy = odd ? va[lo + 1] : va[hi + 1];
-                const uint32_t rx = __shfl_xor_sync(0xffffffffu, sx, 1), ry = __shfl_xor_sync(0xffffffffu, sy, 1);
-                const uint4 f = odd ? make_uint4(rx, ry, va[hi], va[hi + 1]) : make_uint4(va[lo], va[lo + 1], rx, ry);
-                if (r < rows)
-                  *reinterpret_cast<uint4*>(o + (long long)r * D + q0 + 16 * (k >> 1) + (odd ? 8 : 0) + 2 * (lane & 2)) = f;
-              }
-            }
-          }
+          const long long at = x.part * (x.b < 0 ? p.pfx_rows : p.sfx_rows);
+          if (row < x.rows) (x.b < 0 ? p.part_lse_p : p.part_lse_s)[at + row] = sum == 0.f ? -INFINITY : top + __log2f(sum);
+          write_part<D>((x.b < 0 ? p.part_p : p.part_s) + at * D, x.rows, wq, lane, t_lane + D * s0, two, w0 * inv, w1 * inv);
         }
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) {
-          if (!split) {
-            mbar_arrive(bars + L::kOEmpty);
-            if (two) mbar_arrive(bars + L::kOEmpty + 1);
-          } else {
-            mbar_arrive(bars + L::kOEmpty + s);
+          // for itself and in place of the softmax warps
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (has0) mbar_arrive(bars + L::kOEmpty);
+            if (has1) mbar_arrive(bars + L::kOEmpty + 1);
           }
         }
       }
       x = y;
-      have = more;
-      ++n;
+      if (!more) break;
     }
   }
 
@@ -707,8 +789,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
       if (tiles == 0) continue;
       const int r = kind ? row : b * p.rows_per_req + row;
       const int blk = r >> 8;
-      const int t0 = h * line.per_head + (kind ? p.pfx_blocks * tp + before : 0) + blk * tiles;
-      const int c0 = cta_of(line, t0), count = cta_of(line, t0 + tiles - 1) - c0 + 1;
+      const int t0 = h * line.per_head + (kind ? line.pfx * tp + line.sfx * before : 0) + blk * line.heavy * tiles;
+      const int w = tile_units(line, kind ? p.rows_per_req : p.B * p.rows_per_req, blk);
+      const int c0 = cta_of(line, t0), count = cta_of(line, t0 + w * (tiles - 1)) - c0 + 1;
       const long long seg = kind ? ((long long)h * p.B + b) * p.sfx_blocks + blk : (long long)h * p.pfx_blocks + blk;
       const int rows = kind ? p.sfx_rows : p.pfx_rows;
       const long long first = (seg + c0) * rows + (r & 255);
@@ -800,7 +883,7 @@ static int launch_prefix_t(const PrefixParams& p, const CUtensorMap* m, cudaStre
   using L = prefix::Layout<D>;
   auto kern = prefix::prefix_attn_kernel<D>;
   static KernelReady ready;
-  const int rc = ready.check(reinterpret_cast<const void*>(kern), (int)prefix::kLaunchRegs, (int)L::kAlloc);
+  const int rc = ready.check(reinterpret_cast<const void*>(kern), 0, (int)L::kAlloc);
   if (rc != VSA_OK) return rc;
   // at most one CTA per key tile there can be
   const long long cap = (long long)p.Hkv * ((long long)p.pfx_blocks * ((p.prefix_len + 127LL) / 128) +
