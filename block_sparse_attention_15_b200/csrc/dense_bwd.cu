@@ -190,8 +190,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = tid / 32, lane = tid % 32;
   const int cta = blockIdx.x, grid = gridDim.x;
 
-  if (tid == 0) {
-    for (int i = 0; i < L::kNumBars; ++i) {
+  if (warp == 0) {
+    for (int i = lane; i < L::kNumBars; i += 32) {
       // a TMA transaction, a commit or one thread's arrival, except where the
       // epilogue's four or the softmax's eight warps arrive
       const uint32_t count = ((i >= L::kQReady && i < L::kQFree) || i == L::kOEmpty) ? 4u
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                                                       : 1u;
       mbar_init(bars + i, count);
     }
-    *abort_flag = 0;
+    if (lane == 0) *abort_flag = 0;
     mbar_fence_init();
   }
   if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
@@ -660,8 +660,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = tid / 32, lane = tid % 32;
   const int cta = blockIdx.x, grid = gridDim.x;
 
-  if (tid == 0) {
-    for (int i = 0; i < L::kNumBars; ++i) {
+  if (warp == 0) {
+    for (int i = lane; i < L::kNumBars; i += 32) {
       const uint32_t count = (i == L::kDVEmpty || i == L::kDKEmpty) ? 4u
                              : (i == L::kPFull || i == L::kDSFull ||
                                 (i >= L::kRowEmpty && i < L::kRowEmpty + NROW)) ? (uint32_t)kSoftmaxWarps
@@ -669,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                                                : 1u;
       mbar_init(bars + i, count);
     }
-    *abort_flag = 0;
+    if (lane == 0) *abort_flag = 0;
     mbar_fence_init();
   }
   if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);

@@ -156,14 +156,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = tid / 32, lane = tid % 32;
   const int cta = blockIdx.x, grid = gridDim.x;
 
-  if (tid == 0) {
-    for (int i = 0; i < L::kNumBars; ++i) {
+  if (warp == 0) {
+    for (int i = lane; i < L::kNumBars; i += 32) {
       // a TMA transaction, a commit or one thread's arrival, except where the
       // four warps of a softmax or epilogue group arrive
       const bool four = (i >= L::kPFull && i < L::kPFull + 2) || (i >= L::kOEmpty && i < L::kNumBars);
       mbar_init(bars + i, four ? 4u : 1u);
     }
-    *abort_flag = 0;
+    if (lane == 0) *abort_flag = 0;
     mbar_fence_init();
   }
   if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);

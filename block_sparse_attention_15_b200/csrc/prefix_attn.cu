@@ -336,8 +336,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the line needs the lengths from memory: first of all
   Walk walk(p, lane, warp == 3);
 
-  if (tid == 0) {
-    for (int i = 0; i < L::kNumBars; ++i) {
+  if (warp == 0) {
+    for (int i = lane; i < L::kNumBars; i += 32) {
       const uint32_t count = (i < L::kQFree || (i >= L::kPFull && i < L::kPFull + 2) ||
                               (i >= L::kLFull && i < L::kItFull))     ? 4u
                              : (i >= L::kOEmpty && i < L::kLFull)      ? 8u
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                                        : 1u;
       mbar_init(bars + i, count);
     }
-    *abort_flag = 0;
+    if (lane == 0) *abort_flag = 0;
     mbar_fence_init();
   }
   if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
