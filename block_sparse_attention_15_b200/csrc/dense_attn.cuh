@@ -6,6 +6,8 @@
 #include <cuda.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "dense_launch.h"
 #include "vsa_device.cuh"
 
@@ -148,6 +150,162 @@ __device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, uint32_t (&r)[N],
         "=r"(r[o + 6]), "=r"(r[o + 7]), "=r"(r[o + 8]), "=r"(r[o + 9]), "=r"(r[o + 10]), "=r"(r[o + 11]),
         "=r"(r[o + 12]), "=r"(r[o + 13]), "=r"(r[o + 14]), "=r"(r[o + 15])
       : "r"(taddr));
+}
+
+// 16 TMEM lanes x 64 fp32 columns, as above with twice the columns; and back.
+__device__ __forceinline__ void tmem_ld_16x256_64(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st_16x256(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// 16 TMEM lanes x 32 columns of 32 bits: register 2 i + b holds lane
+// threadIdx / 4 + 8 b, column 4 i + threadIdx % 4.
+__device__ __forceinline__ void tmem_st_16x128_32(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// Largest excess (log2 units) of a logit over its row's reference max that is
+// exponentiated without moving the reference: probabilities stay below 2^8.
+constexpr float kRefresh = 8.f;
+
+// One 128-key tile of the online softmax, by a warp that has 16 rows of the
+// query tile (TMEM lanes from t_s's on): a thread has rows lane / 4 + 8 b and a
+// quarter of their columns.  Two warps share the 32 lanes that each may reach,
+// so that a slot's softmax is eight warps' work, and a row stays within one warp:
+// its max takes two shuffles, its sum none until the end.
+// S is read twice (a load takes 50 cycles) rather than kept in 64 registers.
+//   rem[b]: columns of the tile that row b sees; whole / none: the least and the
+//   largest of those over the warp, at most 128
+//   m, l2: the rows' reference max (log2 units) and partial sums; O is rescaled
+//   when a reference moves (S complete implies the PV before it is: one thread
+//   issued both, in order)
+// POLY of eight column pairs take their exponential on the FMA pipe.
+template <int D, int POLY, int UNROLL>
+__device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, float c, const int (&rem)[2], int whole,
+                                             int none, bool first, int lane, float (&m)[2], uint64_t (&l2)[2]) {
+  const int col0 = 2 * (lane & 3);
+  auto mask = [&](uint32_t (&v)[32], int q0) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if (8 * (k >> 2) + (k & 1) >= rem[(k >> 1) & 1] - q0 - col0) v[k] = 0xff800000u;  // -inf
+  };
+  float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll UNROLL
+  for (int q0 = 0; q0 < 128; q0 += 64) {
+    if (q0 >= none) break;
+    uint32_t v[32];
+    tmem_ld_16x256_64(t_s + q0, v);
+    if (q0 + 64 > whole) mask(v, q0);
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) {
+      mx[0] = fmax3(mx[0], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+      mx[1] = fmax3(mx[1], __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+    }
+  }
+  float nm[2];
+  bool move = false;
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    mx[b] = fmaxf(mx[b], __shfl_xor_sync(0xffffffffu, mx[b], 1));
+    mx[b] = fmaxf(mx[b], __shfl_xor_sync(0xffffffffu, mx[b], 2)) * c;
+    const bool up = mx[b] > m[b] + kRefresh;
+    nm[b] = up ? mx[b] : m[b];
+    move = move || up;
+  }
+  if (__any_sync(0xffffffffu, move)) {
+    float a[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      // 1 where the reference stays; 0 while nothing was seen (O and the sum are 0)
+      a[b] = m[b] == -INFINITY ? 0.f : fast_exp2(m[b] - nm[b]);
+      float la, lb;
+      upk2(l2[b], la, lb);
+      l2[b] = pk2(la * a[b], lb * a[b]);
+      m[b] = nm[b];
+    }
+    if (!first) {
+#pragma unroll 1
+      for (int q0 = 0; q0 < D; q0 += 32) {
+        uint32_t ov[16];
+        tmem_ld_16x256(t_o + q0, ov, 0);
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+        for (int k = 0; k < 16; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * a[(k >> 1) & 1]);
+        tmem_st_16x256(t_o + q0, ov);
+      }
+    }
+  }
+  // probabilities 2^(s c - m): bf16 pairs for the tensor core, fp32 sums.  P's 32
+  // columns per step lie over columns of S that were read before.
+  const uint64_t cc = pk2(c, c);
+  uint64_t nm2[2];
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const float ref = m[b] == -INFINITY ? 0.f : -m[b];  // nothing seen yet: all -inf, all 0
+    nm2[b] = pk2(ref, ref);
+  }
+#pragma unroll UNROLL
+  for (int q0 = 0; q0 < 128; q0 += 64) {
+    uint32_t pk[16];
+    if (q0 >= none) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) pk[k] = 0u;
+      tmem_st_16x128_32(t_s + q0 / 2, pk);
+      continue;
+    }
+    uint32_t v[32];
+    tmem_ld_16x256_64(t_s + q0, v);
+    auto probs = [&](auto mk) {
+      constexpr bool kMask = decltype(mk)::value;
+      if (kMask) mask(v, q0);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        float a, b;
+        upk2(ffma2(pk2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), cc, nm2[k & 1]), a, b);
+        if (!kMask && (k & 7) < POLY) {
+          upk2(exp2_fma2_t<true>(a, b), a, b);
+        } else {
+          a = fast_exp2(a);
+          b = fast_exp2(b);
+        }
+        l2[k & 1] = fadd2(l2[k & 1], pk2(a, b));
+        pk[k] = pack_bf16x2(a, b);
+      }
+    };
+    if (q0 + 64 > whole) probs(std::true_type{});
+    else probs(std::false_type{});
+    tmem_st_16x128_32(t_s + q0 / 2, pk);
+  }
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// The whole sum of a row whose partial sums four neighbouring lanes have.
+__device__ __forceinline__ float quad_sum(uint64_t l2) {
+  float la, lb;
+  upk2(l2, la, lb);
+  float l = la + lb;
+  l += __shfl_xor_sync(0xffffffffu, l, 1);
+  return l + __shfl_xor_sync(0xffffffffu, l, 2);
 }
 
 // S = Q . K^T: M = N = 128, K = D; tiles are [D / 64][128 rows][128 B].

@@ -1067,9 +1067,9 @@ static int launch_dense_bwd_t(DenseBwdParams p, const CUtensorMap* m, const int4
   static KernelReady ready_q, ready_k;
   auto kq = dense::dense_dq_kernel<D>;
   auto kk = dense::dense_dkv_kernel<D>;
-  int rc = ready_q.check(reinterpret_cast<const void*>(kq), 0, (int)dense::QLayout<D>::kAlloc);
+  int rc = ready_q.check(reinterpret_cast<const void*>(kq), (int)dense::QLayout<D>::kAlloc);
   if (rc == VSA_OK)
-    rc = ready_k.check(reinterpret_cast<const void*>(kk), 0, (int)dense::KLayout<D>::kAlloc);
+    rc = ready_k.check(reinterpret_cast<const void*>(kk), (int)dense::KLayout<D>::kAlloc);
   if (rc != VSA_OK) return rc;
   const int sms = device_sm_count();
   int units[kDenseMaxSeqs];

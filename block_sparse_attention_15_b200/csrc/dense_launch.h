@@ -56,11 +56,10 @@ struct DenseBatch {
   int chunk(int i0, int4* seqs) const;
 };
 
-// Once per device: the kernel has the register count its split needs, and its
-// shared memory limit is raised.
+// Once per device: the kernel's shared memory limit is raised.
 struct KernelReady {
   std::atomic<unsigned long long> done{0};
-  int check(const void* kern, int regs, int smem);
+  int check(const void* kern, int smem);
 };
 
 int device_sm_count();

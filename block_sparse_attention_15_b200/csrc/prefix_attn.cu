@@ -883,7 +883,7 @@ static int launch_prefix_t(const PrefixParams& p, const CUtensorMap* m, cudaStre
   using L = prefix::Layout<D>;
   auto kern = prefix::prefix_attn_kernel<D>;
   static KernelReady ready;
-  const int rc = ready.check(reinterpret_cast<const void*>(kern), 0, (int)L::kAlloc);
+  const int rc = ready.check(reinterpret_cast<const void*>(kern), (int)L::kAlloc);
   if (rc != VSA_OK) return rc;
   // at most one CTA per key tile there can be
   const long long cap = (long long)p.Hkv * ((long long)p.pfx_blocks * ((p.prefix_len + 127LL) / 128) +
