@@ -37,20 +37,22 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 }
 }  // namespace slim
 
-// Work item i of a launch: one tile unit of one sequence.  Sequences are sorted
-// by their unit counts n_0 >= n_1 >= ..., and units are taken by descending
-// rank t (unit t of a causal sequence costs about t + 1 key tiles), every
-// sequence that has a unit of that rank in turn: longest work first, so the
-// last wave is made of the short items.  The ranks n_r .. n_{r-1} - 1 are those
-// that exactly r sequences have; their items start at first[r].
+// Unit i of a launch, the long ones first.  The table's first sequences are flat
+// (their units cost about the same): by descending cost, one after the other.
+// The others have units whose cost grows with their rank t (tile t of a causal
+// sequence has about t + 1 tiles to read): sorted by their unit counts
+// n_0 >= n_1 >= ..., their units are taken by descending rank, every sequence
+// that has a unit of that rank in turn.  The ranks n_r .. n_{r-1} - 1 are those
+// that exactly r of them have.
 struct Unit {
   int seq;   // index into DenseSeqs::seq
   int rank;  // 0 .. units[seq] - 1
 };
 
 __device__ __forceinline__ Unit find_unit(const DenseSeqs& t, int i) {
-  // largest r in [1, n] with first[r] <= i
-  int lo = 1, hi = t.n;
+  const bool flat = i < t.first[t.n_flat];
+  // the last entry of first[] that is not past i
+  int lo = flat ? 0 : t.n_flat + 1, hi = flat ? t.n_flat - 1 : t.n;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (t.first[mid] <= i) lo = mid;
@@ -58,31 +60,74 @@ __device__ __forceinline__ Unit find_unit(const DenseSeqs& t, int i) {
   }
   const int o = i - t.first[lo];
   Unit u;
-  u.seq = o % lo;
-  u.rank = t.units[lo - 1] - 1 - o / lo;
+  if (flat) {
+    u.seq = lo;
+    u.rank = t.units[lo] - 1 - o;
+  } else {
+    const int r = lo - t.n_flat;
+    u.seq = t.n_flat + o % r;
+    u.rank = t.units[lo - 1] - 1 - o / r;
+  }
   return u;
 }
 
-// The w-th item of CTA c of a persistent grid of g: waves alternate direction,
-// so the CTA that got a wave's longest item gets the next wave's shortest.
-__device__ __forceinline__ int wave_item(int w, int c, int g) {
-  return w * g + ((w & 1) ? g - 1 - c : c);
-}
+// Blocks of the grid are work items.  Those that find an SM at launch stay on it
+// and take over blocks that have not started (cluster launch control), in the
+// grid's order, until none is left: an SM that is through early takes more,
+// without a counter in memory.  One warp asks; `reply` is 16 bytes of shared
+// memory, `bar` counts one arrival.
+struct Takeover {
+  uint64_t* bar;
+  uint4* reply;
+  uint32_t asked;
+
+  __device__ __forceinline__ void ask(int lane) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bar, 16);
+      asm volatile(
+          "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+              smem_u32(reply)),
+          "r"(smem_u32(bar))
+          : "memory");
+    }
+    __syncwarp();
+  }
+  // The block taken over, -1: none is left (and none may be asked for again).
+  __device__ __forceinline__ int answer(volatile int* abort_flag, int* status) {
+    if (!slim::warp_wait(bar, asked++ & 1, abort_flag, status)) return -1;
+    uint32_t got, block;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}\n"
+        : "=r"(got), "=r"(block)
+        : "r"(smem_u32(reply))
+        : "memory");
+    // the reply is read before the next one may be written
+    fence_proxy_async_smem();
+    __syncwarp();
+    return got ? (int)block : -1;
+  }
+};
 
 // Work items of a CTA: one warp finds them (searches and divisions of a few
 // hundred cycles) and hands them to the others through a ring in shared memory.
-constexpr int kItemSlots = 4;
-template <typename Item>
+// (Two slots where items are taken over: no CTA holds many that others could do.)
+template <typename Item, int N>
 struct alignas(16) ItemRing {
-  Item item[kItemSlots];
+  static constexpr int kSlots = N;
+  Item item[N];
 };
 
 // The finder's side, whole warp: the w-th item, or the end mark (n < 0).
-template <typename Item>
-__device__ __forceinline__ bool put_item(ItemRing<Item>* ring, uint64_t* full, uint64_t* empty, uint32_t w,
+template <typename Item, int N>
+__device__ __forceinline__ bool put_item(ItemRing<Item, N>* ring, uint64_t* full, uint64_t* empty, uint32_t w,
                                          const Item& x, int lane, volatile int* abort_flag, int* status) {
-  const int slot = (int)(w % kItemSlots);
-  if (w >= (uint32_t)kItemSlots && !slim::warp_wait(empty + slot, (w / kItemSlots - 1) & 1, abort_flag, status))
+  const int slot = (int)(w % N);
+  if (w >= (uint32_t)N && !slim::warp_wait(empty + slot, (w / N - 1) & 1, abort_flag, status))
     return false;
   if (lane == 0) {
     ring->item[slot] = x;
@@ -93,11 +138,11 @@ __device__ __forceinline__ bool put_item(ItemRing<Item>* ring, uint64_t* full, u
 }
 
 // The other warps' side: false at the end.
-template <typename Item>
-__device__ __forceinline__ bool get_item(const ItemRing<Item>* ring, uint64_t* full, uint64_t* empty, uint32_t& w,
+template <typename Item, int N>
+__device__ __forceinline__ bool get_item(const ItemRing<Item, N>* ring, uint64_t* full, uint64_t* empty, uint32_t& w,
                                          Item& x, int lane, volatile int* abort_flag, int* status) {
-  const int slot = (int)(w % kItemSlots);
-  if (!slim::warp_wait(full + slot, (w / kItemSlots) & 1, abort_flag, status)) return false;
+  const int slot = (int)(w % N);
+  if (!slim::warp_wait(full + slot, (w / N) & 1, abort_flag, status)) return false;
   x = ring->item[slot];
   __syncwarp();
   if (lane == 0) mbar_arrive(empty + slot);
@@ -106,11 +151,11 @@ __device__ __forceinline__ bool get_item(const ItemRing<Item>* ring, uint64_t* f
 }
 
 // The same for a role that one thread plays.
-template <typename Item>
-__device__ __forceinline__ bool get_item_one(const ItemRing<Item>* ring, uint64_t* full, uint64_t* empty,
+template <typename Item, int N>
+__device__ __forceinline__ bool get_item_one(const ItemRing<Item, N>* ring, uint64_t* full, uint64_t* empty,
                                              uint32_t& w, Item& x, volatile int* abort_flag, int* status) {
-  const int slot = (int)(w % kItemSlots);
-  if (!slim::mbar_wait(full + slot, (w / kItemSlots) & 1, abort_flag, status)) return false;
+  const int slot = (int)(w % N);
+  if (!slim::mbar_wait(full + slot, (w / N) & 1, abort_flag, status)) return false;
   x = ring->item[slot];
   mbar_arrive(empty + slot);
   ++w;

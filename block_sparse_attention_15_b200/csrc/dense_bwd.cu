@@ -27,9 +27,9 @@
 //            S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q
 //          P^T and dS^T are A operands in TMEM, over their own S and dP.
 //
-// Both: persistent grid, one CTA per SM, 512 threads: warp 0 tile loads, warp
-// 1 products, warps 2-3 helpers, warps 4-11 softmax (one thread per TMEM lane
-// and half of the 128 columns), warps 12-15 epilogue.  Products are issued in
+// Both: one CTA per SM, item after item, 768 threads: warp 0 tile loads, warp 1
+// products (one thread), warps 2-3 helpers, warps 4-19 softmax (32 of the 128
+// columns each), warps 20-23 epilogue.  Products are issued in
 // the order S(i+1), dQ(i), dP(i+1) and dP(i), dV(i), S(i+1), dK(i): the
 // exponentials of a tile run under the previous tile's last product, its dS
 // under the next tile's S.
@@ -122,6 +122,8 @@ struct QItem {
   int n;           // key tiles
 };
 
+using QItems = ItemRing<QItem, 2>;
+
 template <int D>
 struct QLayout {
   static constexpr int DH = D / 64;
@@ -130,7 +132,7 @@ struct QLayout {
   static constexpr uint32_t kRingOff = 0;
   static constexpr uint32_t kRowOff = kRingOff + NST * kTile;  // [2][2][128] f32: -lse, delta
   static constexpr uint32_t kItemOff = kRowOff + 2048u;
-  static constexpr uint32_t kBarOff = kItemOff + (uint32_t)sizeof(ItemRing<QItem>);
+  static constexpr uint32_t kBarOff = kItemOff + (uint32_t)sizeof(QItems);
   // Q, and dO with out, signal barriers of their item's, K and V tiles their
   // stage's.  Four of the former: the ring holds those of fewer than four items
   // ahead of the one whose operands are being copied.
@@ -141,10 +143,11 @@ struct QLayout {
                        kDReady = kGReady + 1, kQFree = kDReady + 2, kGFree = kQFree + 1,
                        kSFull = kGFree + 1, kSFree = kSFull + 1,
                        kDPFull = kSFree + 1, kDSFull = kDPFull + 1, kOFull = kDSFull + 1,
-                       kOEmpty = kOFull + 1, kItFull = kOEmpty + 1, kItEmpty = kItFull + kItemSlots,
-                       kNumBars = kItEmpty + kItemSlots;
+                       kOEmpty = kOFull + 1, kItFull = kOEmpty + 1, kItEmpty = kItFull + QItems::kSlots,
+                       kTake = kItEmpty + QItems::kSlots, kLoaded = kTake + 1, kNumBars = kLoaded + 1;
   static constexpr uint32_t kMiscOff = kBarOff + 8u * kNumBars;
-  static constexpr uint32_t kAlloc = kMiscOff + 16u;
+  static constexpr uint32_t kTakeOff = (kMiscOff + 16u + 15u) & ~15u;
+  static constexpr uint32_t kAlloc = kTakeOff + 16u;
   static_assert(kAlloc <= 227u * 1024u, "shared memory");
 };
 // TMEM columns
@@ -181,14 +184,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   float* rowv = reinterpret_cast<float*>(smem + L::kRowOff);
-  ItemRing<QItem>* items = reinterpret_cast<ItemRing<QItem>*>(smem + L::kItemOff);
+  QItems* items = reinterpret_cast<QItems*>(smem + L::kItemOff);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
 
   const int tid = threadIdx.x;
   const int warp = tid / 32, lane = tid % 32;
-  const int cta = blockIdx.x, grid = gridDim.x;
 
   if (warp == 0) {
     for (int i = lane; i < L::kNumBars; i += 32) {
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // epilogue's four or the softmax's eight warps arrive
       const uint32_t count = ((i >= L::kQReady && i < L::kQFree) || i == L::kOEmpty) ? 4u
                              : (i == L::kSFree || i == L::kDSFull)                    ? (uint32_t)kSoftmaxWarps
-                             : (i >= L::kItEmpty)                                     ? kThreads / 32 - 1u  // all warps but one
+                             : (i >= L::kItEmpty && i < L::kTake)                                     ? kThreads / 32 - 1u  // all warps but one
                                                                                       : 1u;
       mbar_init(bars + i, count);
     }
@@ -249,6 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 load_rows(to, is_v ? &tm_v : &tm_k, is_v ? p.v_ax : p.k_ax, full, dh * 64, x.kv0 + key, x.hk, 0, keep);
             }
           }
+          mbar_arrive(bars + L::kLoaded);
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       }
@@ -258,13 +261,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t n_item = 0;
       bool ok = true;
       QItem x;
-      for (int w = 0, it; ok && (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
-        if (it >= p.n_work) continue;
+      Takeover take{bars + L::kTake, reinterpret_cast<uint4*>(smem + L::kTakeOff), 0};
+      for (int it = blockIdx.x; ok && it >= 0; it = ok ? take.answer(abort_flag, p.status) : -1) {
         x = load_qitem(p, seqs, it);
         if (x.n > 0) {
-          ok = put_item(items, bars + L::kItFull, bars + L::kItEmpty, n_item++, x, lane, abort_flag, p.status);
+          // ask for more when this item's last tiles are on their way, not earlier:
+          // what a CTA holds no other can take
+          ok = put_item(items, bars + L::kItFull, bars + L::kItEmpty, n_item, x, lane, abort_flag, p.status) &&
+               warp_wait(bars + L::kLoaded, n_item & 1, abort_flag, p.status);
+          ++n_item;
+          if (ok) take.ask(lane);
           continue;
         }
+        take.ask(lane);
         for (int r = lane; r < x.rows; r += 32) {
           __nv_bfloat16* to = p.dq + x.head * p.dq_st.h + (long long)(x.row0 + r) * p.dq_st.s;
           for (int e = 0; e < D; e += 8) *reinterpret_cast<uint4*>(to + e) = make_uint4(0u, 0u, 0u, 0u);
@@ -347,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok) do_dp(x, 0, 0);
         }
         while (ok && have) {
-          const bool more = next_one(y);
+          bool more = false;
           const uint32_t g_next = g + 2 * x.n + 3;
           // delta is formed: dO and out are read.  Released here, before the next
           // item's first S: with one key tile the ring cannot take that item's K
@@ -358,6 +367,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           release(g + 2);
           for (int j = 0; ok && j < x.n; ++j) {
             const bool last = j + 1 == x.n;
+            // (the item's tiles are all here, so that the next one was asked for)
+            if (last) more = next_one(y);
             if (!last) do_s(x, j + 1, g);
             else if (more) do_s(y, 0, g_next);
             // everything that dP will need first, so that it follows dQ at once
@@ -595,6 +606,8 @@ struct KItem {
   int n;           // query tiles of all heads of the group
 };
 
+using KItems = ItemRing<KItem, 2>;
+
 template <int D>
 struct KLayout {
   static constexpr int DH = D / 64;
@@ -605,15 +618,16 @@ struct KLayout {
   static constexpr uint32_t kRingOff = 2 * kTile;
   static constexpr uint32_t kRowOff = kRingOff + NST * kTile;  // [NROW][2][128] f32
   static constexpr uint32_t kItemOff = kRowOff + NROW * 1024u;
-  static constexpr uint32_t kBarOff = kItemOff + (uint32_t)sizeof(ItemRing<KItem>);
+  static constexpr uint32_t kBarOff = kItemOff + (uint32_t)sizeof(KItems);
   static constexpr int kFull = 0, kEmpty = NST, kPre = 2 * NST, kRowFull = 3 * NST,
                        kRowEmpty = kRowFull + NROW, kKFull = kRowEmpty + NROW, kKEmpty = kKFull + 1,
                        kVFull = kKEmpty + 1, kVEmpty = kVFull + 1, kSFull = kVEmpty + 1, kPFull = kSFull + 1, kDPFull = kPFull + 1,
                        kDSFull = kDPFull + 1, kDVFull = kDSFull + 1, kDKFull = kDVFull + 1,
-                       kDVEmpty = kDKFull + 1, kDKEmpty = kDVEmpty + 1, kItFull = kDKEmpty + 1, kItEmpty = kItFull + kItemSlots,
-                       kNumBars = kItEmpty + kItemSlots;
+                       kDVEmpty = kDKFull + 1, kDKEmpty = kDVEmpty + 1, kItFull = kDKEmpty + 1, kItEmpty = kItFull + KItems::kSlots,
+                       kTake = kItEmpty + KItems::kSlots, kLoaded = kTake + 1, kNumBars = kLoaded + 1;
   static constexpr uint32_t kMiscOff = kBarOff + 8u * kNumBars;
-  static constexpr uint32_t kAlloc = kMiscOff + 16u;
+  static constexpr uint32_t kTakeOff = (kMiscOff + 16u + 15u) & ~15u;
+  static constexpr uint32_t kAlloc = kTakeOff + 16u;
   static_assert(kAlloc <= 227u * 1024u, "shared memory");
 };
 constexpr uint32_t kKS = 0, kKDP = 128, kKDV = 256, kKDK = 384;
@@ -651,21 +665,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   float* rowv = reinterpret_cast<float*>(smem + L::kRowOff);
-  ItemRing<KItem>* items = reinterpret_cast<ItemRing<KItem>*>(smem + L::kItemOff);
+  KItems* items = reinterpret_cast<KItems*>(smem + L::kItemOff);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
 
   const int tid = threadIdx.x;
   const int warp = tid / 32, lane = tid % 32;
-  const int cta = blockIdx.x, grid = gridDim.x;
 
   if (warp == 0) {
     for (int i = lane; i < L::kNumBars; i += 32) {
       const uint32_t count = (i == L::kDVEmpty || i == L::kDKEmpty) ? 4u
                              : (i == L::kPFull || i == L::kDSFull ||
                                 (i >= L::kRowEmpty && i < L::kRowEmpty + NROW)) ? (uint32_t)kSoftmaxWarps
-                             : (i >= L::kItEmpty)                              ? kThreads / 32 - 1u  // all warps but one
+                             : (i >= L::kItEmpty && i < L::kTake)                              ? kThreads / 32 - 1u  // all warps but one
                                                                                : 1u;
       mbar_init(bars + i, count);
     }
@@ -713,6 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 load_rows(dst + dh * 16384, is_do ? &tm_do : &tm_q, is_do ? p.do_ax : p.q_ax, full, dh * 64,
                           x.q0 + r, x.hk * p.group + h, 0, keep);
             }
+          mbar_arrive(bars + L::kLoaded);
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       }
@@ -723,10 +737,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t n_item = 0;
       bool ok = true;
       KItem x;
-      for (int w = 0, it; ok && (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
-        if (it >= p.n_work) continue;
+      Takeover take{bars + L::kTake, reinterpret_cast<uint4*>(smem + L::kTakeOff), 0};
+      for (int it = blockIdx.x; ok && it >= 0; it = ok ? take.answer(abort_flag, p.status) : -1) {
         x = load_kitem(p, seqs, it);
         if (x.n == 0) {
+          take.ask(lane);
           for (int r = lane; r < x.keys; r += 32) {
             __nv_bfloat16* tk = p.dk + x.hk * p.dk_st.h + (long long)(x.key0 + r) * p.dk_st.s;
             __nv_bfloat16* tv = p.dv + x.hk * p.dv_st.h + (long long)(x.key0 + r) * p.dv_st.s;
@@ -755,8 +770,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               load_rows(smem + L::kVOff + dh * 16384, &tm_v, p.v_ax, bars + L::kVFull, dh * 64, x.key0, x.hk, 0, once);
           }
         }
-        ++n_item;
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        // ask for more when this item's last tiles are on their way, not earlier:
+        // what a CTA holds no other can take
+        ok = ok && warp_wait(bars + L::kLoaded, n_item & 1, abort_flag, p.status);
+        ++n_item;
+        if (ok) take.ask(lane);
       }
       x.n = -1;
       if (ok) ok = put_item(items, bars + L::kItFull, bars + L::kItEmpty, n_item, x, lane, abort_flag, p.status);
@@ -851,13 +870,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok) do_dp(x, 0, 0);
         }
         while (ok && have) {
-          const bool more = next_one(y);
+          bool more = false;
           int t = 0;  // query tile of the head
           for (int i = 0; ok && i < x.n; ++i, ++g) {
             const bool last = i + 1 == x.n;
             const int left = x.q_len - 128 * t;
             const int steps = left >= 128 ? 8 : (left + 15) >> 4;
             if (++t == x.tiles) t = 0;
+            // (the item's tiles are all here, so that the next one was asked for)
+            if (last) more = next_one(y);
             // dV, then the next S: everything that S will need first, so that it follows at once
             if (!last || more) before_s(last ? 0 : i + 1, g + 1);
             // the epilogue has taken the previous item's dV
@@ -1071,8 +1092,7 @@ static int launch_dense_bwd_t(DenseBwdParams p, const CUtensorMap* m, const int4
   if (rc == VSA_OK)
     rc = ready_k.check(reinterpret_cast<const void*>(kk), (int)dense::KLayout<D>::kAlloc);
   if (rc != VSA_OK) return rc;
-  const int sms = device_sm_count();
-  int units[kDenseMaxSeqs];
+  int units[kDenseMaxSeqs], flat[kDenseMaxSeqs];
   DenseSeqs table;
   long long q_units = 0, k_units = 0;
   for (int i = 0; i < n; ++i) {
@@ -1081,17 +1101,22 @@ static int launch_dense_bwd_t(DenseBwdParams p, const CUtensorMap* m, const int4
   }
   if (q_units >= (1 << 30) || k_units >= (1 << 30)) return VSA_ERR_UNSUPPORTED;  // 32-bit item index
   if (q_units > 0) {
-    for (int i = 0; i < n; ++i) units[i] = (seqs[i].y + 127) / 128 * p.group;
-    fill_dense_seqs(&table, seqs, units, n);
-    p.n_work = table.n_items * p.Hkv;
-    kq<<<(unsigned)(p.n_work < sms ? p.n_work : sms), dense::kThreads, dense::QLayout<D>::kAlloc, stream>>>(
+    for (int i = 0; i < n; ++i) {
+      units[i] = (seqs[i].y + 127) / 128 * p.group;
+      // behind cached keys the first rows, too, have many to see
+      flat[i] = !p.causal || seqs[i].w > seqs[i].y ? seqs[i].w : 0;
+    }
+    fill_dense_seqs(&table, seqs, units, flat, n);
+    kq<<<(unsigned)q_units, dense::kThreads, dense::QLayout<D>::kAlloc, stream>>>(
         m[0], m[1], m[2], m[3], m[4], p, table);
   }
   if (k_units > 0) {
-    for (int i = 0; i < n; ++i) units[i] = (seqs[i].w + 127) / 128;
-    fill_dense_seqs(&table, seqs, units, n);
-    p.n_work = table.n_items * p.Hkv;
-    kk<<<(unsigned)(p.n_work < sms ? p.n_work : sms), dense::kThreads, dense::KLayout<D>::kAlloc, stream>>>(
+    for (int i = 0; i < n; ++i) {
+      units[i] = (seqs[i].w + 127) / 128;
+      flat[i] = p.causal ? 0 : seqs[i].y;
+    }
+    fill_dense_seqs(&table, seqs, units, flat, n);
+    kk<<<(unsigned)k_units, dense::kThreads, dense::KLayout<D>::kAlloc, stream>>>(
         m[0], m[1], m[2], m[3], p, table);
   }
   return cudaGetLastError() == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;

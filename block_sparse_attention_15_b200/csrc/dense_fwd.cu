@@ -21,7 +21,7 @@
 // not overlap the products), so 1457 per tile bound the rate; TMEM is full (S and
 // O of two slots), which keeps Q out of it.
 //
-// Persistent grid, one CTA per SM, 768 threads:
+// One CTA per SM, 768 threads, item after item:
 //   warp 0      K and V tiles (one ring of NST stages, K(j) then V(j))
 //   warp 1      TMEM owner; one thread issues PV(j) and S(j+1) of slot 0, then of
 //               slot 1, back to back, having waited for their tiles before
@@ -72,6 +72,8 @@ struct Item {
 };
 __device__ __forceinline__ const Slot& slot_of(const Item& x, int s) { return s ? x.slot1 : x.slot0; }
 
+using Items = ItemRing<Item, 2>;
+
 template <int D>
 struct Layout {
   static constexpr int DH = D / 64;
@@ -81,13 +83,14 @@ struct Layout {
   static constexpr uint32_t kRingOff = kQOff + 2 * kTile;
   static constexpr uint32_t kInvLOff = kRingOff + NST * kTile;  // [2][128] f32
   static constexpr uint32_t kItemOff = kInvLOff + 2u * 128u * 4u;
-  static constexpr uint32_t kBarOff = kItemOff + (uint32_t)sizeof(ItemRing<Item>);
+  static constexpr uint32_t kBarOff = kItemOff + (uint32_t)sizeof(Items);
   static constexpr int kQFull = 0, kQEmpty = 2, kFull = 4, kEmpty = kFull + NST,
                        kPre = kEmpty + NST, kSFull = kPre + NST, kPFull = kSFull + 2,
                        kLFull = kPFull + 2, kOFull = kLFull + 2, kOEmpty = kOFull + 2,
-                       kItFull = kOEmpty + 2, kItEmpty = kItFull + kItemSlots, kNumBars = kItEmpty + kItemSlots;
+                       kItFull = kOEmpty + 2, kItEmpty = kItFull + Items::kSlots, kTake = kItEmpty + Items::kSlots, kLoaded = kTake + 1, kNumBars = kLoaded + 1;
   static constexpr uint32_t kMiscOff = kBarOff + 8u * kNumBars;  // tmem address, abort flag
-  static constexpr uint32_t kAlloc = kMiscOff + 16u;
+  static constexpr uint32_t kTakeOff = (kMiscOff + 16u + 15u) & ~15u;
+  static constexpr uint32_t kAlloc = kTakeOff + 16u;
   static_assert(kAlloc <= 227u * 1024u, "shared memory");
 };
 
@@ -128,6 +131,14 @@ __device__ __forceinline__ Item load_item(const DenseParams& p, const DenseSeqs&
   return x;
 }
 
+// Row r of a slot, which sees no key.
+template <int D>
+__device__ __forceinline__ void unseen_row(const DenseParams& p, const Slot& sl, int r) {
+  __nv_bfloat16* to = p.out + sl.head * p.out_st.h + (long long)(sl.row0 + r) * p.out_st.s;
+  for (int e = 0; e < D; e += 8) *reinterpret_cast<uint4*>(to + e) = make_uint4(0u, 0u, 0u, 0u);
+  if (p.lse) p.lse[sl.head * p.lse_seq + sl.row0 + r] = -INFINITY;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -142,21 +153,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   float* inv_l = reinterpret_cast<float*>(smem + L::kInvLOff);
-  ItemRing<Item>* items = reinterpret_cast<ItemRing<Item>*>(smem + L::kItemOff);
+  Items* items = reinterpret_cast<Items*>(smem + L::kItemOff);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
 
   const int tid = threadIdx.x;
   const int warp = tid / 32, lane = tid % 32;
-  const int cta = blockIdx.x, grid = gridDim.x;
 
   if (warp == 0) {
     for (int i = lane; i < L::kNumBars; i += 32) {
       // a TMA transaction, a commit or one thread's arrival, except where warps arrive
       const uint32_t count = (i >= L::kPFull && i < L::kOFull)    ? 8u  // a slot's softmax
                              : (i >= L::kOEmpty && i < L::kItFull) ? 4u  // the epilogue
-                             : i >= L::kItEmpty                    ? kThreads / 32 - 1u
+                             : (i >= L::kItEmpty && i < L::kTake)  ? kThreads / 32 - 1u
                                                                    : 1u;
       mbar_init(bars + i, count);
     }
@@ -201,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             load_rows(dst + dh * 16384, is_v ? &tm_v : &tm_k, is_v ? p.v_ax : p.k_ax, full, dh * 64, x.kv0 + key,
                       x.hk, 0, pol);
         }
+        mbar_arrive(bars + L::kLoaded);
       }
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
     }
@@ -211,10 +222,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t n = 0, cs0 = 0, cs1 = 0;  // items; Q tiles of the slots
     bool ok = true;
     Item x;
-    for (int w = 0, it; ok && (it = wave_item(w, cta, grid), w * grid < p.n_work); ++w) {
-      if (it >= p.n_work) continue;
+    Takeover take{bars + L::kTake, reinterpret_cast<uint4*>(smem + L::kTakeOff), 0};
+    for (int it = blockIdx.x; ok && it >= 0; it = ok ? take.answer(abort_flag, p.status) : -1) {
       x = load_item(p, seqs, it);
-      ok = put_item(items, bars + L::kItFull, bars + L::kItEmpty, n++, x, lane, abort_flag, p.status);
+      if (x.n == 0) {
+        // nothing to multiply: not handed on (the products look one item ahead, and
+        // must not wait for one past those that the others have taken)
+#pragma unroll 1
+        for (int s = 0; s < 2; ++s) {
+          const Slot& sl = slot_of(x, s);
+          for (int r = lane; r < sl.rows; r += 32) unseen_row<D>(p, sl, r);
+        }
+        take.ask(lane);
+        continue;
+      }
+      ok = put_item(items, bars + L::kItFull, bars + L::kItEmpty, n, x, lane, abort_flag, p.status);
 #pragma unroll 1
       for (int s = 0; ok && s < 2; ++s) {
         const Slot& sl = slot_of(x, s);
@@ -233,6 +255,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
+      // ask for more when this item's last tiles are on their way, not earlier: what
+      // a CTA holds no other can take
+      ok = ok && warp_wait(bars + L::kLoaded, n++ & 1, abort_flag, p.status);
+      if (ok) take.ask(lane);
     }
     x.n = -1;
     if (ok) put_item(items, bars + L::kItFull, bars + L::kItEmpty, n, x, lane, abort_flag, p.status);
@@ -241,7 +267,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t g = 0, pre = 0, n_got = 0;  // ring tiles so far; phase bit per stage
     Item x;
     while (next(n_got, x)) {
-      if (x.n == 0) continue;
       g += 2 * x.n;
       const int len = x.kv_len - 128 * (x.n - 1);  // keys from the last loaded tile on
       if (len >= 128) continue;
@@ -282,11 +307,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (s == 1 || j >= x.slot1.n) umma_commit(bars + L::kEmpty + (int)((gx + 2 * j) % NST));
         if (j == slot_of(x, s).n - 1) umma_commit(bars + L::kQEmpty + s);
       };
-      auto next_one = [&](Item& x) {  // the next item with key tiles
-        bool r;
-        do r = get_item_one(items, bars + L::kItFull, bars + L::kItEmpty, n_got, x, abort_flag, p.status);
-        while (r && x.n == 0);
-        return r;
+      auto next_one = [&](Item& x) {
+        return get_item_one(items, bars + L::kItFull, bars + L::kItEmpty, n_got, x, abort_flag, p.status);
       };
       Item x, y;
       bool have = next_one(x);
@@ -299,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         do_s(x, s, 0, 0);
       }
       while (ok && have) {
-        const bool more = next_one(y);
+        bool more = false;
         const uint32_t g_next = g + 2 * x.n;
         const int n1 = x.slot1.n;
 #pragma unroll 1
@@ -320,6 +342,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool last = j + 1 == ns;
           const uint32_t gv = g + 2 * j + 1;
           wait_stage(gv);
+          // (the item's tiles are all here, so that the next one was asked for)
+          if (s == 0 && last && ok) more = next_one(y);
           if (!last) before_s(s, j + 1, g);
           // the epilogue has emptied this slot's O
           const uint32_t done = s ? d1 : d0;
@@ -417,16 +441,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = x.slot1.n < x.slot0.n ? 1 - k : k;
         const Slot sl = slot_of(x, s);
         if (sl.rows == 0) continue;
-        __nv_bfloat16* orow = p.out + sl.head * p.out_st.h + (long long)(sl.row0 + row) * p.out_st.s;
         const bool real = row < sl.rows;
         if (sl.n == 0) {
-          // rows that see no key
-          if (real) {
-            for (int e = 0; e < D; e += 8) *reinterpret_cast<uint4*>(orow + e) = make_uint4(0u, 0u, 0u, 0u);
-            if (p.lse) p.lse[sl.head * p.lse_seq + sl.row0 + row] = -INFINITY;
-          }
+          if (real) unseen_row<D>(p, sl, row);
           continue;
         }
+        __nv_bfloat16* orow = p.out + sl.head * p.out_st.h + (long long)(sl.row0 + row) * p.out_st.s;
         const uint32_t ph = (s ? cs1 : cs0) & 1;
         cs0 += s ^ 1;
         cs1 += s;
@@ -504,25 +524,33 @@ int DenseBatch::chunk(int i0, int4* seqs) const {
   return m;
 }
 
-void fill_dense_seqs(DenseSeqs* t, const int4* seqs, const int* units, int n) {
+void fill_dense_seqs(DenseSeqs* t, const int4* seqs, const int* units, const int* flat_cost, int n) {
   int order[kDenseMaxSeqs];
   int m = 0;
   for (int i = 0; i < n; ++i)
     if (units[i] > 0) order[m++] = i;
-  std::stable_sort(order, order + m, [&](int a, int b) { return units[a] > units[b]; });
+  std::stable_sort(order, order + m, [&](int a, int b) {
+    if ((flat_cost[a] > 0) != (flat_cost[b] > 0)) return flat_cost[a] > 0;
+    return flat_cost[a] > 0 ? flat_cost[a] > flat_cost[b] : units[a] > units[b];
+  });
   t->n = m;
+  t->n_flat = 0;
+  int at = 0;
   for (int r = 0; r < m; ++r) {
     t->seq[r] = seqs[order[r]];
     t->units[r] = units[order[r]];
+    if (flat_cost[order[r]] > 0) {
+      t->first[r] = at;
+      at += t->units[r];
+      t->n_flat = r + 1;
+    }
   }
-  int items = 0;
-  t->first[0] = 0;
-  for (int r = 1; r <= m; ++r) {
-    t->first[r] = items;
-    items += r * (t->units[r - 1] - (r < m ? t->units[r] : 0));
+  t->first[t->n_flat] = at;
+  for (int k = t->n_flat + 1; k <= m; ++k) {
+    t->first[k] = at;
+    at += (k - t->n_flat) * (t->units[k - 1] - (k < m ? t->units[k] : 0));
   }
-  t->first[m + 1] = items;
-  t->n_items = items;
+  t->n_units = at;
 }
 
 template <int D>
@@ -533,10 +561,8 @@ static int launch_dense_fwd_t(DenseParams p, const DenseSeqs& seqs, const CUtens
   static KernelReady ready;
   const int rc = ready.check(reinterpret_cast<const void*>(kern), (int)L::kAlloc);
   if (rc != VSA_OK) return rc;
-  p.n_work = seqs.n_items * p.Hkv;
-  if (p.n_work == 0) return VSA_OK;
-  const int sms = device_sm_count();
-  const int grid = p.n_work < sms ? p.n_work : sms;
+  const int grid = seqs.n_units * p.Hkv;
+  if (grid == 0) return VSA_OK;
   kern<<<(unsigned)grid, dense::kThreads, L::kAlloc, stream>>>(mq, mk, mv, p, seqs);
   return cudaGetLastError() == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
 }
@@ -555,7 +581,7 @@ int launch_dense_fwd(const DenseParams& p_in, const DenseTensors& t, const Dense
     return VSA_ERR_CUDA;
   for (int i0 = 0; i0 < b.n; i0 += kDenseMaxSeqs) {
     int4 seqs[kDenseMaxSeqs];
-    int units[kDenseMaxSeqs];
+    int units[kDenseMaxSeqs], flat[kDenseMaxSeqs];
     const int n = b.chunk(i0, seqs);
     long long slots = 0;
     for (int i = 0; i < n; ++i) slots += (seqs[i].y + 127LL) / 128 * p.Hq;
@@ -564,10 +590,13 @@ int launch_dense_fwd(const DenseParams& p_in, const DenseTensors& t, const Dense
     // under the other's products; with no more row tiles than SMs one tile per
     // item spreads them over twice as many SMs instead.
     p.slots = slots > device_sm_count() ? 2 : 1;
-    for (int i = 0; i < n; ++i)
+    for (int i = 0; i < n; ++i) {
       units[i] = ((seqs[i].y + 127) / 128 * p.group + p.slots - 1) / p.slots;
+      // behind cached keys the first rows, too, have many to see
+      flat[i] = !p.causal || seqs[i].w > seqs[i].y ? seqs[i].w : 0;
+    }
     DenseSeqs table;
-    fill_dense_seqs(&table, seqs, units, n);
+    fill_dense_seqs(&table, seqs, units, flat, n);
     const int rc = D == 128 ? launch_dense_fwd_t<128>(p, table, mq, mk, mv, stream)
                             : launch_dense_fwd_t<64>(p, table, mq, mk, mv, stream);
     if (rc != VSA_OK) return rc;

@@ -16,14 +16,15 @@ namespace vsa {
 constexpr int kDenseMaxSeqs = 256;
 
 // Packed sequences of one launch, passed by value (so a captured launch keeps
-// its lengths), sorted by units descending.  5.1 KB of the kernel's 32 KB of
-// parameters.
+// its lengths).  6.2 KB of the kernel's 32 KB of parameters.
 struct DenseSeqs {
-  int n;
-  int n_items;                      // units of all sequences
+  int n, n_flat;
+  int n_units;                      // of all sequences (what a unit is, each kernel says)
   int4 seq[kDenseMaxSeqs];          // first q row, q rows, first kv row, kv rows
-  int units[kDenseMaxSeqs];         // units of the sequence (what a unit is, each kernel says)
-  int first[kDenseMaxSeqs + 2];     // items before the ranks that exactly r sequences have
+  int units[kDenseMaxSeqs];         // units of the sequence
+  // [0, n_flat): units before the sequence; [n_flat]: units of the flat ones;
+  // [n_flat + r]: units before the ranks that exactly r of the others have
+  int first[kDenseMaxSeqs + 1];
 };
 
 struct DenseParams {
@@ -35,7 +36,6 @@ struct DenseParams {
   int Hq, Hkv, group;               // group = Hq / Hkv
   int causal;
   int slots;                        // row tiles per work item: 1 or 2
-  int n_work;                 // work items of the launch
   float scale_log2;
   int* status;
 };
@@ -63,9 +63,10 @@ struct KernelReady {
 };
 
 int device_sm_count();
-// Sorts sequences by units (dropping those without) and fills the table;
-// `units` in the order of `seqs`, their sum below 2^30.
-void fill_dense_seqs(DenseSeqs* t, const int4* seqs, const int* units, int n);
+// Fills the table (dropping sequences without units).  `flat_cost` of a sequence:
+// the cost of each of its units where they cost about the same, else 0; all in
+// the order of `seqs`, the units' sum below 2^30.
+void fill_dense_seqs(DenseSeqs* t, const int4* seqs, const int* units, const int* flat_cost, int n);
 int launch_dense_fwd(const DenseParams& p, const DenseTensors& t, const DenseBatch& b, int D,
                      cudaStream_t stream);
 
@@ -79,7 +80,6 @@ struct DenseBwdParams {
   TmaAxes q_ax, k_ax, v_ax, do_ax, o_ax;
   int Hq, Hkv, group;
   int causal;
-  int n_work;
   float scale, scale_log2;
   int* status;
 };

@@ -64,6 +64,8 @@ struct Piece {
   long long part; // partial-result number within its kind
 };
 
+using PieceRing = dense::ItemRing<Piece, 4>;
+
 template <int D>
 struct Layout {
   static constexpr int DH = D / 64;
@@ -73,12 +75,12 @@ struct Layout {
   static constexpr uint32_t kRingOff = kQOff + 2 * kTile;
   static constexpr uint32_t kMLOff = kRingOff + NST * kTile;  // [2 slots][m, l][128] f32
   static constexpr uint32_t kItemOff = kMLOff + 2048u;
-  static constexpr uint32_t kBarOff = kItemOff + (uint32_t)sizeof(dense::ItemRing<Piece>);
+  static constexpr uint32_t kBarOff = kItemOff + (uint32_t)sizeof(PieceRing);
   // kQFull and kQFree alternate between pieces: one piece may be ahead of a waiter
   static constexpr int kQFull = 0, kQFree = 2, kFull = 4, kEmpty = kFull + NST, kPre = kEmpty + NST,
                        kSFull = kPre + NST, kPFull = kSFull + 2, kOFull = kPFull + 2,
                        kOEmpty = kOFull + 2, kLFull = kOEmpty + 2, kItFull = kLFull + 2,
-                       kItEmpty = kItFull + dense::kItemSlots, kNumBars = kItEmpty + dense::kItemSlots;
+                       kItEmpty = kItFull + PieceRing::kSlots, kNumBars = kItEmpty + PieceRing::kSlots;
   static constexpr uint32_t kMiscOff = kBarOff + 8u * kNumBars;
   static constexpr uint32_t kAlloc = kMiscOff + 16u;
   static_assert(kAlloc <= 227u * 1024u, "shared memory");
@@ -325,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the joining kernel may be set up while this one runs
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   float* ml = reinterpret_cast<float*>(smem + L::kMLOff);
-  dense::ItemRing<Piece>* items = reinterpret_cast<dense::ItemRing<Piece>*>(smem + L::kItemOff);
+  PieceRing* items = reinterpret_cast<PieceRing*>(smem + L::kItemOff);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
