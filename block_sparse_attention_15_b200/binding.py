@@ -8,9 +8,11 @@ shared library is missing or a call fails, these functions raise.
 
 from __future__ import annotations
 
+import array
 import ctypes
 import math
 import os
+import struct
 
 import numpy as np
 import torch
@@ -57,7 +59,6 @@ class VsaPrefixLayout(ctypes.Structure):
 
 
 _PL = ctypes.POINTER(VsaLayout)
-_PDL = ctypes.POINTER(VsaDenseLayout)
 VSA_LAYOUT_BHSD, VSA_LAYOUT_BSHD = 0, 1
 
 # name -> (restype, argtypes); mirrors include/vsa.h
@@ -108,14 +109,14 @@ SIGNATURES = {
                                  [_c_int] * 3 + [_c_void_p, _c_void_p, _c_int, _c_float,
                                                  _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                                  _c_void_p, _c_size_t, _c_void_p]),
-    "dense_attn_varlen": (_c_int, [_c_void_p] * 3 + [_PDL, _P32, _P32] + [_c_int] * 4 +
+    "dense_attn_varlen": (_c_int, [_c_void_p] * 6 + [_c_int] * 4 +
                           [_c_int64, _c_int64, _c_int, _c_float, _c_void_p, _c_void_p, _c_void_p]),
     "dense_attn_varlen_backward_workspace_size": (_c_size_t, [_c_int, _c_int64]),
-    "dense_attn_varlen_backward": (_c_int, [_c_void_p] * 6 + [_PDL, _P32, _P32] + [_c_int] * 4 +
+    "dense_attn_varlen_backward": (_c_int, [_c_void_p] * 9 + [_c_int] * 4 +
                                    [_c_int64, _c_int64, _c_int, _c_float, _c_void_p, _c_void_p, _c_void_p,
                                     _c_void_p, _c_size_t, _c_void_p]),
     "shared_prefix_attn_workspace_size": (_c_size_t, [_c_int] * 5 + [_c_int64] * 2),
-    "shared_prefix_attn": (_c_int, [_c_void_p] * 6 + [ctypes.POINTER(VsaPrefixLayout)] + [_c_int] * 5 +
+    "shared_prefix_attn": (_c_int, [_c_void_p] * 7 + [_c_int] * 5 +
                            [_c_int64, _c_int64, _c_float, _c_void_p, _c_void_p, _c_void_p, _c_size_t,
                             _c_void_p]),
     "build_vsa_metadata": (_c_int, [_c_int] * 6 + [_P64, _P64, _P32, _P64, _P64, _P32]),
@@ -178,19 +179,16 @@ def _require(t, dtype, name, device=True):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _require_view(t, name, empty=False):
+def _require_view(t, name):
     """A bf16 CUDA tensor whose last (head-dim) axis is contiguous and whose
     other strides are multiples of 8 elements (any layout: BHSD, BSHD, a
-    slice of a fused tensor, a transposed view); where `empty` allows it, one
-    without elements, whatever its strides."""
+    slice of a fused tensor, a transposed view)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if empty and t.dim() == 4 and t.numel() == 0:
-        return
     if t.dim() != 4 or t.stride(3) != 1:
         raise ValueError(f"{name} must be a 4-D view with a contiguous last axis")
     for ax in range(3):
@@ -603,10 +601,19 @@ def block_sparse_attn_varlen_backward(q, k, v, out, dout, lse, cu_seqlens_q, cu_
     return dq, dk, dv
 
 
-def _require_rows(t, name):
-    """A bf16 CUDA [H, rows, D] view: head dim contiguous, other strides
-    multiples of 8 elements (token-major memory transposed, a slice of a
-    fused tensor)."""
+# The dense entries are called once per layer and token, and their kernels may
+# take less time than Python's part of a call: each tensor is looked at once,
+# and the structures the library takes are packed as bytes.
+_LAYOUT8 = struct.Struct("24q")   # vsa_dense_layout
+_LAYOUT6 = struct.Struct("18q")   # vsa_prefix_layout
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _rows(t, name):
+    """(H, rows, D, head stride, row stride, address) of a bf16 CUDA [H, rows, D]
+    view: head dim contiguous, other strides multiples of 8 elements
+    (token-major memory transposed, a slice of a fused tensor)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != torch.bfloat16:
@@ -615,31 +622,54 @@ def _require_rows(t, name):
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dim() != 3:
         raise ValueError(f"{name} must be a 3-D [H, rows, D] view")
-    if t.numel() == 0:
-        return
-    if t.stride(2) != 1 or any(t.shape[a] > 1 and (t.stride(a) <= 0 or t.stride(a) % 8) for a in (0, 1)):
-        raise ValueError(f"{name}: strides {t.stride()} must be positive multiples of 8 elements, "
+    h, r, d = t.shape
+    if not (h and r and d):
+        return h, r, d, 0, 0, t.data_ptr()
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (h > 1 and (s0 <= 0 or s0 & 7)) or (r > 1 and (s1 <= 0 or s1 & 7)):
+        raise ValueError(f"{name}: strides {(s0, s1, s2)} must be positive multiples of 8 elements, "
                          "the last 1")
-    if t.data_ptr() % 16:
+    ptr = t.data_ptr()
+    if ptr & 15:
         raise ValueError(f"{name} must start on a 16-byte boundary")
+    return h, r, d, s0, s1, ptr
 
 
-def _same_device(dev, **tensors):
+def _heads(t, name):
+    """(shape, strides, address) of a bf16 CUDA [B, H, S, D] view, likewise."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be a 4-D [B, H, S, D] view")
+    shape, st = t.shape, t.stride()
+    if 0 in shape:
+        return shape, (0, 0, 0), t.data_ptr()
+    if st[3] != 1 or any(n > 1 and (x <= 0 or x & 7) for n, x in zip(shape[:3], st)):
+        raise ValueError(f"{name}: strides {st} must be positive multiples of 8 elements, the last 1")
+    ptr = t.data_ptr()
+    if ptr & 15:
+        raise ValueError(f"{name} must start on a 16-byte boundary")
+    return shape, st[:3], ptr
+
+
+def _same_device(index, **tensors):
     for n, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{n} is on {t.device}, q on {dev}")
-
-
-def _strides_rows(t):
-    return VsaStrides(0, t.stride(0), t.stride(1))
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{n} is on {t.device}, q on cuda:{index}")
 
 
 class _Launch:
     """The device and stream of a call: the tensors' device becomes the current
-    one, and memory allocated inside belongs to the stream the kernels run on."""
+    one, and memory allocated inside belongs to the stream the kernels run on.
+    Enters as that stream's handle."""
 
-    def __init__(self, dev, stream):
-        self._dev = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    def __init__(self, index, stream):
+        self._index = index
+        self._dev = None if torch.cuda.current_device() == index else torch.cuda.device(index)
         self._ctx = None if stream is None else torch.cuda.stream(stream)
 
     def __enter__(self):
@@ -647,7 +677,7 @@ class _Launch:
             self._dev.__enter__()
         if self._ctx is not None:
             self._ctx.__enter__()
-        return _c_void_p(torch.cuda.current_stream().cuda_stream)
+        return _raw_stream(self._index)
 
     def __exit__(self, *exc):
         if self._ctx is not None:
@@ -656,19 +686,36 @@ class _Launch:
             self._dev.__exit__(*exc)
 
 
+def _cumulative(xs, name):
+    """Host int32 copy of cumulative lengths, an array."""
+    if isinstance(xs, (list, tuple)):
+        try:
+            return array.array("i", xs)
+        except TypeError:
+            pass  # tensors' or arrays' elements
+    a = np.asarray(xs, dtype=np.int32)
+    if a.ndim != 1:
+        raise ValueError(f"{name} must be a 1-D sequence")
+    return array.array("i", a.tolist())
+
+
 def _dense_common(q, k, v, cu_seqlens_q, cu_seqlens_kv):
-    for t, n in ((q, "q"), (k, "k"), (v, "v")):
-        _require_rows(t, n)
-    Hq, Sq, D = q.shape
-    Hkv, Skv = k.shape[0], k.shape[1]
-    if v.shape != k.shape or k.shape[2] != D:
+    qi, ki, vi = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
+    if vi[:3] != ki[:3] or ki[2] != qi[2]:
         raise ValueError("k and v must be [Hkv, kv_rows, D] with q's D")
-    _same_device(q.device, k=k, v=v)
-    cq, cq_p = _host_i32(cu_seqlens_q)
-    ck, ck_p = _host_i32(cu_seqlens_kv)
-    if cq.ndim != 1 or cq.shape != ck.shape or len(cq) < 1:
+    cq, ck = _cumulative(cu_seqlens_q, "cu_seqlens_q"), _cumulative(cu_seqlens_kv, "cu_seqlens_kv")
+    if len(cq) != len(ck) or not cq:
         raise ValueError("cu_seqlens_q and cu_seqlens_kv must have n_seqs + 1 entries each")
-    return Hq, Hkv, D, Sq, Skv, cq, cq_p, ck, ck_p
+    return qi, ki, vi, cq, ck
+
+
+def _fresh(like, cu):
+    """An output like a packed tensor, its rows past the last sequence 0."""
+    t = torch.empty_like(like)
+    rows, tail = like.shape[1], cu[-1]
+    if 0 <= tail < rows:
+        t[:, tail:].zero_()
+    return t
 
 
 def dense_attn_varlen(q, k, v, cu_seqlens_q, cu_seqlens_kv, *, causal: bool = True,
@@ -685,28 +732,26 @@ def dense_attn_varlen(q, k, v, cu_seqlens_q, cu_seqlens_kv, *, causal: bool = Tr
     allocated here).  With ``return_lse`` also returns the fp32 [Hq, q_rows]
     natural-log log-sum-exp (-inf where a row sees no key), which
     :func:`dense_attn_varlen_backward` takes."""
-    Hq, Hkv, D, Sq, Skv, cq, cq_p, ck, ck_p = _dense_common(q, k, v, cu_seqlens_q, cu_seqlens_kv)
-    L = lib()
-    with _Launch(q.device, stream) as st:
-        tail = int(cq[-1]) if 0 <= cq[-1] <= Sq else Sq
+    qi, ki, vi, cq, ck = _dense_common(q, k, v, cu_seqlens_q, cu_seqlens_kv)
+    index = q.get_device()
+    _same_device(index, k=k, v=v, out=out)
+    with _Launch(index, stream) as st:
         if out is None:
-            out = torch.empty_like(q)
-            if tail < Sq:
-                out[:, tail:].zero_()
-        else:
-            _require_rows(out, "out")
-            _same_device(q.device, out=out)
-            if out.shape != q.shape:
-                raise ValueError("out must be shaped like q")
+            out = _fresh(q, cq)
+        elif out.shape != q.shape:
+            raise ValueError("out must be shaped like q")
+        oi = _rows(out, "out")
         lse = None
         if return_lse:
-            lse = torch.empty((Hq, Sq), dtype=torch.float32, device=q.device)
-            if tail < Sq:
-                lse[:, tail:].zero_()
-        lay = VsaDenseLayout(_strides_rows(q), _strides_rows(k), _strides_rows(v), _strides_rows(out))
-        _check("dense_attn_varlen", L.dense_attn_varlen(
-            _ptr(q), _ptr(k), _ptr(v), ctypes.byref(lay), cq_p, ck_p, len(cq) - 1, Hq, Hkv, D, Sq, Skv,
-            1 if causal else 0, float(scale) if scale is not None else 0.0, _ptr(out), _ptr(lse), st))
+            lse = torch.empty((qi[0], qi[1]), dtype=torch.float32, device=q.device)
+            if 0 <= cq[-1] < qi[1]:
+                lse[:, cq[-1]:].zero_()
+        lay = _LAYOUT8.pack(0, qi[3], qi[4], 0, ki[3], ki[4], 0, vi[3], vi[4], 0, oi[3], oi[4],
+                            0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+        _check("dense_attn_varlen", lib().dense_attn_varlen(
+            qi[5], ki[5], vi[5], lay, cq.buffer_info()[0], ck.buffer_info()[0], len(cq) - 1, qi[0], ki[0], qi[2],
+            qi[1], ki[1], 1 if causal else 0, 0.0 if scale is None else float(scale), oi[5],
+            None if lse is None else lse.data_ptr(), st))
     return (out, lse) if return_lse else out
 
 
@@ -718,42 +763,35 @@ def dense_attn_varlen_backward(q, k, v, out, dout, lse, cu_seqlens_q, cu_seqlens
     ``dout`` and the gradients may be strided views like q and k.  dk and dv sum
     over the query heads of a key head.  Rows of given gradients past the last
     sequence are left as they were (0 where they are allocated here)."""
-    Hq, Hkv, D, Sq, Skv, cq, cq_p, ck, ck_p = _dense_common(q, k, v, cu_seqlens_q, cu_seqlens_kv)
-    for t, n in ((out, "out"), (dout, "dout")):
-        _require_rows(t, n)
-        if t.shape != q.shape:
-            raise ValueError(f"{n} must be shaped like q")
+    qi, ki, vi, cq, ck = _dense_common(q, k, v, cu_seqlens_q, cu_seqlens_kv)
+    oi, gi = _rows(out, "out"), _rows(dout, "dout")
+    if oi[:3] != qi[:3] or gi[:3] != qi[:3]:
+        raise ValueError("out and dout must be shaped like q")
     _require(lse, torch.float32, "lse")
-    if lse.shape != (Hq, Sq):
-        raise ValueError(f"lse must be [Hq, q_rows] = {(Hq, Sq)}")
-    given = {"dq": dq, "dk": dk, "dv": dv}
-    for n, like in (("dq", q), ("dk", k), ("dv", v)):
-        if given[n] is not None:
-            _require_rows(given[n], n)
-            if given[n].shape != like.shape:
-                raise ValueError(f"{n} must be shaped like {n[1]}")
-    _same_device(q.device, out=out, dout=dout, lse=lse, workspace=workspace, **given)
+    if lse.shape != (qi[0], qi[1]):
+        raise ValueError(f"lse must be [Hq, q_rows] = {(qi[0], qi[1])}")
+    index = q.get_device()
+    _same_device(index, k=k, v=v, out=out, dout=dout, lse=lse, workspace=workspace, dq=dq, dk=dk, dv=dv)
+    for n, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        if t is not None and t.shape != like.shape:
+            raise ValueError(f"{n} must be shaped like {n[1]}")
     L = lib()
-    with _Launch(q.device, stream) as st:
-        grads = []
-        for n, like, cu in (("dq", q, cq), ("dk", k, ck), ("dv", v, ck)):
-            g = given[n]
-            if g is None:
-                g = torch.empty_like(like)
-                rows = like.shape[1]
-                tail = int(cu[-1]) if 0 <= cu[-1] <= rows else rows
-                if tail < rows:
-                    g[:, tail:].zero_()
-            grads.append(g)
+    with _Launch(index, stream) as st:
+        dq = _fresh(q, cq) if dq is None else dq
+        dk = _fresh(k, ck) if dk is None else dk
+        dv = _fresh(v, ck) if dv is None else dv
+        a, b, c = _rows(dq, "dq"), _rows(dk, "dk"), _rows(dv, "dv")
         if workspace is None:
-            need = L.dense_attn_varlen_backward_workspace_size(Hq, Sq)
+            need = L.dense_attn_varlen_backward_workspace_size(qi[0], qi[1])
             workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-        lay = VsaDenseLayout(*[_strides_rows(t) for t in (q, k, v, out, dout, *grads)])
+        lay = _LAYOUT8.pack(0, qi[3], qi[4], 0, ki[3], ki[4], 0, vi[3], vi[4], 0, oi[3], oi[4],
+                            0, gi[3], gi[4], 0, a[3], a[4], 0, b[3], b[4], 0, c[3], c[4])
         _check("dense_attn_varlen_backward", L.dense_attn_varlen_backward(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(dout), _ptr(lse), ctypes.byref(lay), cq_p, ck_p,
-            len(cq) - 1, Hq, Hkv, D, Sq, Skv, 1 if causal else 0, float(scale) if scale is not None else 0.0,
-            _ptr(grads[0]), _ptr(grads[1]), _ptr(grads[2]), _ptr(workspace), workspace.numel(), st))
-    return tuple(grads)
+            qi[5], ki[5], vi[5], oi[5], gi[5], lse.data_ptr(), lay, cq.buffer_info()[0], ck.buffer_info()[0],
+            len(cq) - 1, qi[0], ki[0], qi[2], qi[1], ki[1], 1 if causal else 0,
+            0.0 if scale is None else float(scale), a[5], b[5], c[5], workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), st))
+    return dq, dk, dv
 
 
 def shared_prefix_attn(q, k_prefix, v_prefix, k_suffix, v_suffix, suffix_lens, *,
@@ -770,40 +808,37 @@ def shared_prefix_attn(q, k_prefix, v_prefix, k_suffix, v_suffix, suffix_lens, *
     [B], read on the device.  Token t sees the prefix and its first
     ``suffix_lens[b] - T + 1 + t`` suffix keys.  Returns [B, Hq, T, D], with
     ``return_lse`` also the fp32 [B, Hq, T] natural-log log-sum-exp."""
-    for t, n in ((q, "q"), (k_suffix, "k_suffix"), (v_suffix, "v_suffix")):
-        _require_view(t, n, empty=True)
-    for t, n in ((k_prefix, "k_prefix"), (v_prefix, "v_prefix")):
-        _require_rows(t, n)
+    (B, Hq, T, D), qs, qp = _heads(q, "q")
+    ks_shape, kss, ksp = _heads(k_suffix, "k_suffix")
+    vs_shape, vss, vsp = _heads(v_suffix, "v_suffix")
+    kp, vp = _rows(k_prefix, "k_prefix"), _rows(v_prefix, "v_prefix")
     _require(suffix_lens, torch.int32, "suffix_lens")
-    B, Hq, T, D = q.shape
-    Hkv, P = k_prefix.shape[:2]
-    cap = k_suffix.shape[2]
-    if k_prefix.shape != (Hkv, P, D) or v_prefix.shape != k_prefix.shape:
+    Hkv, P, cap = kp[0], kp[1], ks_shape[2]
+    if vp[:3] != kp[:3] or kp[2] != D:
         raise ValueError("k_prefix and v_prefix must be [Hkv, P, D] with q's D")
-    if k_suffix.shape != (B, Hkv, cap, D) or v_suffix.shape != k_suffix.shape:
+    if ks_shape != (B, Hkv, cap, D) or vs_shape != ks_shape:
         raise ValueError(f"k_suffix and v_suffix must be [B, Hkv, capacity, D] = {(B, Hkv, cap, D)}")
     if suffix_lens.shape != (B,):
         raise ValueError(f"suffix_lens must be [B] = [{B}]")
-    _same_device(q.device, k_prefix=k_prefix, v_prefix=v_prefix, k_suffix=k_suffix, v_suffix=v_suffix,
+    index = q.get_device()
+    _same_device(index, k_prefix=k_prefix, v_prefix=v_prefix, k_suffix=k_suffix, v_suffix=v_suffix,
                  suffix_lens=suffix_lens, out=out, workspace=workspace)
     L = lib()
-    with _Launch(q.device, stream) as st:
+    with _Launch(index, stream) as st:
         if out is None:
             out = torch.empty_like(q)
-        else:
-            _require_view(out, "out", empty=True)
-            if out.shape != q.shape:
-                raise ValueError("out must be shaped like q")
+        elif out.shape != q.shape:
+            raise ValueError("out must be shaped like q")
+        _, os_, op = _heads(out, "out")
         lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device) if return_lse else None
-        need = L.shared_prefix_attn_workspace_size(B, Hq, Hkv, T, D, P, cap)
         if workspace is None:
+            need = L.shared_prefix_attn_workspace_size(B, Hq, Hkv, T, D, P, cap)
             workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-        lay = VsaPrefixLayout(_strides_bhsd(q), _strides_bhsd(out), _strides_rows(k_prefix),
-                              _strides_rows(v_prefix), _strides_bhsd(k_suffix), _strides_bhsd(v_suffix))
+        lay = _LAYOUT6.pack(*qs, *os_, 0, kp[3], kp[4], 0, vp[3], vp[4], *kss, *vss)
         _check("shared_prefix_attn", L.shared_prefix_attn(
-            _ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(k_suffix), _ptr(v_suffix), _ptr(suffix_lens),
-            ctypes.byref(lay), B, Hq, Hkv, T, D, P, cap, float(scale) if scale is not None else 0.0,
-            _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), st))
+            qp, kp[5], vp[5], ksp, vsp, suffix_lens.data_ptr(), lay, B, Hq, Hkv, T, D, P, cap,
+            0.0 if scale is None else float(scale), op, None if lse is None else lse.data_ptr(),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), st))
     return (out, lse) if return_lse else out
 
 
