@@ -111,7 +111,8 @@ SIGNATURES = {
                                                  _c_void_p, _c_size_t, _c_void_p]),
     "dense_attn_varlen": (_c_int, [_c_void_p] * 6 + [_c_int] * 4 +
                           [_c_int64, _c_int64, _c_int, _c_float, _c_void_p, _c_void_p, _c_void_p]),
-    "dense_attn_varlen_backward_workspace_size": (_c_size_t, [_c_int, _c_int64]),
+    "dense_attn_varlen_backward_workspace_size": (_c_size_t, [_c_void_p] * 2 + [_c_int] * 4 + [_c_int64] * 2 +
+                                                  [_c_int]),
     "dense_attn_varlen_backward": (_c_int, [_c_void_p] * 9 + [_c_int] * 4 +
                                    [_c_int64, _c_int64, _c_int, _c_float, _c_void_p, _c_void_p, _c_void_p,
                                     _c_void_p, _c_size_t, _c_void_p]),
@@ -782,7 +783,9 @@ def dense_attn_varlen_backward(q, k, v, out, dout, lse, cu_seqlens_q, cu_seqlens
         dv = _fresh(v, ck) if dv is None else dv
         a, b, c = _rows(dq, "dq"), _rows(dk, "dk"), _rows(dv, "dv")
         if workspace is None:
-            need = L.dense_attn_varlen_backward_workspace_size(qi[0], qi[1])
+            need = L.dense_attn_varlen_backward_workspace_size(
+                cq.buffer_info()[0], ck.buffer_info()[0], len(cq) - 1, qi[0], ki[0], qi[2], qi[1], ki[1],
+                1 if causal else 0)
             workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
         lay = _LAYOUT8.pack(0, qi[3], qi[4], 0, ki[3], ki[4], 0, vi[3], vi[4], 0, oi[3], oi[4],
                             0, gi[3], gi[4], 0, a[3], a[4], 0, b[3], b[4], 0, c[3], c[4])

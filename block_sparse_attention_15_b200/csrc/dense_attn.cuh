@@ -16,17 +16,35 @@ namespace dense {
 
 // The waits of vsa_device.cuh with their polling out of line: a kernel waits in
 // dozens of places, and with the polling inlined its code (90-115 KB) did not
-// stay in the instruction caches.  (A kernel that moves registers between its
-// warpgroups cannot call functions and keeps the inlined form.)
+// stay in the instruction caches.
 namespace slim {
+// A wait may last as long as the longest work item: abort_flag[1] holds the
+// microseconds that adds to the limit.
 static __device__ __noinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                               int* status) {
-  return vsa::mbar_wait(bar, parity, abort_flag, status);
+  unsigned long long t0 = 0;
+  for (;;) {
+    // (a failed try has slept for some microseconds, or until the phase completed)
+    for (int i = 0; i < 16; ++i)
+      if (mbar_try_wait_sleep(bar, parity, kPollSleepNs)) return true;
+    if (abort_flag[0]) return false;
+    if (status && *reinterpret_cast<volatile int*>(status) == VSA_ERR_DEVICE_TIMEOUT) {
+      abort_flag[0] = 1;
+      return false;
+    }
+    const unsigned long long now = global_timer_ns();
+    if (t0 == 0) t0 = now;
+    else if (now - t0 > kWaitTimeoutNs + 1000ull * (unsigned)abort_flag[1]) {
+      set_status(status, VSA_ERR_DEVICE_TIMEOUT);
+      abort_flag[0] = 1;
+      return false;
+    }
+  }
 }
 static __device__ __noinline__ bool warp_poll(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                               int* status) {
   int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = vsa::mbar_wait(bar, parity, abort_flag, status) ? 1 : 0;
+  if ((threadIdx.x & 31) == 0) ok = mbar_poll(bar, parity, abort_flag, status) ? 1 : 0;
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
@@ -387,7 +405,7 @@ __device__ __forceinline__ void issue_pv(uint32_t tmem_o, uint32_t tmem_p, uint3
 // A launch whose waits ran out leaves only after copies that may still be in
 // flight have landed (they take microseconds).
 __device__ __forceinline__ void settle_after_abort(volatile int* abort_flag) {
-  if (*abort_flag)
+  if (abort_flag[0])
     for (int i = 0; i < 20; ++i) __nanosleep(100000);
 }
 

@@ -25,7 +25,9 @@
 //  dk/dv:  a work item is one 128-row key tile of one key head; it walks the
 //          query tiles of all heads of the group that see it.  Per query tile
 //            S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q
-//          P^T and dS^T are A operands in TMEM, over their own S and dP.
+//          P^T and dS^T are A operands in TMEM, over their own S and dP.  Where
+//          there are fewer key tiles than SMs, several items share a tile's
+//          walk, leave fp32 sums, and a third kernel adds them up in order.
 //
 // Both: one CTA per SM, item after item, 768 threads: warp 0 tile loads, warp 1
 // products (one thread), warps 2-3 helpers, warps 4-19 softmax (32 of the 128
@@ -39,6 +41,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "dense_attn.cuh"
@@ -202,7 +205,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                                                       : 1u;
       mbar_init(bars + i, count);
     }
-    if (lane == 0) *abort_flag = 0;
+    if (lane == 0) {
+      abort_flag[0] = 0;
+      abort_flag[1] = p.item_us;
+    }
     mbar_fence_init();
   }
   if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
@@ -582,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       g += 2 * x.n + 3;
       ++n_item;
     }
-    if (ok && !*abort_flag && n_item >= 1) read_out(prev, n_item - 1);
+    if (ok && !abort_flag[0] && n_item >= 1) read_out(prev, n_item - 1);
   }
 
   settle_after_abort(abort_flag);
@@ -603,7 +609,9 @@ struct KItem {
   int q0, q_len;   // first row of q that sees the tile, and the rows from there on
   int diag;        // causal: tile key i is seen by rows q0 + r with r + diag >= i
   int tiles;       // query tiles of one head
-  int n;           // query tiles of all heads of the group
+  int head0, t0;   // where the item's walk begins: head of the group, query tile
+  int n;           // query tiles of the walk
+  int part;        // which share of the tile's walk it is
 };
 
 using KItems = ItemRing<KItem, 2>;
@@ -634,6 +642,8 @@ constexpr uint32_t kKS = 0, kKDP = 128, kKDV = 256, kKDK = 384;
 
 __device__ __forceinline__ KItem load_kitem(const DenseBwdParams& p, const DenseSeqs& t, int w) {
   KItem x;
+  x.part = w % p.parts;
+  w /= p.parts;
   x.hk = w % p.Hkv;
   const Unit un = find_unit(t, w / p.Hkv);
   const int4 q = t.seq[un.seq];
@@ -647,8 +657,19 @@ __device__ __forceinline__ KItem load_kitem(const DenseBwdParams& p, const Dense
   x.q_len = max(0, q.y - skip);
   x.diag = skip + off - 128 * tile;
   x.tiles = (x.q_len + 127) >> 7;
-  x.n = x.tiles * p.group;
+  // (the host keeps walks below 2^27 tiles)
+  const int all = x.tiles * p.group, from = all * x.part / p.parts;
+  x.n = all * (x.part + 1) / p.parts - from;
+  x.head0 = x.tiles ? from / x.tiles : 0;
+  x.t0 = from - x.head0 * x.tiles;
   return x;
+}
+
+// Row r of the item's key tile among the partial sums; dv's lie Hkv * part_rows
+// rows after dk's.
+template <int D>
+__device__ __forceinline__ float* part_row(const DenseBwdParams& p, const KItem& x, int r) {
+  return p.part + (((long long)x.part * 2 * p.Hkv + x.hk) * p.part_rows + (x.key0 - p.part_row0 + r)) * D;
 }
 
 template <int D>
@@ -682,7 +703,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                                                : 1u;
       mbar_init(bars + i, count);
     }
-    if (lane == 0) *abort_flag = 0;
+    if (lane == 0) {
+      abort_flag[0] = 0;
+      abort_flag[1] = p.item_us;
+    }
     mbar_fence_init();
   }
   if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
@@ -709,23 +733,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       KItem x;
       while (ok && next(n_item, x)) {
         if (lane == 0) {
-          for (int h = 0; ok && h < p.group; ++h)
-            for (int t = 0; ok && t < 2 * x.tiles; ++t, ++g) {
-              const int st = (int)(g % NST);
-              const uint32_t u = g / NST;
-              if (u >= 1) ok = mbar_wait(bars + L::kEmpty + st, (u - 1) & 1, abort_flag, p.status);
-              if (!ok) break;
-              const bool is_do = t & 1;
-              const int r = 128 * (t >> 1);
-              // a tile with rows past the sequence goes through warp 3 first
-              uint64_t* full = bars + (x.q_len - r < 128 ? L::kPre : L::kFull) + st;
-              uint8_t* dst = smem + L::kRingOff + st * L::kTile;
-              mbar_arrive_expect_tx(full, L::kTile);
+          int head = x.hk * p.group + x.head0, t = x.t0;
+          for (int i = 0; ok && i < 2 * x.n; ++i, ++g) {
+            const int st = (int)(g % NST);
+            const uint32_t u = g / NST;
+            if (u >= 1) ok = mbar_wait(bars + L::kEmpty + st, (u - 1) & 1, abort_flag, p.status);
+            if (!ok) break;
+            const bool is_do = i & 1;
+            const int r = 128 * t;
+            // a tile with rows past the sequence goes through warp 3 first
+            uint64_t* full = bars + (x.q_len - r < 128 ? L::kPre : L::kFull) + st;
+            uint8_t* dst = smem + L::kRingOff + st * L::kTile;
+            mbar_arrive_expect_tx(full, L::kTile);
 #pragma unroll
-              for (int dh = 0; dh < L::DH; ++dh)
-                load_rows(dst + dh * 16384, is_do ? &tm_do : &tm_q, is_do ? p.do_ax : p.q_ax, full, dh * 64,
-                          x.q0 + r, x.hk * p.group + h, 0, keep);
+            for (int dh = 0; dh < L::DH; ++dh)
+              load_rows(dst + dh * 16384, is_do ? &tm_do : &tm_q, is_do ? p.do_ax : p.q_ax, full, dh * 64,
+                        x.q0 + r, head, 0, keep);
+            if (is_do && ++t == x.tiles) {
+              t = 0;
+              ++head;
             }
+          }
           mbar_arrive(bars + L::kLoaded);
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -743,6 +771,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (x.n == 0) {
           take.ask(lane);
           for (int r = lane; r < x.keys; r += 32) {
+            if (p.parts > 1) {
+              float* to = part_row<D>(p, x, r);
+              for (int e = 0; e < D; e += 4) {
+                *reinterpret_cast<float4*>(to + e) = make_float4(0.f, 0.f, 0.f, 0.f);
+                *reinterpret_cast<float4*>(to + (long long)p.Hkv * p.part_rows * D + e) = make_float4(0.f, 0.f, 0.f, 0.f);
+              }
+              continue;
+            }
             __nv_bfloat16* tk = p.dk + x.hk * p.dk_st.h + (long long)(x.key0 + r) * p.dk_st.s;
             __nv_bfloat16* tv = p.dv + x.hk * p.dv_st.h + (long long)(x.key0 + r) * p.dv_st.s;
             for (int e = 0; e < D; e += 8) {
@@ -788,40 +824,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       KItem x;
       while (ok && next(n_item, x)) {
-        for (int h = 0; ok && h < p.group; ++h) {
-          const long long at = (x.hk * p.group + h) * p.lse_seq + x.q0;
-          for (int t = 0; ok && t < x.tiles; ++t, ++g) {
-            const int slot = (int)(g % NROW);
-            const int left = x.q_len - 128 * t;
-            float nl[4], de[4];
+        int head = x.hk * p.group + x.head0, t = x.t0;
+        for (int i = 0; ok && i < x.n; ++i, ++g) {
+          const long long at = head * p.lse_seq + x.q0 + 128 * t;
+          const int slot = (int)(g % NROW);
+          const int left = x.q_len - 128 * t;
+          if (++t == x.tiles) {
+            t = 0;
+            ++head;
+          }
+          float nl[4], de[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int r = 32 * e + lane;
-              const bool real = r < left;
-              nl[e] = real ? -kLog2 * p.lse[at + 128 * t + r] : -INFINITY;  // no row: p = 0
-              de[e] = real ? p.delta[at + 128 * t + r] : 0.f;
-            }
-            if (g >= (uint32_t)NROW &&
-                !warp_wait(bars + L::kRowEmpty + slot, (g / NROW - 1) & 1, abort_flag, p.status)) { ok = false; break; }
-            float* to = rowv + slot * 256;
+          for (int e = 0; e < 4; ++e) {
+            const int r = 32 * e + lane;
+            const bool real = r < left;
+            nl[e] = real ? -kLog2 * p.lse[at + r] : -INFINITY;  // no row: p = 0
+            de[e] = real ? p.delta[at + r] : 0.f;
+          }
+          if (g >= (uint32_t)NROW &&
+              !warp_wait(bars + L::kRowEmpty + slot, (g / NROW - 1) & 1, abort_flag, p.status)) { ok = false; break; }
+          float* to = rowv + slot * 256;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              to[32 * e + lane] = nl[e];
-              to[128 + 32 * e + lane] = -de[e];
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bars + L::kRowFull + slot);
-            if (left >= 128) continue;
+          for (int e = 0; e < 4; ++e) {
+            to[32 * e + lane] = nl[e];
+            to[128 + 32 * e + lane] = -de[e];
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars + L::kRowFull + slot);
+          if (left >= 128) continue;
 #pragma unroll 1
-            for (int s = 0; ok && s < 2; ++s) {
-              const int st = (int)((2 * g + s) % NST);
-              if (!warp_wait(bars + L::kPre + st, (pre >> st) & 1, abort_flag, p.status)) { ok = false; break; }
-              pre ^= 1u << st;
-              zero_rows<128>(smem + L::kRingOff + st * L::kTile, L::DH, left, (left + 15) & ~15, lane);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bars + L::kFull + st);
-            }
+          for (int s = 0; ok && s < 2; ++s) {
+            const int st = (int)((2 * g + s) % NST);
+            if (!warp_wait(bars + L::kPre + st, (pre >> st) & 1, abort_flag, p.status)) { ok = false; break; }
+            pre ^= 1u << st;
+            zero_rows<128>(smem + L::kRingOff + st * L::kTile, L::DH, left, (left + 15) & ~15, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars + L::kFull + st);
           }
         }
       }
@@ -871,7 +910,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         while (ok && have) {
           bool more = false;
-          int t = 0;  // query tile of the head
+          int t = x.t0;  // query tile of the head
           for (int i = 0; ok && i < x.n; ++i, ++g) {
             const bool last = i + 1 == x.n;
             const int left = x.q_len - 128 * t;
@@ -926,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     KItem x;
     while (ok && next(n_got, x)) {
-      int t = 0;
+      int t = x.t0;
       for (int i = 0; i < x.n; ++i, ++g) {
         // column c of this quarter sees key row r where c >= r - shift
         const int shift = x.diag + 128 * t + 32 * quarter;
@@ -1050,15 +1089,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bars + (k ? L::kDKEmpty : L::kDVEmpty));
           }
-          if (real) {
+          if (!real) continue;
+          if (p.parts > 1) {
+            float* sum = part_row<D>(p, x, row) + (k ? 0 : (long long)p.Hkv * p.part_rows * D);
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint32_t o[4];
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(sum + q0 + e) = make_uint4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+            continue;
+          }
 #pragma unroll
-              for (int q = 0; q < 4; ++q)
-                o[q] = pack_bf16x2(__uint_as_float(ov[e + 2 * q]) * m, __uint_as_float(ov[e + 2 * q + 1]) * m);
-              *reinterpret_cast<uint4*>(to + q0 + e) = make_uint4(o[0], o[1], o[2], o[3]);
-            }
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t o[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              o[q] = pack_bf16x2(__uint_as_float(ov[e + 2 * q]) * m, __uint_as_float(ov[e + 2 * q + 1]) * m);
+            *reinterpret_cast<uint4*>(to + q0 + e) = make_uint4(o[0], o[1], o[2], o[3]);
           }
         }
       }
@@ -1076,12 +1121,85 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// ---------------------------------------------------------------------------
+// the sum of the items that shared a key tile: eight elements a thread, parts in order
+// ---------------------------------------------------------------------------
+template <int D>
+__global__ void __launch_bounds__(256) dense_dkv_join_kernel(const __grid_constant__ DenseBwdParams p) {
+  const long long per = (long long)p.Hkv * p.part_rows * (D / 8);  // of one gradient
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= 2 * per) return;
+  const bool is_v = i >= per;
+  const long long j = is_v ? i - per : i;
+  const int ch = (int)(j % (D / 8));
+  const long long hr = j / (D / 8);
+  const int row = (int)(hr % p.part_rows), h = (int)(hr / p.part_rows);
+  float sum[8] = {};
+#pragma unroll 4
+  for (int k = 0; k < p.parts; ++k) {
+    const float4* from = reinterpret_cast<const float4*>(p.part + k * (16 * per) + i * 8);
+    const float4 a = from[0], b = from[1];
+    sum[0] += a.x, sum[1] += a.y, sum[2] += a.z, sum[3] += a.w;
+    sum[4] += b.x, sum[5] += b.y, sum[6] += b.z, sum[7] += b.w;
+  }
+  const float m = is_v ? 1.f : p.scale;
+  uint32_t o[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) o[q] = pack_bf16x2(sum[2 * q] * m, sum[2 * q + 1] * m);
+  const Strides3& st = is_v ? p.dv_st : p.dk_st;
+  __nv_bfloat16* to = (is_v ? p.dv : p.dk) + h * st.h + (long long)(p.part_row0 + row) * st.s + 8 * ch;
+  *reinterpret_cast<uint4*>(to) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 }  // namespace
 }  // namespace dense
 
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
+int dkv_parts(const int4* seqs, int n, int Hq, int Hkv, bool causal) {
+  const int sms = device_sm_count();
+  long long items = 0;
+  for (int i = 0; i < n; ++i) items += (seqs[i].w + 127LL) / 128 * Hkv;
+  if (items == 0 || items >= 2 * sms) return 1;  // (this also bounds the partial sums' memory)
+  // query tiles that the longest item, and all of them, walk over
+  long long longest = 0, total = 0;
+  for (int i = 0; i < n; ++i)
+    for (long long key = 0; key < seqs[i].w; key += 128) {
+      const long long skip = causal ? std::max(0LL, key - (seqs[i].w - seqs[i].y)) : 0;
+      const long long tiles = (std::max(0LL, seqs[i].y - skip) + 127) / 128 * (Hq / Hkv);
+      longest = std::max(longest, tiles);
+      total += tiles * Hkv;
+    }
+  // Sharing evens the SMs out and costs a launch and the partial sums, about what
+  // 11 tiles take: one sequence of 2000 rows, 8 heads over 1: 249 us in one part,
+  // 77 in 16; 384 rows, 4 over 1 (12 tiles at most): 44 and 38; 2000 rows, 8 heads
+  // over 8 (16 tiles at most, 7 on average per SM): 71 and 89.
+  if (longest - total / sms < 11) return 1;
+  // two items or more to an SM, four tiles or more to an item
+  return (int)std::min(std::min(16LL, longest / 4), std::max(2LL, (2 * sms + items - 1) / items));
+}
+
+static size_t dkv_part_bytes(const int4* seqs, int n, int parts, int Hkv, int D) {
+  const long long rows = seqs[n - 1].z + (long long)seqs[n - 1].w - seqs[0].z;
+  return parts == 1 ? 0 : (size_t)parts * 2 * Hkv * rows * D * sizeof(float);
+}
+
+// delta, then the partial sums of one launch after the other
+static size_t delta_bytes(int Hq, long long q_rows) {
+  return ((size_t)Hq * q_rows * sizeof(float) + 255) & ~size_t(255);
+}
+
+size_t dense_bwd_workspace(const DenseBatch& b, int Hq, int Hkv, int D, long long q_rows, bool causal) {
+  size_t most = 0;
+  for (int i0 = 0; i0 < b.n; i0 += kDenseMaxSeqs) {
+    int4 seqs[kDenseMaxSeqs];
+    const int n = b.chunk(i0, seqs);
+    most = std::max(most, dkv_part_bytes(seqs, n, dkv_parts(seqs, n, Hq, Hkv, causal), Hkv, D));
+  }
+  return delta_bytes(Hq, q_rows) + most;
+}
+
 template <int D>
 static int launch_dense_bwd_t(DenseBwdParams p, const CUtensorMap* m, const int4* seqs, int n,
                               cudaStream_t stream) {
@@ -1098,7 +1216,12 @@ static int launch_dense_bwd_t(DenseBwdParams p, const CUtensorMap* m, const int4
   for (int i = 0; i < n; ++i) {
     q_units += (seqs[i].y + 127LL) / 128 * p.Hq;
     k_units += (seqs[i].w + 127LL) / 128 * p.Hkv;
+    if ((seqs[i].y + 127LL) / 128 * p.group >= (1 << 27)) return VSA_ERR_UNSUPPORTED;
   }
+  p.parts = dkv_parts(seqs, n, p.Hq, p.Hkv, p.causal != 0);
+  p.part_row0 = seqs[0].z;
+  p.part_rows = seqs[n - 1].z + seqs[n - 1].w - seqs[0].z;
+  p.part = reinterpret_cast<float*>(reinterpret_cast<char*>(p.delta) + delta_bytes(p.Hq, p.lse_seq));
   if (q_units >= (1 << 30) || k_units >= (1 << 30)) return VSA_ERR_UNSUPPORTED;  // 32-bit item index
   if (q_units > 0) {
     for (int i = 0; i < n; ++i) {
@@ -1116,8 +1239,12 @@ static int launch_dense_bwd_t(DenseBwdParams p, const CUtensorMap* m, const int4
       flat[i] = p.causal ? 0 : seqs[i].y;
     }
     fill_dense_seqs(&table, seqs, units, flat, n);
-    kk<<<(unsigned)k_units, dense::kThreads, dense::KLayout<D>::kAlloc, stream>>>(
+    kk<<<(unsigned)(k_units * p.parts), dense::kThreads, dense::KLayout<D>::kAlloc, stream>>>(
         m[0], m[1], m[2], m[3], p, table);
+    if (p.parts > 1) {
+      const long long chunks = 2LL * p.Hkv * p.part_rows * (D / 8);
+      dense::dense_dkv_join_kernel<D><<<(unsigned)((chunks + 255) / 256), 256, 0, stream>>>(p);
+    }
   }
   return cudaGetLastError() == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
 }
@@ -1142,6 +1269,7 @@ int launch_dense_bwd(const DenseBwdParams& p_in, const DenseTensors& t, const vo
       !map(&m[3], &p.do_ax, rows, dout, t.q_seq, p.Hq, do_st) ||
       !map(&m[4], &p.o_ax, rows, out, t.q_seq, p.Hq, out_st))
     return VSA_ERR_CUDA;
+  p.item_us = std::max(item_microseconds(b, false, 1), item_microseconds(b, true, p.group));
   for (int i0 = 0; i0 < b.n; i0 += kDenseMaxSeqs) {
     int4 seqs[kDenseMaxSeqs];
     const int n = b.chunk(i0, seqs);

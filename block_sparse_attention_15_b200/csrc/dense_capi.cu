@@ -121,9 +121,11 @@ int dense_attn_varlen(const void* q, const void* k, const void* v, const vsa_den
   return launch_dense_fwd(p, t, b, D, static_cast<cudaStream_t>(stream));
 }
 
-size_t dense_attn_varlen_backward_workspace_size(int Hq, int64_t q_rows) {
-  if (Hq <= 0 || Hq > 65535 || q_rows < 0 || q_rows > kMaxRows) return 0;
-  return (size_t)Hq * (size_t)q_rows * sizeof(float);
+size_t dense_attn_varlen_backward_workspace_size(const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_kv,
+                                                 int n_seqs, int Hq, int Hkv, int D, int64_t q_rows,
+                                                 int64_t kv_rows, int causal) {
+  if (check_dense(n_seqs, cu_seqlens_q, cu_seqlens_kv, Hq, Hkv, D, q_rows, kv_rows, 0.f) != VSA_OK) return 0;
+  return dense_bwd_workspace(DenseBatch{cu_seqlens_q, cu_seqlens_kv, n_seqs}, Hq, Hkv, D, q_rows, causal != 0);
 }
 
 int dense_attn_varlen_backward(const void* q, const void* k, const void* v, const void* out, const void* dout,
@@ -150,7 +152,8 @@ int dense_attn_varlen_backward(const void* q, const void* k, const void* v, cons
                 !view_ok(L.dv, Hkv, kv_rows))))
     return VSA_ERR_UNSUPPORTED;
   if (rows && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
-               workspace_bytes < dense_attn_varlen_backward_workspace_size(Hq, q_rows)))
+               workspace_bytes < dense_bwd_workspace(DenseBatch{cu_seqlens_q, cu_seqlens_kv, n_seqs}, Hq, Hkv, D,
+                                                     q_rows, causal != 0)))
     return VSA_ERR_WORKSPACE;
   DenseBwdParams p;
   memset(&p, 0, sizeof(p));

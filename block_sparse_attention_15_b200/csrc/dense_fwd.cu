@@ -170,7 +170,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                                    : 1u;
       mbar_init(bars + i, count);
     }
-    if (lane == 0) *abort_flag = 0;
+    if (lane == 0) {
+      abort_flag[0] = 0;
+      abort_flag[1] = p.item_us;
+    }
     mbar_fence_init();
   }
   if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
@@ -524,6 +527,15 @@ int DenseBatch::chunk(int i0, int4* seqs) const {
   return m;
 }
 
+int item_microseconds(const DenseBatch& b, bool over_rows, int group) {
+  long long tiles = 0;
+  for (int i = 0; i < b.n; ++i) {
+    const int32_t* cu = over_rows ? b.cu_q : b.cu_kv;
+    tiles = std::max(tiles, (cu[i + 1] - cu[i] + 127LL) / 128 * group);
+  }
+  return (int)std::min(20 * tiles, 1000000000LL);
+}
+
 void fill_dense_seqs(DenseSeqs* t, const int4* seqs, const int* units, const int* flat_cost, int n) {
   int order[kDenseMaxSeqs];
   int m = 0;
@@ -579,6 +591,7 @@ int launch_dense_fwd(const DenseParams& p_in, const DenseTensors& t, const Dense
       !make_view_map_rows(&mv, &p.v_ax, keys ? t.v : t.q, D, keys ? t.kv_seq : t.q_seq,
                           keys ? p.Hkv : p.Hq, 1, keys ? t.v_st : t.q_st, 128))
     return VSA_ERR_CUDA;
+  p.item_us = item_microseconds(b, false, 1);
   for (int i0 = 0; i0 < b.n; i0 += kDenseMaxSeqs) {
     int4 seqs[kDenseMaxSeqs];
     int units[kDenseMaxSeqs], flat[kDenseMaxSeqs];

@@ -36,6 +36,7 @@ struct DenseParams {
   int Hq, Hkv, group;               // group = Hq / Hkv
   int causal;
   int slots;                        // row tiles per work item: 1 or 2
+  int item_us;                      // see item_microseconds
   float scale_log2;
   int* status;
 };
@@ -63,6 +64,10 @@ struct KernelReady {
 };
 
 int device_sm_count();
+// 20 us per tile of the longest work item (10 times what one takes), which a wait
+// on an item may last on top of the waits' own limit: over the keys of a sequence,
+// or over its rows in each head of a group.
+int item_microseconds(const DenseBatch& b, bool over_rows, int group);
 // Fills the table (dropping sequences without units).  `flat_cost` of a sequence:
 // the cost of each of its units where they cost about the same, else 0; all in
 // the order of `seqs`, the units' sum below 2^30.
@@ -76,13 +81,20 @@ struct DenseBwdParams {
   Strides3 dq_st, dk_st, dv_st;
   const float* lse;                 // [Hq, lse_seq]
   float* delta;                     // [Hq, lse_seq] workspace
+  float* part;                      // [parts][dk, dv][Hkv][part_rows][D] workspace, see dkv_parts
+  int parts, part_row0, part_rows;  // rows part_row0 .. of k and v
   long long lse_seq;
   TmaAxes q_ax, k_ax, v_ax, do_ax, o_ax;
   int Hq, Hkv, group;
   int causal;
+  int item_us;                      // see item_microseconds
   float scale, scale_log2;
   int* status;
 };
+// CTAs that share a key tile's walk over the query rows: more than one where the
+// key tiles of a launch (n sequences) would leave SMs idle for long.
+int dkv_parts(const int4* seqs, int n, int Hq, int Hkv, bool causal);
+size_t dense_bwd_workspace(const DenseBatch& b, int Hq, int Hkv, int D, long long q_rows, bool causal);
 int launch_dense_bwd(const DenseBwdParams& p, const DenseTensors& t, const void* out, Strides3 out_st,
                      const void* dout, Strides3 do_st, const DenseBatch& b, int D, cudaStream_t stream);
 
@@ -99,6 +111,7 @@ struct PrefixParams {
   int B, Hq, Hkv, T, prefix_len, suffix_cap;
   float scale_log2;
   int* status;
+  int item_us;
   // filled by prefix_shape
   int group, rows_per_req;          // Hq / Hkv, group * T
   int pfx_blocks, sfx_blocks;       // row blocks of 256 of a prefix / suffix segment

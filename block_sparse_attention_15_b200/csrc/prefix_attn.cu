@@ -347,7 +347,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                                        : 1u;
       mbar_init(bars + i, count);
     }
-    if (lane == 0) *abort_flag = 0;
+    if (lane == 0) {
+      abort_flag[0] = 0;
+      abort_flag[1] = p.item_us;
+    }
     mbar_fence_init();
   }
   if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
@@ -908,6 +911,8 @@ static int launch_prefix_t(const PrefixParams& p, const CUtensorMap* m, cudaStre
 
 int launch_prefix(const PrefixParams& p_in, const PrefixTensors& t, int D, cudaStream_t stream) {
   PrefixParams p = p_in;
+  // a CTA's piece is a share of the line: far shorter than the waits' limit
+  p.item_us = 0;
   CUtensorMap m[4];
   const bool pfx = p.prefix_len > 0, sfx = p.suffix_cap > 0;
   // a part that is empty loads nothing; its map only has to be valid

@@ -575,9 +575,12 @@ int dense_attn_varlen(const void* q, const void* k, const void* v, const vsa_den
                       int Hkv, int D, int64_t q_rows, int64_t kv_rows, int causal, float scale,
                       void* out, float* lse, void* stream);
 
-/* Workspace bytes dense_attn_varlen_backward needs: delta per query row and
- * head (0 for invalid arguments, or without rows). */
-size_t dense_attn_varlen_backward_workspace_size(int Hq, int64_t q_rows);
+/* Workspace bytes dense_attn_varlen_backward needs for these arguments: delta
+ * per query row and head and, where few key tiles are shared out over the SMs,
+ * their partial sums (at most some 80 MB); 0 for invalid arguments. */
+size_t dense_attn_varlen_backward_workspace_size(const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_kv,
+                                                 int n_seqs, int Hq, int Hkv, int D, int64_t q_rows,
+                                                 int64_t kv_rows, int causal);
 
 /*
  * dense_attn_varlen_backward -- dq, dk, dv of dense_attn_varlen:
@@ -597,9 +600,9 @@ size_t dense_attn_varlen_backward_workspace_size(int Hq, int64_t q_rows);
  * layout   host (all eight members), or NULL for contiguous tensors
  * dq       device bf16 [Hq, q_rows, D] view; dk, dv [Hkv, kv_rows, D] views;
  *          rows past the last sequence are left as they were
- * workspace  device, >= dense_attn_varlen_backward_workspace_size(Hq, q_rows),
+ * workspace  device, >= dense_attn_varlen_backward_workspace_size(...),
  *          256-aligned; no two calls in flight may share it
- * Two launches on `stream` per 256 sequences.
+ * Two or three launches on `stream` per 256 sequences.
  */
 int dense_attn_varlen_backward(const void* q, const void* k, const void* v, const void* out, const void* dout,
                                const float* lse, const vsa_dense_layout* layout, const int32_t* cu_seqlens_q,

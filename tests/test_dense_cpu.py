@@ -14,7 +14,7 @@ def _p(x):
 
 
 def _i32(xs):
-    return None if xs is None else np.asarray(xs, dtype=np.int32).ctypes.data_as(ctypes.POINTER(ctypes.c_int32))
+    return (ctypes.c_int32 * len(xs))(*xs)
 
 
 def _dense(**kw):
@@ -114,10 +114,30 @@ def test_backward_argument_checks():
         assert _backward(**{n: None}) == 1 and _backward(**{n: FAKE + 8}) == 1
     assert _backward(lse=None) == 1 and _backward(n=0) == 2 and _backward(hq=5) == 2 and _backward(d=96) == 3
     assert _backward(cq=[0, 11]) == 2 and _backward(ck=[3, 10]) == 2
-    assert _backward(ws=None) == 7 and _backward(ws=FAKE + 16) == 7 and _backward(bytes=159) == 7
-    assert _lib().dense_attn_varlen_backward_workspace_size(4, 10) == 160
+    cu = _i32([0, 10])
+    need = _lib().dense_attn_varlen_backward_workspace_size(cu, cu, 1, 4, 2, 128, 10, 10, 1)
+    assert need >= 160 and _lib().dense_attn_varlen_backward_workspace_size(cu, cu, 1, 5, 2, 128, 10, 10, 1) == 0
+    assert _backward(ws=None) == 7 and _backward(ws=FAKE + 16) == 7 and _backward(bytes=need - 1) == 7
     good = dict(zip([n for n, _ in B.VsaDenseLayout._fields_], [(0, 1280, 128)] * 8))
     for n in good:
         lay = B.VsaDenseLayout(*[B.VsaStrides(*(good | {n: (0, 1280, 132)})[m]) for m in good])
         assert _backward(layout=ctypes.byref(lay)) == 3
     assert _backward(cq=[0, 0], ck=[0, 0], q=None, dk=None, lse=None, ws=None) == 0
+
+
+def test_backward_workspace_of_shared_key_tiles():
+    """One long sequence of many query heads over one key head has fewer key tiles
+    than SMs: room for their partial sums, and no more than 80 MB."""
+    f = _lib().dense_attn_varlen_backward_workspace_size
+
+    def partial(hq, hkv, n, causal=1):
+        cu = _i32([0, n])
+        return f(cu, cu, 1, hq, hkv, 128, n, n, causal) - (4 * hq * n + 255) // 256 * 256
+
+    assert partial(8, 1, 2000) == 16 * 2 * 2000 * 128 * 4               # 16 key tiles, shared by 16 items each
+    assert partial(4, 1, 130) == 0 and partial(8, 8, 2000) == 0          # walks of 8 tiles; key tiles enough
+    assert partial(40, 8, 8192) == 0
+    for n in (130, 2000, 8192, 18000, 40000):
+        for hq, hkv in ((8, 1), (16, 2), (64, 8), (12, 12)):
+            for causal in (0, 1):
+                assert 0 <= partial(hq, hkv, n, causal) <= 80 << 20

@@ -45,6 +45,16 @@ def test_more_items_than_sms(d, heads):
     check(*make(*heads, d, pairs, seed=6), False)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("heads", [(8, 1), (32, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_shared_key_tiles(d, heads, causal):
+    """Fewer key tiles than SMs: their walks are shared out, some shares empty,
+    beside sequences without rows or keys."""
+    check(*make(*heads, d, [(700, 700)], seed=d), causal)
+    check(*make(*heads, d, [(130, 400), (0, 5), (600, 777), (5, 0), (1, 200), (300, 20)], seed=d + 1, extra=7), causal)
+
+
 def test_long():
     """2049 rows behind 5000 keys."""
     check(*make(16, 4, 128, [(2049, 5000), (3, 3)], seed=9), True)
