@@ -646,45 +646,48 @@ def _heads(t, name):
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dim() != 4:
         raise ValueError(f"{name} must be a 4-D [B, H, S, D] view")
-    shape, st = t.shape, t.stride()
-    if 0 in shape:
+    shape = t.shape
+    b, h, n, d = shape
+    if not (b and h and n and d):
         return shape, (0, 0, 0), t.data_ptr()
-    if st[3] != 1 or any(n > 1 and (x <= 0 or x & 7) for n, x in zip(shape[:3], st)):
+    st = s0, s1, s2, s3 = t.stride()
+    if (s3 != 1 or (b > 1 and (s0 <= 0 or s0 & 7)) or (h > 1 and (s1 <= 0 or s1 & 7)) or
+            (n > 1 and (s2 <= 0 or s2 & 7))):
         raise ValueError(f"{name}: strides {st} must be positive multiples of 8 elements, the last 1")
     ptr = t.data_ptr()
     if ptr & 15:
         raise ValueError(f"{name} must start on a 16-byte boundary")
-    return shape, st[:3], ptr
+    return shape, (s0, s1, s2), ptr
 
 
-def _same_device(index, **tensors):
-    for n, t in tensors.items():
+def _same_device(index, *tensors):
+    for t in tensors:
         if t is not None and t.get_device() != index:
-            raise ValueError(f"{n} is on {t.device}, q on cuda:{index}")
+            raise ValueError(f"a tensor is on {t.device}, q on cuda:{index}")
 
 
 class _Launch:
     """The device and stream of a call: the tensors' device becomes the current
     one, and memory allocated inside belongs to the stream the kernels run on.
     Enters as that stream's handle."""
+    __slots__ = ("_index", "_with")
 
     def __init__(self, index, stream):
         self._index = index
-        self._dev = None if torch.cuda.current_device() == index else torch.cuda.device(index)
-        self._ctx = None if stream is None else torch.cuda.stream(stream)
+        self._with = ()
+        if torch.cuda.current_device() != index:
+            self._with += (torch.cuda.device(index),)
+        if stream is not None:
+            self._with += (torch.cuda.stream(stream),)
 
     def __enter__(self):
-        if self._dev is not None:
-            self._dev.__enter__()
-        if self._ctx is not None:
-            self._ctx.__enter__()
+        for c in self._with:
+            c.__enter__()
         return _raw_stream(self._index)
 
     def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
-        if self._dev is not None:
-            self._dev.__exit__(*exc)
+        for c in reversed(self._with):
+            c.__exit__(*exc)
 
 
 def _cumulative(xs, name):
@@ -735,7 +738,7 @@ def dense_attn_varlen(q, k, v, cu_seqlens_q, cu_seqlens_kv, *, causal: bool = Tr
     :func:`dense_attn_varlen_backward` takes."""
     qi, ki, vi, cq, ck = _dense_common(q, k, v, cu_seqlens_q, cu_seqlens_kv)
     index = q.get_device()
-    _same_device(index, k=k, v=v, out=out)
+    _same_device(index, k, v, out)
     with _Launch(index, stream) as st:
         if out is None:
             out = _fresh(q, cq)
@@ -772,7 +775,7 @@ def dense_attn_varlen_backward(q, k, v, out, dout, lse, cu_seqlens_q, cu_seqlens
     if lse.shape != (qi[0], qi[1]):
         raise ValueError(f"lse must be [Hq, q_rows] = {(qi[0], qi[1])}")
     index = q.get_device()
-    _same_device(index, k=k, v=v, out=out, dout=dout, lse=lse, workspace=workspace, dq=dq, dk=dk, dv=dv)
+    _same_device(index, k, v, out, dout, lse, workspace, dq, dk, dv)
     for n, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
         if t is not None and t.shape != like.shape:
             raise ValueError(f"{n} must be shaped like {n[1]}")
@@ -824,8 +827,7 @@ def shared_prefix_attn(q, k_prefix, v_prefix, k_suffix, v_suffix, suffix_lens, *
     if suffix_lens.shape != (B,):
         raise ValueError(f"suffix_lens must be [B] = [{B}]")
     index = q.get_device()
-    _same_device(index, k_prefix=k_prefix, v_prefix=v_prefix, k_suffix=k_suffix, v_suffix=v_suffix,
-                 suffix_lens=suffix_lens, out=out, workspace=workspace)
+    _same_device(index, k_prefix, v_prefix, k_suffix, v_suffix, suffix_lens, out, workspace)
     L = lib()
     with _Launch(index, stream) as st:
         if out is None:
