@@ -11,12 +11,12 @@
 //   dv_j = sum_{h, r} p(r, j) dout_r
 //
 // How (sm_100a): two kernels, each with one kind of accumulator in TMEM, so
-// that every sum has one owner and a fixed order (no atomics, no fp32 copies
-// of the gradients in memory).  The price is that S and dout V^T are formed
-// twice (7 products of 128 x 128 x D instead of 5).  One kernel for all five
-// would send its dq tiles to memory as fp32 sums, 64 KB per pair of tiles each
-// way through shared memory, and keep dS there too: its shared-memory traffic
-// (128 bytes a cycle) would take as long as these seven products.
+// that every sum has one owner and a fixed order (no atomics).  The price is
+// that S and dout V^T are formed twice (7 products of 128 x 128 x D instead of
+// 5).  One kernel for all five would send its dq tiles to memory as fp32 sums,
+// 64 KB per pair of tiles each way through shared memory, and keep dS there too:
+// some 3800 cycles of shared-memory traffic (128 bytes a cycle) per pair of
+// tiles, against the 4700 cycles that these seven products take.
 //
 //  dq:     a work item is one 128-row query tile of one head.  Per key tile
 //            S = Q K^T, dP = dO V^T, dQ += dS K
@@ -26,15 +26,26 @@
 //          query tiles of all heads of the group that see it.  Per query tile
 //            S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q
 //          P^T and dS^T are A operands in TMEM, over their own S and dP.  Where
-//          there are fewer key tiles than SMs, several items share a tile's
-//          walk, leave fp32 sums, and a third kernel adds them up in order.
+//          key tiles are too few, several items share a tile's walk, leave fp32
+//          sums, and a third kernel adds them up in order.
 //
 // Both: one CTA per SM, item after item, 768 threads: warp 0 tile loads, warp 1
 // products (one thread), warps 2-3 helpers, warps 4-19 softmax (32 of the 128
-// columns each), warps 20-23 epilogue.  Products are issued in
-// the order S(i+1), dQ(i), dP(i+1) and dP(i), dV(i), S(i+1), dK(i): the
-// exponentials of a tile run under the previous tile's last product, its dS
-// under the next tile's S.
+// columns each), warps 20-23 epilogue.  Products are issued in pairs, dQ(j) with
+// dP(j+1), and dV(i) with S(i+1), dK(i) with dP(i+1), after everything that
+// both need was waited for: the thread's waits cost 100-250 cycles each, and a
+// product's completion reaches a waiting warp 300 cycles after its last
+// multiplication.  The exponentials of a tile run under one pair, its dS under
+// the other (dq: under the next S).  dP of the dq kernel comes in halves of 64
+// keys, so that the first half's dS runs under the second, and dQ begins with it.
+//
+// What bounds it at D = 128: a product of 128 x 128 x 128 takes 596 cycles with
+// its A operand in TMEM, 861 with it in shared memory (A's 4 KB per instruction
+// do not load under the multiplication), so dq has 3 x 596 = 1788 cycles a tile
+// and dk/dv 2 x 596 + 2 x 861 = 2914 (TMEM holds no K and V beside two sums of
+// 128 columns).  Measured on 8192 rows, 40 heads over 8: 2390 and 3110 cycles;
+// without any softmax work 2230 and 3060.  1.94 ms together, 886 TFLOP/s of the
+// five products, at 1.58 GHz (the power limit's clock).
 // P and dS are rounded to bf16 for the tensor core; everything else is fp32.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -74,32 +85,33 @@ __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// D = A B^T: A [128][D] bf16 in TMEM, B a tile [D / 64][128 rows][128 B].
-template <int D>
-__device__ __forceinline__ void issue_ta(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_base) {
-  constexpr uint32_t idesc = make_idesc_bf16(128, 128, false, false);
-  const uint64_t b0 = make_sdesc_sw128(b_base, 16u, 1024u);
+// D = A B^T over N rows of B from its row `from` on: A [128][D] bf16 in TMEM, B a
+// tile [D / 64][128 rows][128 B].
+template <int D, int N>
+__device__ __forceinline__ void issue_ta(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_base, int from) {
+  constexpr uint32_t idesc = make_idesc_bf16(128, N, false, false);
+  const uint64_t b0 = make_sdesc_sw128(b_base + 128u * from, 16u, 1024u);
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk)
-    umma_bf16_tmem_a(tmem_d, tmem_a + 8u * kk,
+    umma_bf16_tmem_a(tmem_d + from, tmem_a + 8u * kk,
                      b0 + (uint64_t)(((kk / 4) * 16384 + (kk % 4) * 32) >> 4), idesc, kk > 0 ? 1u : 0u);
 }
 
-// D (+)= A B over the first 16 * steps rows of the tile B [D / 64][128][128 B];
-// A [128][128] bf16 in TMEM: 32 columns at each of tmem_a + 0, 32, 64, 96 (over
+// D (+)= A B over the steps [from, to) of 16 rows of the tile B [D / 64][128][128 B]
+// (FROM, TO, and no further than `steps`); A [128][128] bf16 in TMEM: 32 columns at each of tmem_a + 0, 32, 64, 96 (over
 // the fp32 columns of the softmax warpgroup that wrote them).
-template <int D>
-__device__ __forceinline__ void issue_quarters(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_base,
-                                             int steps, bool accumulate) {
+template <int D, int FROM, int TO>
+__device__ __forceinline__ void issue_quarters(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_base, int steps,
+                                               bool accumulate) {
   constexpr uint32_t idesc = make_idesc_bf16(128, D, false, true);
   const uint64_t b0 = make_sdesc_sw128(b_base, 16384u, 1024u);
-  if (steps == 8) {
+  if (steps >= TO) {
 #pragma unroll
-    for (int kk = 0; kk < 8; ++kk)
+    for (int kk = FROM; kk < TO; ++kk)
       umma_bf16_tmem_a(tmem_d, tmem_a + 32u * (kk / 2) + 8u * (kk % 2), b0 + (uint64_t)((kk * 2048) >> 4),
                        idesc, (accumulate || kk > 0) ? 1u : 0u);
   } else {
-    for (int kk = 0; kk < steps; ++kk)
+    for (int kk = FROM; kk < steps; ++kk)
       umma_bf16_tmem_a(tmem_d, tmem_a + 32u * (kk / 2) + 8u * (kk % 2), b0 + (uint64_t)((kk * 2048) >> 4),
                        idesc, (accumulate || kk > 0) ? 1u : 0u);
   }
@@ -145,7 +157,7 @@ struct QLayout {
                        kGFull = kQFull + NOP, kQReady = kGFull + NOP, kGReady = kQReady + 2,
                        kDReady = kGReady + 1, kQFree = kDReady + 2, kGFree = kQFree + 1,
                        kSFull = kGFree + 1, kSFree = kSFull + 1,
-                       kDPFull = kSFree + 1, kDSFull = kDPFull + 1, kOFull = kDSFull + 1,
+                       kDPFull = kSFree + 1, kDSFull = kDPFull + 2, kOFull = kDSFull + 2,
                        kOEmpty = kOFull + 1, kItFull = kOEmpty + 1, kItEmpty = kItFull + QItems::kSlots,
                        kTake = kItEmpty + QItems::kSlots, kLoaded = kTake + 1, kNumBars = kLoaded + 1;
   static constexpr uint32_t kMiscOff = kBarOff + 8u * kNumBars;
@@ -200,7 +212,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a TMA transaction, a commit or one thread's arrival, except where the
       // epilogue's four or the softmax's eight warps arrive
       const uint32_t count = ((i >= L::kQReady && i < L::kQFree) || i == L::kOEmpty) ? 4u
-                             : (i == L::kSFree || i == L::kDSFull)                    ? (uint32_t)kSoftmaxWarps
+                             : i == L::kSFree                                         ? (uint32_t)kSoftmaxWarps
+                             : (i >= L::kDSFull && i < L::kOFull)                     ? kSoftmaxWarps / 2u
                              : (i >= L::kItEmpty && i < L::kTake)                                     ? kThreads / 32 - 1u  // all warps but one
                                                                                       : 1u;
       mbar_init(bars + i, count);
@@ -336,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) return;
           ++ts;
           tc_fence_after_sync();
-          issue_ta<D>(tmem_base + kQS, tmem_base + kQQ, tile(gx + 3 + 2 * j));
+          issue_ta<D, 128>(tmem_base + kQS, tmem_base + kQQ, tile(gx + 3 + 2 * j), 0);
           umma_commit(bars + L::kSFull);
           if (j == x.n - 1) umma_commit(bars + L::kQFree);
         };
@@ -346,8 +359,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_stage(gx + 4 + 2 * j);
         };
         auto do_dp = [&](const QItem& x, int j, uint32_t gx) {
-          issue_ta<D>(tmem_base + kQDP, tmem_base + kQDO, tile(gx + 4 + 2 * j));
+          issue_ta<D, 64>(tmem_base + kQDP, tmem_base + kQDO, tile(gx + 4 + 2 * j), 0);
           umma_commit(bars + L::kDPFull);
+          issue_ta<D, 64>(tmem_base + kQDP, tmem_base + kQDO, tile(gx + 4 + 2 * j), 64);
+          umma_commit(bars + L::kDPFull + 1);
           if (j == x.n - 1) umma_commit(bars + L::kGFree);
         };
         auto next_one = [&](QItem& x) {
@@ -387,8 +402,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             tc_fence_after_sync();
             const int keys = x.last - 128 * j;
-            issue_quarters<D>(tmem_base + kQDQ, tmem_base + kQDP, tile(g + 3 + 2 * j),
-                              keys >= 128 ? 8 : (keys + 15) >> 4, j > 0);
+            const int steps = keys >= 128 ? 8 : (keys + 15) >> 4;
+            issue_quarters<D, 0, 4>(tmem_base + kQDQ, tmem_base + kQDP, tile(g + 3 + 2 * j), steps, j > 0);
+            wait(L::kDSFull + 1, tq - 1);
+            if (!ok) break;
+            tc_fence_after_sync();
+            issue_quarters<D, 4, 8>(tmem_base + kQDQ, tmem_base + kQDP, tile(g + 3 + 2 * j), steps, j > 0);
             if (last) umma_commit(bars + L::kOFull);
             if (!last) do_dp(x, j + 1, g);
             else if (more) do_dp(y, 0, g_next);
@@ -456,10 +475,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float nd = -rowv[(n_item & 1) * 256 + 128 + row];
           nd2 = pk2(nd, nd);
         }
-        if (!warp_wait(bars + L::kDPFull, g & 1, abort_flag, p.status)) { ok = false; break; }
+        if (!warp_wait(bars + L::kDPFull + (quarter >> 1), g & 1, abort_flag, p.status)) { ok = false; break; }
         tc_fence_after_sync();
-        if (warp == 4 && lane == 0) {
-          // dP is complete, and with it the dQ issued before it: their V and K tiles are free
+        if (warp == 12 && lane == 0) {
+          // dP's second half is complete, and with it all before it: its V tile and the
+          // previous dQ's K tile are free
           mbar_arrive(bars + L::kEmpty + (int)((at + 4 + 2 * j) % NST));
           if (g > 0) mbar_arrive(bars + L::kEmpty + (int)(last_k % NST));
           last_k = at + 3 + 2 * j;
@@ -484,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bars + L::kDSFull);
+        if (lane == 0) mbar_arrive(bars + L::kDSFull + (quarter >> 1));
       }
       ++n_item;
       at += 2 * x.n + 3;
@@ -925,7 +945,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait(L::kPFull, g);
             if (!ok) break;
             tc_fence_after_sync();
-            issue_quarters<D>(tmem_base + kKDV, tmem_base + kKS, tile(2 * g + 1), steps, i > 0);
+            issue_quarters<D, 0, 8>(tmem_base + kKDV, tmem_base + kKS, tile(2 * g + 1), steps, i > 0);
             if (last) umma_commit(bars + L::kDVFull);
             if (!last) do_s(x, i + 1, g + 1);
             else if (more) do_s(y, 0, g + 1);
@@ -935,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait(L::kDSFull, g);
             if (!ok) break;
             tc_fence_after_sync();
-            issue_quarters<D>(tmem_base + kKDK, tmem_base + kKDP, tile(2 * g), steps, i > 0);
+            issue_quarters<D, 0, 8>(tmem_base + kKDK, tmem_base + kKDP, tile(2 * g), steps, i > 0);
             umma_commit(bars + L::kEmpty + (int)((2 * g) % NST));
             if (last) umma_commit(bars + L::kDKFull);
             if (!last) do_dp(x, i + 1, g + 1);
@@ -955,7 +975,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // that held one key's part of S would read 32 of each, and a warp's reads of
     // one address cost as much as reads of 32.  In the 16x256b form a thread
     // holds four keys (lane / 4 + 8 k) and the columns 8 i + 2 (lane % 4) + {0, 1}
-    // and reads a quarter of that (measured: 1950 -> @A@ cycles for p, 760 -> @B@ for ds).
+    // and reads a quarter of that (8 warps of 64 columns: 1950 -> 1510 cycles for p).
     const int quarter = (warp - 4) >> 2;
     const uint32_t t_lane = tmem_base + (uint32_t((warp & 3) * 32) << 16) + 32u * quarter;
     constexpr uint32_t kUpper = 16u << 16;  // lanes 16-31 of the warp

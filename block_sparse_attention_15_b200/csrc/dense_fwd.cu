@@ -30,6 +30,11 @@
 //   warp 3      finds the work items, loads their Q tiles
 //   warps 4-11, 12-19   softmax of slot 0, slot 1, 16 rows a warp (softmax_tile)
 //   warps 20-23 epilogue: O / l, bf16 rows
+// Measured on 15488 rows, 40 heads over 8, causal: 2.10 ms, 1170 TFLOP/s (0.72 of
+// the measured bf16 peak), about 1650 cycles a tile; four softmax warps a slot,
+// one row per thread: 2.51 ms.  Part of the exponentials run on the FMA pipe
+// (DENSE_POLY8 0 / 1 / 2 / 3 of 8: 828, 820, 814, 826 us on three full clips of
+// 3000 to 9216 rows; the special-function unit alone does 16 a cycle).
 // P is rounded to bf16 for the tensor core (half a step is 2^-9 of a value,
 // and its error averages over the keys); sums, maxima and O stay fp32.
 #include <cuda.h>

@@ -33,6 +33,11 @@
 // last one's results.  Loops are kept short: the first pass through each line of
 // code costs an instruction fetch that waits behind the K/V stream (a softmax
 // unrolled over its 128 columns spent 25 us of a call on that).
+//
+// Measured at D = 128: 24 requests of 9216 keys at most, 56 heads over 8, no
+// prefix: 90 us, 5.0 TB/s; 64 requests behind 15488 shared keys, 40 heads over 8:
+// 94 us, 3.5 TB/s (an SM streams 46 GB/s: its ring over the loaded latency, and
+// the SMs that work on the prefix stream nothing); 16 requests of 5 tokens: 41 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
