@@ -609,21 +609,23 @@ _LAYOUT8 = struct.Struct("24q")   # vsa_dense_layout
 _LAYOUT6 = struct.Struct("18q")   # vsa_prefix_layout
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_Tensor, _BF16, _F32, _U8 = torch.Tensor, torch.bfloat16, torch.float32, torch.uint8
 
 
 def _rows(t, name):
     """(H, rows, D, head stride, row stride, address) of a bf16 CUDA [H, rows, D]
     view: head dim contiguous, other strides multiples of 8 elements
     (token-major memory transposed, a slice of a fused tensor)."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype != _BF16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3:
+    shape = t.shape
+    if len(shape) != 3:
         raise ValueError(f"{name} must be a 3-D [H, rows, D] view")
-    h, r, d = t.shape
+    h, r, d = shape
     if not (h and r and d):
         return h, r, d, 0, 0, t.data_ptr()
     s0, s1, s2 = t.stride()
@@ -638,15 +640,15 @@ def _rows(t, name):
 
 def _heads(t, name):
     """(shape, strides, address) of a bf16 CUDA [B, H, S, D] view, likewise."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype != _BF16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 4:
-        raise ValueError(f"{name} must be a 4-D [B, H, S, D] view")
     shape = t.shape
+    if len(shape) != 4:
+        raise ValueError(f"{name} must be a 4-D [B, H, S, D] view")
     b, h, n, d = shape
     if not (b and h and n and d):
         return shape, (0, 0, 0), t.data_ptr()
@@ -666,28 +668,16 @@ def _same_device(index, *tensors):
             raise ValueError(f"a tensor is on {t.device}, q on cuda:{index}")
 
 
-class _Launch:
-    """The device and stream of a call: the tensors' device becomes the current
-    one, and memory allocated inside belongs to the stream the kernels run on.
-    Enters as that stream's handle."""
-    __slots__ = ("_index", "_with")
-
-    def __init__(self, index, stream):
-        self._index = index
-        self._with = ()
-        if torch.cuda.current_device() != index:
-            self._with += (torch.cuda.device(index),)
-        if stream is not None:
-            self._with += (torch.cuda.stream(stream),)
-
-    def __enter__(self):
-        for c in self._with:
-            c.__enter__()
-        return _raw_stream(self._index)
-
-    def __exit__(self, *exc):
-        for c in reversed(self._with):
-            c.__exit__(*exc)
+def _on(index, stream, call):
+    """call(handle of the stream the kernels run on), with the tensors' device
+    current and memory allocated on that stream."""
+    if stream is None and torch.cuda.current_device() == index:
+        return call(_raw_stream(index))
+    with torch.cuda.device(index):
+        if stream is None:
+            return call(_raw_stream(index))
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
 
 
 def _cumulative(xs, name):
@@ -713,13 +703,27 @@ def _dense_common(q, k, v, cu_seqlens_q, cu_seqlens_kv):
     return qi, ki, vi, cq, ck
 
 
-def _fresh(like, cu):
-    """An output like a packed tensor, its rows past the last sequence 0."""
-    t = torch.empty_like(like)
-    rows, tail = like.shape[1], cu[-1]
-    if 0 <= tail < rows:
-        t[:, tail:].zero_()
-    return t
+def _output(t, like, info, cu, name):
+    """(tensor, head stride, row stride, address) of an output like the packed
+    tensor `like` (its _rows `info`): `t` if given, else a new one whose rows past
+    the last sequence are 0."""
+    if t is None:
+        t = torch.empty_like(like)
+        if 0 <= cu[-1] < info[1]:
+            t[:, cu[-1]:].zero_()
+        s0, s1, _ = t.stride()
+        return t, s0, s1, t.data_ptr()
+    if t.shape != like.shape:
+        raise ValueError(f"{name} must be shaped like its input, {tuple(like.shape)}")
+    i = _rows(t, name)
+    return t, i[3], i[4], i[5]
+
+
+def _workspace(t, need, like):
+    """(tensor, address, bytes)."""
+    if t is None:
+        t = torch.empty(max(need, 256), dtype=_U8, device=like.device)
+    return t, t.data_ptr(), t.numel() * t.element_size()
 
 
 def dense_attn_varlen(q, k, v, cu_seqlens_q, cu_seqlens_kv, *, causal: bool = True,
@@ -739,24 +743,23 @@ def dense_attn_varlen(q, k, v, cu_seqlens_q, cu_seqlens_kv, *, causal: bool = Tr
     qi, ki, vi, cq, ck = _dense_common(q, k, v, cu_seqlens_q, cu_seqlens_kv)
     index = q.get_device()
     _same_device(index, k, v, out)
-    with _Launch(index, stream) as st:
-        if out is None:
-            out = _fresh(q, cq)
-        elif out.shape != q.shape:
-            raise ValueError("out must be shaped like q")
-        oi = _rows(out, "out")
+
+    def call(st):
+        o, o0, o1, op = _output(out, q, qi, cq, "out")
         lse = None
         if return_lse:
-            lse = torch.empty((qi[0], qi[1]), dtype=torch.float32, device=q.device)
+            lse = torch.empty((qi[0], qi[1]), dtype=_F32, device=q.device)
             if 0 <= cq[-1] < qi[1]:
                 lse[:, cq[-1]:].zero_()
-        lay = _LAYOUT8.pack(0, qi[3], qi[4], 0, ki[3], ki[4], 0, vi[3], vi[4], 0, oi[3], oi[4],
+        lay = _LAYOUT8.pack(0, qi[3], qi[4], 0, ki[3], ki[4], 0, vi[3], vi[4], 0, o0, o1,
                             0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
         _check("dense_attn_varlen", lib().dense_attn_varlen(
             qi[5], ki[5], vi[5], lay, cq.buffer_info()[0], ck.buffer_info()[0], len(cq) - 1, qi[0], ki[0], qi[2],
-            qi[1], ki[1], 1 if causal else 0, 0.0 if scale is None else float(scale), oi[5],
+            qi[1], ki[1], 1 if causal else 0, 0.0 if scale is None else float(scale), op,
             None if lse is None else lse.data_ptr(), st))
-    return (out, lse) if return_lse else out
+        return (o, lse) if return_lse else o
+
+    return _on(index, stream, call)
 
 
 def dense_attn_varlen_backward(q, k, v, out, dout, lse, cu_seqlens_q, cu_seqlens_kv, *, causal: bool = True,
@@ -776,28 +779,24 @@ def dense_attn_varlen_backward(q, k, v, out, dout, lse, cu_seqlens_q, cu_seqlens
         raise ValueError(f"lse must be [Hq, q_rows] = {(qi[0], qi[1])}")
     index = q.get_device()
     _same_device(index, k, v, out, dout, lse, workspace, dq, dk, dv)
-    for n, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        if t is not None and t.shape != like.shape:
-            raise ValueError(f"{n} must be shaped like {n[1]}")
     L = lib()
-    with _Launch(index, stream) as st:
-        dq = _fresh(q, cq) if dq is None else dq
-        dk = _fresh(k, ck) if dk is None else dk
-        dv = _fresh(v, ck) if dv is None else dv
-        a, b, c = _rows(dq, "dq"), _rows(dk, "dk"), _rows(dv, "dv")
-        if workspace is None:
-            need = L.dense_attn_varlen_backward_workspace_size(
-                cq.buffer_info()[0], ck.buffer_info()[0], len(cq) - 1, qi[0], ki[0], qi[2], qi[1], ki[1],
-                1 if causal else 0)
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+
+    def call(st):
+        a, a0, a1, ap = _output(dq, q, qi, cq, "dq")
+        b, b0, b1, bp = _output(dk, k, ki, ck, "dk")
+        c, c0, c1, cp = _output(dv, v, vi, ck, "dv")
+        cqp, ckp, n = cq.buffer_info()[0], ck.buffer_info()[0], len(cq) - 1
+        need = 0 if workspace is not None else L.dense_attn_varlen_backward_workspace_size(
+            cqp, ckp, n, qi[0], ki[0], qi[2], qi[1], ki[1], 1 if causal else 0)
+        ws, wp, nbytes = _workspace(workspace, need, q)
         lay = _LAYOUT8.pack(0, qi[3], qi[4], 0, ki[3], ki[4], 0, vi[3], vi[4], 0, oi[3], oi[4],
-                            0, gi[3], gi[4], 0, a[3], a[4], 0, b[3], b[4], 0, c[3], c[4])
+                            0, gi[3], gi[4], 0, a0, a1, 0, b0, b1, 0, c0, c1)
         _check("dense_attn_varlen_backward", L.dense_attn_varlen_backward(
-            qi[5], ki[5], vi[5], oi[5], gi[5], lse.data_ptr(), lay, cq.buffer_info()[0], ck.buffer_info()[0],
-            len(cq) - 1, qi[0], ki[0], qi[2], qi[1], ki[1], 1 if causal else 0,
-            0.0 if scale is None else float(scale), a[5], b[5], c[5], workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), st))
-    return dq, dk, dv
+            qi[5], ki[5], vi[5], oi[5], gi[5], lse.data_ptr(), lay, cqp, ckp, n, qi[0], ki[0], qi[2], qi[1], ki[1],
+            1 if causal else 0, 0.0 if scale is None else float(scale), ap, bp, cp, wp, nbytes, st))
+        return a, b, c
+
+    return _on(index, stream, call)
 
 
 def shared_prefix_attn(q, k_prefix, v_prefix, k_suffix, v_suffix, suffix_lens, *,
@@ -829,22 +828,22 @@ def shared_prefix_attn(q, k_prefix, v_prefix, k_suffix, v_suffix, suffix_lens, *
     index = q.get_device()
     _same_device(index, k_prefix, v_prefix, k_suffix, v_suffix, suffix_lens, out, workspace)
     L = lib()
-    with _Launch(index, stream) as st:
-        if out is None:
-            out = torch.empty_like(q)
-        elif out.shape != q.shape:
+
+    def call(st):
+        o = torch.empty_like(q) if out is None else out
+        shape, os_, op = _heads(o, "out")
+        if shape != (B, Hq, T, D):
             raise ValueError("out must be shaped like q")
-        _, os_, op = _heads(out, "out")
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device) if return_lse else None
-        if workspace is None:
-            need = L.shared_prefix_attn_workspace_size(B, Hq, Hkv, T, D, P, cap)
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        lse = torch.empty((B, Hq, T), dtype=_F32, device=q.device) if return_lse else None
+        need = 0 if workspace is not None else L.shared_prefix_attn_workspace_size(B, Hq, Hkv, T, D, P, cap)
+        ws, wp, nbytes = _workspace(workspace, need, q)
         lay = _LAYOUT6.pack(*qs, *os_, 0, kp[3], kp[4], 0, vp[3], vp[4], *kss, *vss)
         _check("shared_prefix_attn", L.shared_prefix_attn(
             qp, kp[5], vp[5], ksp, vsp, suffix_lens.data_ptr(), lay, B, Hq, Hkv, T, D, P, cap,
-            0.0 if scale is None else float(scale), op, None if lse is None else lse.data_ptr(),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), st))
-    return (out, lse) if return_lse else out
+            0.0 if scale is None else float(scale), op, None if lse is None else lse.data_ptr(), wp, nbytes, st))
+        return (o, lse) if return_lse else o
+
+    return _on(index, stream, call)
 
 
 def build_vsa_metadata(T: int, Hh: int, W: int, tile=(4, 4, 4)) -> dict:
