@@ -207,6 +207,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x;
   const int warp = tid / 32, lane = tid % 32;
 
+  // the first item takes a search in memory: before all else
+  QItem first = {};
+  if (warp == 3) first = load_qitem(p, seqs, blockIdx.x);
+
   if (warp == 0) {
     for (int i = lane; i < L::kNumBars; i += 32) {
       // a TMA transaction, a commit or one thread's arrival, except where the
@@ -279,10 +283,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ===================== work items; rows that see no key =====================
       uint32_t n_item = 0;
       bool ok = true;
-      QItem x;
+      QItem x = first;
       Takeover take{bars + L::kTake, reinterpret_cast<uint4*>(smem + L::kTakeOff), 0};
       for (int it = blockIdx.x; ok && it >= 0; it = ok ? take.answer(abort_flag, p.status) : -1) {
-        x = load_qitem(p, seqs, it);
+        if (it != (int)blockIdx.x) x = load_qitem(p, seqs, it);
         if (x.n > 0) {
           // ask for more when this item's last tiles are on their way, not earlier:
           // what a CTA holds no other can take
@@ -714,6 +718,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x;
   const int warp = tid / 32, lane = tid % 32;
 
+  // the first item takes a search in memory: before all else
+  KItem first = {};
+  if (warp == 2) first = load_kitem(p, seqs, blockIdx.x);
+
   if (warp == 0) {
     for (int i = lane; i < L::kNumBars; i += 32) {
       const uint32_t count = (i == L::kDVEmpty || i == L::kDKEmpty) ? 4u
@@ -784,10 +792,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t once = l2_policy_evict_first();
       uint32_t n_item = 0;
       bool ok = true;
-      KItem x;
+      KItem x = first;
       Takeover take{bars + L::kTake, reinterpret_cast<uint4*>(smem + L::kTakeOff), 0};
       for (int it = blockIdx.x; ok && it >= 0; it = ok ? take.answer(abort_flag, p.status) : -1) {
-        x = load_kitem(p, seqs, it);
+        if (it != (int)blockIdx.x) x = load_kitem(p, seqs, it);
         if (x.n == 0) {
           take.ask(lane);
           for (int r = lane; r < x.keys; r += 32) {

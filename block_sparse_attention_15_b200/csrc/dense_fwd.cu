@@ -166,6 +166,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x;
   const int warp = tid / 32, lane = tid % 32;
 
+  // the first item takes a search in memory: before all else
+  Item first = {};
+  if (warp == 3) first = load_item(p, seqs, blockIdx.x);
+
   if (warp == 0) {
     for (int i = lane; i < L::kNumBars; i += 32) {
       // a TMA transaction, a commit or one thread's arrival, except where warps arrive
@@ -229,10 +233,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t pol = l2_policy_evict_first();
     uint32_t n = 0, cs0 = 0, cs1 = 0;  // items; Q tiles of the slots
     bool ok = true;
-    Item x;
+    Item x = first;
     Takeover take{bars + L::kTake, reinterpret_cast<uint4*>(smem + L::kTakeOff), 0};
     for (int it = blockIdx.x; ok && it >= 0; it = ok ? take.answer(abort_flag, p.status) : -1) {
-      x = load_item(p, seqs, it);
+      if (it != (int)blockIdx.x) x = load_item(p, seqs, it);
       if (x.n == 0) {
         // nothing to multiply: not handed on (the products look one item ahead, and
         // must not wait for one past those that the others have taken)

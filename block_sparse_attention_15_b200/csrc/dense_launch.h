@@ -12,11 +12,12 @@
 
 namespace vsa {
 
-// Sequences one launch takes; longer batches are split over launches.
-constexpr int kDenseMaxSeqs = 256;
+// Sequences one launch takes; longer batches are split over launches.  (With 128
+// a launch's parameters stay below 4 KB: 3.2 us of host time instead of 4.0.)
+constexpr int kDenseMaxSeqs = 128;
 
 // Packed sequences of one launch, passed by value (so a captured launch keeps
-// its lengths).  6.2 KB of the kernel's 32 KB of parameters.
+// its lengths).  3.1 KB.
 struct DenseSeqs {
   int n, n_flat;
   int n_units;                      // of all sequences (what a unit is, each kernel says)
@@ -111,7 +112,7 @@ struct PrefixParams {
   int B, Hq, Hkv, T, prefix_len, suffix_cap;
   float scale_log2;
   int* status;
-  int item_us;
+  int item_us;                      // microseconds that the longest share may take
   // filled by prefix_shape
   int group, rows_per_req;          // Hq / Hkv, group * T
   int pfx_blocks, sfx_blocks;       // row blocks of 256 of a prefix / suffix segment

@@ -43,6 +43,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "dense_attn.cuh"
 #include "dense_launch.h"
 #include "vsa.h"
@@ -889,7 +891,7 @@ size_t prefix_workspace(PrefixParams* p, int D, void* base) {
 }
 
 template <int D>
-static int launch_prefix_t(const PrefixParams& p, const CUtensorMap* m, cudaStream_t stream) {
+static int launch_prefix_t(PrefixParams p, const CUtensorMap* m, cudaStream_t stream) {
   using L = prefix::Layout<D>;
   auto kern = prefix::prefix_attn_kernel<D>;
   static KernelReady ready;
@@ -899,6 +901,8 @@ static int launch_prefix_t(const PrefixParams& p, const CUtensorMap* m, cudaStre
   const long long cap = (long long)p.Hkv * ((long long)p.pfx_blocks * ((p.prefix_len + 127LL) / 128) +
                                             (long long)p.B * p.sfx_blocks * ((p.suffix_cap + 127LL) / 128));
   const int grid = cap < kPrefixGrid ? (int)(cap > 0 ? cap : 1) : kPrefixGrid;
+  // 20 us per tile of a CTA's share, ten times what one takes: a wait may last a piece
+  p.item_us = (int)std::min(20 * (cap / grid + 1), 1000000000LL);
   kern<<<grid, prefix::kThreads, L::kAlloc, stream>>>(m[0], m[1], m[2], m[3], p);
   if (cudaGetLastError() != cudaSuccess) return VSA_ERR_CUDA;
   // set up while the attention kernel runs; waits for it before it reads partial results
@@ -916,8 +920,6 @@ static int launch_prefix_t(const PrefixParams& p, const CUtensorMap* m, cudaStre
 
 int launch_prefix(const PrefixParams& p_in, const PrefixTensors& t, int D, cudaStream_t stream) {
   PrefixParams p = p_in;
-  // a CTA's piece is a share of the line: far shorter than the waits' limit
-  p.item_us = 0;
   CUtensorMap m[4];
   const bool pfx = p.prefix_len > 0, sfx = p.suffix_cap > 0;
   // a part that is empty loads nothing; its map only has to be valid

@@ -568,7 +568,7 @@ typedef struct vsa_dense_layout {
  * lse      device fp32 [Hq, q_rows] or NULL; rows past the last sequence too
  * scale    <= 0 selects 1/sqrt(D)
  * D 64 or 128; Hq a multiple of Hkv (VSA_ERR_SHAPE).  16-byte aligned views.
- * No workspace; one launch per 256 sequences.
+ * No workspace; one launch per 128 sequences.
  */
 int dense_attn_varlen(const void* q, const void* k, const void* v, const vsa_dense_layout* layout,
                       const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_kv, int n_seqs, int Hq,
@@ -602,7 +602,7 @@ size_t dense_attn_varlen_backward_workspace_size(const int32_t* cu_seqlens_q, co
  *          rows past the last sequence are left as they were
  * workspace  device, >= dense_attn_varlen_backward_workspace_size(...),
  *          256-aligned; no two calls in flight may share it
- * Two or three launches on `stream` per 256 sequences.
+ * Two or three launches on `stream` per 128 sequences.
  */
 int dense_attn_varlen_backward(const void* q, const void* k, const void* v, const void* out, const void* dout,
                                const float* lse, const vsa_dense_layout* layout, const int32_t* cu_seqlens_q,

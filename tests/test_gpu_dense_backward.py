@@ -185,3 +185,40 @@ def test_refusals():
     with pytest.raises(B.VSAError):
         f(q, k, v, out, q, lse, cu_q, cu_kv, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
     assert B.get_device_status() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_no_keys_or_no_rows_at_all(d):
+    B = vsa()
+    q, dout = R.normal((4, 50, d), 90), R.normal((4, 50, d), 91)
+    none = torch.empty((2, 0, d), dtype=torch.bfloat16, device="cuda")
+    out, lse = B.dense_attn_varlen(q, none, none, [0, 20, 50], [0, 0, 0], return_lse=True)
+    assert (out == 0).all() and (lse == -float("inf")).all()
+    dq, dk, dv = B.dense_attn_varlen_backward(q, none, none, out, dout, lse, [0, 20, 50], [0, 0, 0])
+    assert (dq == 0).all() and dk.shape == dv.shape == none.shape
+    rows = torch.empty((4, 0, d), dtype=torch.bfloat16, device="cuda")
+    k, v = R.normal((2, 300, d), 92), R.normal((2, 300, d), 93)
+    out, lse = B.dense_attn_varlen(rows, k, v, [0, 0], [0, 300], return_lse=True)
+    dq, dk, dv = B.dense_attn_varlen_backward(rows, k, v, out, out, lse, [0, 0], [0, 300])
+    assert dq.shape == rows.shape and (dk == 0).all() and (dv == 0).all()
+    B.check_device_status()
+
+
+def test_calls_side_by_side():
+    """Forward and gradients on two streams at once, each with more items than
+    SMs and waiting for the other's: the results of the calls alone."""
+    sets = []
+    for seed, lens in ((95, [(700, 700), (900, 1111)]), (96, [(1000, 1000), (130, 400), (5, 0)])):
+        args = make(28, 4, 128, lens, seed=seed)
+        dout = R.normal(args[0].shape, seed)
+        sets.append((args, dout, gradients(*args, True, dout), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for args, dout, want, stream in sets:
+            with torch.cuda.stream(stream):
+                got.append((gradients(*args, True, dout), want))
+    torch.cuda.synchronize()
+    vsa().check_device_status()
+    for a, b in got:
+        assert all(torch.equal(x, y) for x, y in zip(a, b))

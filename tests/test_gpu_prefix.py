@@ -175,3 +175,21 @@ def test_refusals():
         got = B.shared_prefix_attn(q, kp, vp, ks, vs, torch.tensor([1, n, 3], dtype=torch.int32, device="cuda"))
         assert B.get_device_status() == 6 and torch.equal(got, want)
     assert B.get_device_status() == 0
+
+
+def test_calls_side_by_side():
+    """Two streams at once, each call with a workspace of its own."""
+    sets = []
+    for seed, shape in ((14, (17, 20, 4, 1, 128, 2000, 900)), (15, (9, 16, 2, 5, 64, 700, 600))):
+        cap, t = shape[-1], shape[3]
+        args = make(*shape, [t + (71 * i) % (cap - t) for i in range(shape[0])], seed=seed)
+        sets.append((args, vsa().shared_prefix_attn(*args), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(6):
+        for args, want, stream in sets:
+            got.append((vsa().shared_prefix_attn(*args, stream=stream), want))
+    torch.cuda.synchronize()
+    vsa().check_device_status()
+    for a, b in got:
+        assert torch.equal(a, b)
