@@ -16,7 +16,9 @@
 //   S[128][128] = Q . K^T       (operands in shared memory)
 //   O[128][D]  += P . V         (P in TMEM over its own S, V from shared memory)
 // The tensor pipe alternates between the slots, so one slot's softmax runs
-// under the other slot's products.  At D = 128 a product takes 596 cycles with
+// under the other slot's products.  Where there are no more query tiles than SMs
+// an item is one of them: both slots have it, take its key tiles in turn, and
+// their results are joined on the way out.  At D = 128 a product takes 596 cycles with
 // its A operand in TMEM and 861 with it in shared memory (measured: A's loads do
 // not overlap the products), so 1457 per tile bound the rate; TMEM is full (S and
 // O of two slots), which keeps Q out of it.
@@ -71,7 +73,7 @@ struct Slot {
 };
 
 struct Item {
-  int n;  // key tiles of slot 0, which has no fewer than slot 1
+  int n;  // key tiles; slot 0 has no fewer of them than slot 1
   int hk, kv0, kv_len;
   Slot slot0, slot1;
 };
@@ -86,8 +88,8 @@ struct Layout {
   static constexpr int NST = D == 128 ? 5 : 10;     // K/V ring
   static constexpr uint32_t kQOff = 0;               // [2]
   static constexpr uint32_t kRingOff = kQOff + 2 * kTile;
-  static constexpr uint32_t kInvLOff = kRingOff + NST * kTile;  // [2][128] f32
-  static constexpr uint32_t kItemOff = kInvLOff + 2u * 128u * 4u;
+  static constexpr uint32_t kMLOff = kRingOff + NST * kTile;  // [2][max, sum][128] f32
+  static constexpr uint32_t kItemOff = kMLOff + 2048u;
   static constexpr uint32_t kBarOff = kItemOff + (uint32_t)sizeof(Items);
   static constexpr int kQFull = 0, kQEmpty = 2, kFull = 4, kEmpty = kFull + NST,
                        kPre = kEmpty + NST, kSFull = kPre + NST, kPFull = kSFull + 2,
@@ -131,8 +133,14 @@ __device__ __forceinline__ Item load_item(const DenseParams& p, const DenseSeqs&
   x.kv_len = seq.w;
   const int u0 = ((seq.y + 127) >> 7) * p.group - 1 - p.slots * (t.units[un.seq] - 1 - un.rank);
   x.slot0 = get_slot(p, seq, x.hk, u0);
-  x.slot1 = get_slot(p, seq, x.hk, p.slots == 2 ? u0 - 1 : -1);
   x.n = x.slot0.n;
+  if (p.slots == 2) {
+    x.slot1 = get_slot(p, seq, x.hk, u0 - 1);
+  } else {
+    x.slot1 = x.slot0;
+    x.slot0.n = (x.n + 1) >> 1;
+    x.slot1.n = x.n >> 1;
+  }
   return x;
 }
 
@@ -157,7 +165,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     set_status(p.status, VSA_ERR_UNSUPPORTED);
     return;
   }
-  float* inv_l = reinterpret_cast<float*>(smem + L::kInvLOff);
+  float* ml = reinterpret_cast<float*>(smem + L::kMLOff);
+  const bool turns = p.slots == 1;  // the slots take an item's key tiles in turn
   Items* items = reinterpret_cast<Items*>(smem + L::kItemOff);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
@@ -241,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // nothing to multiply: not handed on (the products look one item ahead, and
         // must not wait for one past those that the others have taken)
 #pragma unroll 1
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < p.slots; ++s) {
           const Slot& sl = slot_of(x, s);
           for (int r = lane; r < sl.rows; r += 32) unseen_row<D>(p, sl, r);
         }
@@ -304,6 +313,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto tile = [&](uint32_t at) { return sbase + L::kRingOff + (at % NST) * L::kTile; };
       auto wait_stage = [&](uint32_t at) { wait(L::kFull + (int)(at % NST), at / NST); };
+      // which key tile is the j-th of slot s; whether slot s is the last to read it
+      auto key_tile = [&](int s, int j) { return turns ? 2 * j + s : j; };
+      auto last_reader = [&](const Item& x, int s, int j) { return turns || s == 1 || j >= x.slot1.n; };
       // what S(j) of slot s waits for, and S(j); the item's ring tiles start at gx
       auto before_s = [&](int s, int j, uint32_t gx) {
         if (j == 0) {
@@ -311,12 +323,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           q0 += s ^ 1;
           q1 += s;
         }
-        wait_stage(gx + 2 * j);
+        wait_stage(gx + 2 * key_tile(s, j));
       };
       auto do_s = [&](const Item& x, int s, int j, uint32_t gx) {
-        issue_s<D>(tmem_base + 128u * s, sbase + L::kQOff + s * L::kTile, tile(gx + 2 * j));
+        const uint32_t at = gx + 2 * key_tile(s, j);
+        issue_s<D>(tmem_base + 128u * s, sbase + L::kQOff + s * L::kTile, tile(at));
         umma_commit(bars + L::kSFull + s);
-        if (s == 1 || j >= x.slot1.n) umma_commit(bars + L::kEmpty + (int)((gx + 2 * j) % NST));
+        if (last_reader(x, s, j)) umma_commit(bars + L::kEmpty + (int)(at % NST));
         if (j == slot_of(x, s).n - 1) umma_commit(bars + L::kQEmpty + s);
       };
       auto next_one = [&](Item& x) {
@@ -335,13 +348,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (ok && have) {
         bool more = false;
         const uint32_t g_next = g + 2 * x.n;
-        const int n1 = x.slot1.n;
+        const int n0 = x.slot0.n, n1 = x.slot1.n;
 #pragma unroll 1
-        for (int i = 0; ok && i < 2 * x.n; ++i) {
-          const int s = i & 1, j = i >> 1, ns = s ? n1 : x.n;
+        for (int i = 0; ok && i < 2 * n0; ++i) {
+          const int s = i & 1, j = i >> 1, ns = s ? n1 : n0;
           if (j >= ns) {
             // slot 1 is through; its next item begins when slot 0 is, too
-            if (j == x.n - 1 && more && y.slot1.n > 0) {
+            if (j == n0 - 1 && more && y.slot1.n > 0) {
               before_s(1, 0, g_next);
               if (!ok) break;
               tc_fence_after_sync();
@@ -352,9 +365,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           // PV(j), then the next S: within an item what S will need first, so that it
           // follows at once (the next item's Q may still be on its way)
           const bool last = j + 1 == ns;
-          const uint32_t gv = g + 2 * j + 1;
+          const uint32_t gv = g + 2 * key_tile(s, j) + 1;
           wait_stage(gv);
-          // (the item's tiles are all here, so that the next one was asked for)
+          // (the item's tiles are here or on their way, so that the next one was asked for)
           if (s == 0 && last && ok) more = next_one(y);
           if (!last) before_s(s, j + 1, g);
           // the epilogue has emptied this slot's O
@@ -365,10 +378,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           p1 += s;
           if (!ok) break;
           tc_fence_after_sync();
-          const int keys = slot_of(x, s).last - 128 * j;
+          const int keys = slot_of(x, s).last - 128 * key_tile(s, j);
           issue_pv<D>(tmem_base + kTmemO + D * s, tmem_base + 128u * s, tile(gv),
                       keys >= 128 ? 8 : (keys + 15) >> 4, j > 0);
-          if (s == 1 || j >= n1) umma_commit(bars + L::kEmpty + (int)(gv % NST));
+          if (last_reader(x, s, j)) umma_commit(bars + L::kEmpty + (int)(gv % NST));
           if (last) {
             umma_commit(bars + L::kOFull + s);
             d0 += s ^ 1;
@@ -376,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!last) {
             do_s(x, s, j + 1, g);
-          } else if (j == x.n - 1 && more && slot_of(y, s).n > 0) {
+          } else if (j == n0 - 1 && more && slot_of(y, s).n > 0) {
             before_s(s, 0, g_next);
             if (!ok) break;
             tc_fence_after_sync();
@@ -405,10 +418,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t l2[2] = {0, 0};
       for (int j = 0; j < sl.n; ++j, ++g) {
         // columns of the tile that rows see: one more per row where causal
-        int rem[2], whole = x.kv_len - 128 * j, none = whole;
+        const int key = 128 * (turns ? 2 * j + s : j);
+        int rem[2], whole = x.kv_len - key, none = whole;
         rem[0] = rem[1] = whole;
         if (p.causal) {
-          const int r0 = sl.lim0 + first_row - 128 * j;
+          const int r0 = sl.lim0 + first_row - key;
           rem[0] = min(whole, r0 + lane / 4);
           rem[1] = min(whole, r0 + lane / 4 + 8);
           none = min(whole, r0 + 15);
@@ -422,18 +436,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bars + L::kPFull + s);
       }
       if (!ok) break;
-      // hand 1 / l to the epilogue, once it has taken the previous item's
+      // hand max and sum to the epilogue, once it has taken the previous item's
       if (n >= 1 && !warp_wait(bars + L::kOEmpty + s, (n - 1) & 1, abort_flag, p.status)) { ok = false; break; }
       ++n;
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const float l = quad_sum(l2[b]);
-        const int row = first_row + lane / 4 + 8 * b;
         if ((lane & 3) == 0) {
-          inv_l[s * 128 + row] = l == 0.f ? 0.f : 1.f / l;
-          if (p.lse && row < sl.rows)
-            p.lse[sl.head * p.lse_seq + sl.row0 + row] =
-                l == 0.f ? -INFINITY : (m[b] + __log2f(l)) * 0.69314718055994531f;
+          ml[s * 256 + first_row + lane / 4 + 8 * b] = m[b];
+          ml[s * 256 + 128 + first_row + lane / 4 + 8 * b] = l;
         }
       }
       __syncwarp();
@@ -455,36 +466,63 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (sl.rows == 0) continue;
         const bool real = row < sl.rows;
         if (sl.n == 0) {
-          if (real) unseen_row<D>(p, sl, row);
+          if (real && !turns) unseen_row<D>(p, sl, row);
           continue;
         }
-        __nv_bfloat16* orow = p.out + sl.head * p.out_st.h + (long long)(sl.row0 + row) * p.out_st.s;
         const uint32_t ph = (s ? cs1 : cs0) & 1;
         cs0 += s ^ 1;
         cs1 += s;
         if (!warp_wait(bars + L::kLFull + s, ph, abort_flag, p.status) ||
             !warp_wait(bars + L::kOFull + s, ph, abort_flag, p.status)) { ok = false; break; }
+        // slots that took turns are written together
+        const bool both = turns && x.slot1.n > 0;
+        if (both && k == 0) continue;
         tc_fence_after_sync();
-        const float il = inv_l[s * 128 + row];
+        const int s0 = both ? 0 : s;
+        float top = ml[s0 * 256 + row], sum = ml[s0 * 256 + 128 + row], w0 = 1.f, w1 = 0.f;
+        if (both) {
+          const float m0 = top, m1 = ml[256 + row], l1 = ml[384 + row];
+          top = fmaxf(m0, m1);
+          const float ref = top == -INFINITY ? 0.f : top;
+          w0 = fast_exp2(m0 - ref);
+          w1 = fast_exp2(m1 - ref);
+          sum = sum * w0 + l1 * w1;
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        w0 *= inv;
+        w1 *= inv;
+        if (p.lse && real)
+          p.lse[sl.head * p.lse_seq + sl.row0 + row] =
+              sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994531f;
+        __nv_bfloat16* orow = p.out + sl.head * p.out_st.h + (long long)(sl.row0 + row) * p.out_st.s;
 #pragma unroll 1
-        for (int q0 = 0; q0 < D; q0 += 32) {
-          uint32_t ov[32];
-          tmem_ld32(t_lane + D * s + q0, ov);
-          if (q0 + 32 == D) {
+        for (int q0 = 0; q0 < D; q0 += 16) {
+          uint32_t ov[16], o1[16];
+          VSA_TMEM_LD16(t_lane + D * s0 + q0, ov, 0);
+          if (both) VSA_TMEM_LD16(t_lane + D + q0, o1, 0);
+          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+          if (q0 + 16 == D) {
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bars + L::kOEmpty + s);
+            if (lane == 0) {
+              mbar_arrive(bars + L::kOEmpty + s0);
+              if (both) mbar_arrive(bars + L::kOEmpty + 1);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float f = __uint_as_float(ov[e]) * w0;
+            if (both) f = fmaf(__uint_as_float(o1[e]), w1, f);
+            ov[e] = __float_as_uint(f);
           }
           if (real) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint32_t o[4];
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                o[q] = pack_bf16x2(__uint_as_float(ov[e + 2 * q]) * il,
-                                   __uint_as_float(ov[e + 2 * q + 1]) * il);
-              *reinterpret_cast<uint4*>(orow + q0 + e) = make_uint4(o[0], o[1], o[2], o[3]);
-            }
+            for (int e = 0; e < 16; e += 8)
+              *reinterpret_cast<uint4*>(orow + q0 + e) = make_uint4(
+                  pack_bf16x2(__uint_as_float(ov[e]), __uint_as_float(ov[e + 1])),
+                  pack_bf16x2(__uint_as_float(ov[e + 2]), __uint_as_float(ov[e + 3])),
+                  pack_bf16x2(__uint_as_float(ov[e + 4]), __uint_as_float(ov[e + 5])),
+                  pack_bf16x2(__uint_as_float(ov[e + 6]), __uint_as_float(ov[e + 7])));
           }
         }
       }
@@ -608,9 +646,9 @@ int launch_dense_fwd(const DenseParams& p_in, const DenseTensors& t, const Dense
     long long slots = 0;
     for (int i = 0; i < n; ++i) slots += (seqs[i].y + 127LL) / 128 * p.Hq;
     if (slots >= (1 << 30)) return VSA_ERR_UNSUPPORTED;  // 32-bit item index
-    // Two row tiles per item halve the K/V reads and let one slot's softmax run
-    // under the other's products; with no more row tiles than SMs one tile per
-    // item spreads them over twice as many SMs instead.
+    // Two row tiles per item halve the K/V reads; with no more row tiles than SMs
+    // one tile per item spreads them over twice as many SMs instead (one sequence
+    // of 2000 rows, 8 heads: @A1@ us in pairs, @A2@ one by one).
     p.slots = slots > device_sm_count() ? 2 : 1;
     for (int i = 0; i < n; ++i) {
       units[i] = ((seqs[i].y + 127) / 128 * p.group + p.slots - 1) / p.slots;
