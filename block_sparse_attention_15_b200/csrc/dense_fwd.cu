@@ -16,9 +16,9 @@
 //   S[128][128] = Q . K^T       (operands in shared memory)
 //   O[128][D]  += P . V         (P in TMEM over its own S, V from shared memory)
 // The tensor pipe alternates between the slots, so one slot's softmax runs
-// under the other slot's products.  Where there are no more query tiles than SMs
-// an item is one of them: both slots have it, take its key tiles in turn, and
-// their results are joined on the way out.  At D = 128 a product takes 596 cycles with
+// under the other slot's products.  With at most two query tiles
+// per SM an item is one of them: both slots have it, take its key tiles in turn,
+// and their results are joined on the way out.  At D = 128 a product takes 596 cycles with
 // its A operand in TMEM and 861 with it in shared memory (measured: A's loads do
 // not overlap the products), so 1457 per tile bound the rate; TMEM is full (S and
 // O of two slots), which keeps Q out of it.
@@ -646,10 +646,11 @@ int launch_dense_fwd(const DenseParams& p_in, const DenseTensors& t, const Dense
     long long slots = 0;
     for (int i = 0; i < n; ++i) slots += (seqs[i].y + 127LL) / 128 * p.Hq;
     if (slots >= (1 << 30)) return VSA_ERR_UNSUPPORTED;  // 32-bit item index
-    // Two row tiles per item halve the K/V reads; with no more row tiles than SMs
-    // one tile per item spreads them over twice as many SMs instead (one sequence
-    // of 2000 rows, 8 heads: @A1@ us in pairs, @A2@ one by one).
-    p.slots = slots > device_sm_count() ? 2 : 1;
+    // Two row tiles per item halve the K/V reads; up to two tiles per SM, one
+    // tile per item whose key tiles the slots share ends sooner (rows x heads, us
+    // with pairs and with single tiles: 1000 x 20: 28.7, 20.5; 3000 x 12: 59.4,
+    // 46.1; above it they tie: 1000 x 40: 30.7, 28.7-30.7; 2000 x 40: 61.4, 61.4).
+    p.slots = slots > 2 * device_sm_count() ? 2 : 1;
     for (int i = 0; i < n; ++i) {
       units[i] = ((seqs[i].y + 127) / 128 * p.group + p.slots - 1) / p.slots;
       // behind cached keys the first rows, too, have many to see
