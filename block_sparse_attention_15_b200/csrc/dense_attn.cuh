@@ -251,11 +251,11 @@ __device__ __forceinline__ void tmem_st_16x128_32(uint32_t taddr, const uint32_t
 // exponentiated without moving the reference: probabilities stay below 2^8.
 constexpr float kRefresh = 8.f;
 
-// One 128-key tile of the online softmax, by a warp that has 16 rows of the
-// query tile (TMEM lanes from t_s's on): a thread has rows lane / 4 + 8 b and a
-// quarter of their columns.  Two warps share the 32 lanes that each may reach,
-// so that a slot's softmax is eight warps' work, and a row stays within one warp:
-// its max takes two shuffles, its sum none until the end.
+// One 128-key tile of the online softmax, by a warp that has 8 NB rows of the
+// query tile (TMEM lanes from t_s's on): a thread has rows lane / 4 + 8 b, b < NB,
+// and a quarter of their columns.  In the forward kernel NB is 2: 
+// two warps share the 32 lanes that each may reach, so that a slot's softmax is
+// eight warps' work.  A row stays within one warp: its max takes two shuffles, its sum none until the end.
 // S is read twice (a load takes 50 cycles) rather than kept in 64 registers.
 //   rem[b]: columns of the tile that row b sees; whole / none: the least and the
 //   largest of those over the warp, at most 128
@@ -263,16 +263,18 @@ constexpr float kRefresh = 8.f;
 //   when a reference moves (S complete implies the PV before it is: one thread
 //   issued both, in order)
 // POLY of eight column pairs take their exponential on the FMA pipe.
-template <int D, int POLY, int UNROLL>
-__device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, float c, const int (&rem)[2], int whole,
-                                             int none, bool first, int lane, float (&m)[2], uint64_t (&l2)[2]) {
+template <int D, int POLY, int UNROLL, int NB>
+__device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, float c, const int (&rem)[NB], int whole,
+                                             int none, bool first, int lane, float (&m)[NB], uint64_t (&l2)[NB]) {
   const int col0 = 2 * (lane & 3);
   auto mask = [&](uint32_t (&v)[32], int q0) {
 #pragma unroll
     for (int k = 0; k < 32; ++k)
-      if (8 * (k >> 2) + (k & 1) >= rem[(k >> 1) & 1] - q0 - col0) v[k] = 0xff800000u;  // -inf
+      if (((k >> 1) & 1) < NB && 8 * (k >> 2) + (k & 1) >= rem[(k >> 1) & (NB - 1)] - q0 - col0) v[k] = 0xff800000u;  // -inf
   };
-  float mx[2] = {-INFINITY, -INFINITY};
+  float mx[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) mx[b] = -INFINITY;
 #pragma unroll UNROLL
   for (int q0 = 0; q0 < 128; q0 += 64) {
     if (q0 >= none) break;
@@ -282,13 +284,13 @@ __device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, float c
 #pragma unroll
     for (int k = 0; k < 32; k += 4) {
       mx[0] = fmax3(mx[0], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-      mx[1] = fmax3(mx[1], __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+      if (NB == 2) mx[NB - 1] = fmax3(mx[NB - 1], __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
     }
   }
-  float nm[2];
+  float nm[NB];
   bool move = false;
 #pragma unroll
-  for (int b = 0; b < 2; ++b) {
+  for (int b = 0; b < NB; ++b) {
     mx[b] = fmaxf(mx[b], __shfl_xor_sync(0xffffffffu, mx[b], 1));
     mx[b] = fmaxf(mx[b], __shfl_xor_sync(0xffffffffu, mx[b], 2)) * c;
     const bool up = mx[b] > m[b] + kRefresh;
@@ -296,9 +298,9 @@ __device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, float c
     move = move || up;
   }
   if (__any_sync(0xffffffffu, move)) {
-    float a[2];
+    float a[NB];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < NB; ++b) {
       // 1 where the reference stays; 0 while nothing was seen (O and the sum are 0)
       a[b] = m[b] == -INFINITY ? 0.f : fast_exp2(m[b] - nm[b]);
       float la, lb;
@@ -313,7 +315,8 @@ __device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, float c
         tmem_ld_16x256(t_o + q0, ov, 0);
         asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-        for (int k = 0; k < 16; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * a[(k >> 1) & 1]);
+        for (int k = 0; k < 16; ++k)
+          if (((k >> 1) & 1) < NB) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * a[(k >> 1) & (NB - 1)]);
         tmem_st_16x256(t_o + q0, ov);
       }
     }
@@ -321,9 +324,9 @@ __device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, float c
   // probabilities 2^(s c - m): bf16 pairs for the tensor core, fp32 sums.  P's 32
   // columns per step lie over columns of S that were read before.
   const uint64_t cc = pk2(c, c);
-  uint64_t nm2[2];
+  uint64_t nm2[NB];
 #pragma unroll
-  for (int b = 0; b < 2; ++b) {
+  for (int b = 0; b < NB; ++b) {
     const float ref = m[b] == -INFINITY ? 0.f : -m[b];  // nothing seen yet: all -inf, all 0
     nm2[b] = pk2(ref, ref);
   }
@@ -343,15 +346,20 @@ __device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, float c
       if (kMask) mask(v, q0);
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
+        if ((k & 1) >= NB) {  // a row of none of this warp's
+          pk[k] = 0u;
+          continue;
+        }
+        const int w = k & (NB - 1);
         float a, b;
-        upk2(ffma2(pk2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), cc, nm2[k & 1]), a, b);
+        upk2(ffma2(pk2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), cc, nm2[w]), a, b);
         if (!kMask && (k & 7) < POLY) {
           upk2(exp2_fma2_t<true>(a, b), a, b);
         } else {
           a = fast_exp2(a);
           b = fast_exp2(b);
         }
-        l2[k & 1] = fadd2(l2[k & 1], pk2(a, b));
+        l2[w] = fadd2(l2[w], pk2(a, b));
         pk[k] = pack_bf16x2(a, b);
       }
     };

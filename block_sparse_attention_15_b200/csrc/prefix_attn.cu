@@ -263,6 +263,13 @@ __device__ __forceinline__ int slot_rows(const Piece& x, int s) {
   return split_rows(x) ? min(128, x.rows - 128 * s) : x.rows;
 }
 
+// Rows a softmax warp has, as a power of two.  A tile of few rows spreads them
+// over the four warps (row i in TMEM lane 32 (i >> shift) + its low bits), four
+// lanes to a row: a chain of product, softmax, product bounds the rate of such
+// tiles, and one thread to a row takes @L1@ cycles for its 128 columns, four take
+// @L2@.
+__device__ __forceinline__ int row_shift(const Piece& x) { return x.rows <= 32 ? 3 : x.rows <= 64 ? 4 : 5; }
+
 // The products, out of line: they are issued from several places.
 template <int D>
 static __device__ __noinline__ void s_product(uint32_t tmem_d, uint32_t q_base, uint32_t k_base) {
@@ -274,15 +281,15 @@ static __device__ __noinline__ void pv_product(uint32_t tmem_o, uint32_t tmem_p,
   dense::issue_pv<D>(tmem_o, tmem_p, v_base, steps, accumulate);
 }
 
-// This warp's rows of a partial result: O (or both slots' O, D columns apart)
-// from TMEM times the row's weight, which lane r has for the warp's row r.  Four
+// Rows [r0, r_end) of a partial result, up to 32 in this warp's TMEM lanes: O (or both slots' O, D columns apart)
+// from TMEM times the row's weight, which lane i has for row r0 + i.  Four
 // lanes write 64 bytes of a row.
 template <int D>
-static __device__ __noinline__ void write_part(float* o, int rows, int wq, int lane, uint32_t t_o, bool both,
+static __device__ __noinline__ void write_part(float* o, int r0, int r_end, int lane, uint32_t t_o, bool both,
                                            float w0, float w1) {
 #pragma unroll 1
   for (int u = 0; u < 2; ++u) {
-    if (32 * wq + 16 * u >= rows) break;
+    if (r0 + 16 * u >= r_end) break;
     float a0[2], a1[2];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
@@ -307,11 +314,11 @@ static __device__ __noinline__ void write_part(float* o, int rows, int wq, int l
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int b = k & 1, lo = 8 * (k >> 1) + 2 * b, hi = lo + 4;  // registers of groups 2 (k / 2), + 1
-        const int r = 32 * wq + 16 * u + 8 * b + lane / 4;
+        const int r = r0 + 16 * u + 8 * b + lane / 4;
         const uint32_t sx = odd ? va[lo] : va[hi], sy = odd ? va[lo + 1] : va[hi + 1];
         const uint32_t rx = __shfl_xor_sync(0xffffffffu, sx, 1), ry = __shfl_xor_sync(0xffffffffu, sy, 1);
         const uint4 f = odd ? make_uint4(rx, ry, va[hi], va[hi + 1]) : make_uint4(va[lo], va[lo + 1], rx, ry);
-        if (r < rows)
+        if (r < r_end)
           *reinterpret_cast<uint4*>(o + (long long)r * D + q0 + 16 * (k >> 1) + (odd ? 8 : 0) + 2 * (lane & 2)) = f;
       }
     }
@@ -523,10 +530,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
   } else if (warp < 12) {
-    // ===================== softmax: one thread per row =====================
+    // ============ softmax: one thread per row, or four (row_shift) ============
     const int s = (warp - 4) >> 2;
     const int wq = warp & 3;
-    const int row = wq * 32 + lane;
     const uint32_t t_s = tmem_base + (uint32_t(wq * 32) << 16) + 128u * s;
     const uint32_t t_o = tmem_base + (uint32_t(wq * 32) << 16) + kTmemO + D * s;
     const float c = p.scale_log2;
@@ -537,17 +543,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && next(n_got, x)) {
       const int nt = slot_tiles(x, s);
       if (nt == 0) continue;  // a piece of one key tile leaves one slot nothing
-      const bool any = 32 * wq < slot_rows(x, s);  // this warp has rows
-      int limit = x.kv_len;                        // keys the row sees
-      if (x.b >= 0) limit += 1 - p.T + (256 * x.blk + (split_rows(x) ? 128 * s : 0) + row) % p.T;
-      float m = -INFINITY;
-      uint64_t l2 = pk2(0.f, 0.f);
+      const int shift = row_shift(x);
+      const bool any = (wq << shift) < slot_rows(x, s);  // this warp has rows
+      // this thread's row, or the first of them
+      const int row = (wq << shift) + (shift < 5 ? lane >> 2 : lane);
+      auto keys_seen = [&](int r) {
+        return x.kv_len + (x.b < 0 ? 0 : 1 - p.T + (256 * x.blk + (split_rows(x) ? 128 * s : 0) + r) % p.T);
+      };
+      const int limit = keys_seen(row), limit8 = keys_seen(row + 8);
+      float m = -INFINITY, m8 = -INFINITY;
+      uint64_t l2 = pk2(0.f, 0.f), l28 = l2;
       for (int j = 0; j < nt; ++j, ++g) {
         if (!warp_wait(bars + L::kSFull + s, g & 1, abort_flag, p.status)) { ok = false; break; }
         tc_fence_after_sync();
-        if (any) {
+        const int key0 = 128 * (x.tile0 + slot_tile(x, s, j));
+        if (any && shift == 3) {
+          const int rem[1] = {min(128, limit - key0)};
+          float mm[1] = {m};
+          uint64_t ll[1] = {l2};
+          dense::softmax_tile<D, 0, 1>(t_s, t_o, c, rem, __reduce_min_sync(0xffffffffu, rem[0]),
+                                       __reduce_max_sync(0xffffffffu, rem[0]), j == 0, lane, mm, ll);
+          m = mm[0], l2 = ll[0];
+        } else if (any && shift == 4) {
+          const int rem[2] = {min(128, limit - key0), min(128, limit8 - key0)};
+          float mm[2] = {m, m8};
+          uint64_t ll[2] = {l2, l28};
+          dense::softmax_tile<D, 0, 1>(t_s, t_o, c, rem, __reduce_min_sync(0xffffffffu, min(rem[0], rem[1])),
+                                       __reduce_max_sync(0xffffffffu, max(rem[0], rem[1])), j == 0, lane, mm, ll);
+          m = mm[0], m8 = mm[1], l2 = ll[0], l28 = ll[1];
+        } else if (any) {
           // columns before `whole` are seen by all of the warp's rows, from `none` on by none
-          const int rem = min(128, limit - 128 * (x.tile0 + slot_tile(x, s, j)));
+          const int rem = min(128, limit - key0);
           const int whole = __reduce_min_sync(0xffffffffu, rem), none = __reduce_max_sync(0xffffffffu, rem);
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
@@ -628,9 +654,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the epilogue has read the slot's previous maxima and sums
       if (n >= 1 && !warp_wait(bars + L::kOEmpty + s, (n - 1) & 1, abort_flag, p.status)) { ok = false; break; }
       ++n;
-      float la, lb;
-      upk2(l2, la, lb);
-      const float l = la + lb;
+      float la, lb, l;
+      if (shift < 5) {
+        l = dense::quad_sum(l2);
+        const float l8 = dense::quad_sum(l28);
+        if (shift == 4 && (lane & 3) == 0) ml[s * 256 + row + 8] = m8, ml[s * 256 + 136 + row] = l8;
+      } else {
+        upk2(l2, la, lb);
+        l = la + lb;
+      }
+      // (four lanes may write the same)
       ml[s * 256 + row] = m;
       ml[s * 256 + 128 + row] = l;
       __syncwarp();
@@ -643,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (any) {
           const long long at = x.part * (x.b < 0 ? p.pfx_rows : p.sfx_rows) + 128 * s;
           if (row < rows) (x.b < 0 ? p.part_lse_p : p.part_lse_s)[at + row] = l == 0.f ? -INFINITY : m + __log2f(l);
-          write_part<D>((x.b < 0 ? p.part_p : p.part_s) + at * D, rows, wq, lane, t_o, false,
+          write_part<D>((x.b < 0 ? p.part_p : p.part_s) + at * D, 32 * wq, rows, lane, t_o, false,
                         l == 0.f ? 0.f : 1.f / l, 0.f);
         }
         tc_fence_before_sync();
@@ -669,7 +702,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; freed < need; ++freed)
         if (!warp_wait(bars + L::kQFree + (int)(freed & 1), (freed >> 1) & 1, abort_flag, p.status)) return false;
       constexpr int CH = D / 8, RPI = 32 / CH;  // chunks of a row, rows per access of the warp
-      for (int r0 = 32 * wq; r0 < x.rows; r0 += 128) {
+      const int shift = row_shift(x);
+      for (int r0 = wq << shift; r0 < x.rows; r0 += 128) {
         // this lane's row
         int i = 256 * x.blk + r0 + lane, b = x.b;
         if (b < 0) {
@@ -679,12 +713,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int gi = i / p.T;
         const long long off = b * p.q_st.b + (long long)(x.h * p.group + gi) * p.q_st.h + (long long)(i - gi * p.T) * p.q_st.s;
         uint8_t* qt = smem + L::kQOff + (split ? r0 >> 7 : (int)(n & 1)) * L::kTile;
-        const int rows = min(32, x.rows - r0), ch = lane % CH;
+        const int rows = min(1 << shift, x.rows - r0), ch = lane % CH;
 #pragma unroll 4
         for (int r = 0; r < rows; r += RPI) {
           const int mine = r + lane / CH;
           const long long from = __shfl_sync(0xffffffffu, off, mine & 31);
-          const int at = (r0 & 127) + mine;
+          const int at = 32 * wq + mine;
           // all rows in flight at once, none of them in registers
           if (mine < rows)
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
@@ -733,10 +767,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (s == 0) continue;
         tc_fence_after_sync();
-        if (32 * wq < x.rows) {
+        const int shift = row_shift(x), r0 = wq << shift, r_end = min(x.rows, r0 + (1 << shift));
+        if (r0 < x.rows) {
           // weights of the slots' sums for this lane's row
           float w0 = 1.f, w1 = 0.f;
-          const int row = 32 * wq + lane;
+          const int row = r0 + lane;
           const int s0 = has0 ? 0 : 1;
           const float m0 = ml[s0 * 256 + row], l0 = ml[s0 * 256 + 128 + row];
           float top = m0, sum = l0;
@@ -750,8 +785,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
           const long long at = x.part * (x.b < 0 ? p.pfx_rows : p.sfx_rows);
-          if (row < x.rows) (x.b < 0 ? p.part_lse_p : p.part_lse_s)[at + row] = sum == 0.f ? -INFINITY : top + __log2f(sum);
-          write_part<D>((x.b < 0 ? p.part_p : p.part_s) + at * D, x.rows, wq, lane, t_lane + D * s0, two, w0 * inv, w1 * inv);
+          if (row < r_end) (x.b < 0 ? p.part_lse_p : p.part_lse_s)[at + row] = sum == 0.f ? -INFINITY : top + __log2f(sum);
+          write_part<D>((x.b < 0 ? p.part_p : p.part_s) + at * D, r0, r_end, lane, t_lane + D * s0, two, w0 * inv, w1 * inv);
         }
         tc_fence_before_sync();
         __syncwarp();
