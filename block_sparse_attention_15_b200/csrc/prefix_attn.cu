@@ -258,6 +258,14 @@ __device__ __forceinline__ int slot_tiles(const Piece& x, int s) {
 __device__ __forceinline__ int slot_tile(const Piece& x, int s, int j) {
   return split_rows(x) ? j : 2 * j + (s ^ x.turn);
 }
+// Place of K and V of tile t among a piece's 2 n ring tiles: in the order of the
+// products that read them.  Where the slots alternate that is S(0) S(1) PV(0) S(2)
+// PV(1) ..: loaded tile by tile, K(t + 2) would wait for V(t)'s stage instead of
+// V(t - 1)'s (2400 cycles a tile instead of @R1@).
+__device__ __forceinline__ int place_k(const Piece& x, int t) { return split_rows(x) ? 2 * t : max(0, 2 * t - 1); }
+__device__ __forceinline__ int place_v(const Piece& x, int t) {
+  return split_rows(x) ? 2 * t + 1 : min(2 * t + 2, 2 * x.n - 1);
+}
 // Real rows of a slot.
 __device__ __forceinline__ int slot_rows(const Piece& x, int s) {
   return split_rows(x) ? min(128, x.rows - 128 * s) : x.rows;
@@ -398,8 +406,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t u = g / NST;
             if (u >= 1) ok = mbar_wait(bars + L::kEmpty + st, (u - 1) & 1, abort_flag, p.status);
             if (!ok) break;
-            const bool is_v = j & 1;
-            const int key = 128 * (x.tile0 + (j >> 1));
+            const bool order = split_rows(x) || j == 0 || j == 2 * x.n - 1;  // see place_k
+            const bool is_v = order ? j & 1 : !(j & 1);
+            const int key = 128 * (x.tile0 + (order ? j >> 1 : is_v ? (j >> 1) - 1 : (j + 1) >> 1));
             uint64_t* full = bars + (is_v && x.kv_len - key < 128 ? L::kPre : L::kFull) + st;
             uint8_t* dst = smem + L::kRingOff + st * L::kTile;
             const CUtensorMap* map = own ? (is_v ? &tm_vs : &tm_ks) : (is_v ? &tm_vp : &tm_kp);
@@ -456,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto do_s = [&](const Piece& x, uint32_t n, int s, int j, uint32_t gx) {
           const int tile = slot_tile(x, s, j);
           const bool split = split_rows(x);
-          const uint32_t gk = gx + 2 * tile;
+          const uint32_t gk = gx + place_k(x, tile);
           if (n_q == n) {  // the piece's first product
             wait(L::kQFull + (int)(n & 1), n >> 1);
             ++n_q;
@@ -495,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the slots in turn
             const int s = (i & 1) ^ x.turn, j = i >> 1, ns = slot_tiles(x, s);
             const int tile = slot_tile(x, s, j);
-            const uint32_t gv = g + 2 * tile + 1;
+            const uint32_t gv = g + place_v(x, tile);
             const int st = (int)(gv % NST);
             wait(L::kFull + st, gv / NST);
             // the epilogue has emptied this slot's O
