@@ -47,6 +47,18 @@ static __device__ __noinline__ bool warp_poll(uint64_t* bar, uint32_t parity, vo
   if ((threadIdx.x & 31) == 0) ok = mbar_poll(bar, parity, abort_flag, status) ? 1 : 0;
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
+// Whether the phase is complete, at once.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
   return mbar_try_wait(bar, parity) || mbar_poll(bar, parity, abort_flag, status);
 }
@@ -253,9 +265,9 @@ constexpr float kRefresh = 8.f;
 
 // One 128-key tile of the online softmax, by a warp that has 8 NB rows of the
 // query tile (TMEM lanes from t_s's on): a thread has rows lane / 4 + 8 b, b < NB,
-// and a quarter of their columns.  In the forward kernel NB is 2: 
-// two warps share the 32 lanes that each may reach, so that a slot's softmax is
-// eight warps' work.  A row stays within one warp: its max takes two shuffles, its sum none until the end.
+// and a quarter of their columns.  In the forward kernel two warps share the 32
+// lanes that each may reach, so that a slot's softmax is eight warps' work.  A row
+// stays within one warp: its max takes two shuffles, its sum none until the end.
 // S is read twice (a load takes 50 cycles) rather than kept in 64 registers.
 //   rem[b]: columns of the tile that row b sees; whole / none: the least and the
 //   largest of those over the warp, at most 128

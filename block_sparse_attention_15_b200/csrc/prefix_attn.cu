@@ -28,16 +28,17 @@
 //
 // 512 threads: warp 0 loads K and V tiles, warp 1 (one thread) issues products,
 // warp 2 zeroes what a segment's last V tile holds past its keys, warp 3 walks
-// the line, warps 4-7 and 8-11 are the slots' softmax (one thread per row; warps
-// without rows pass), warps 12-15 gather the next piece's Q rows and write the
+// the line, warps 4-7 and 8-11 are the slots' softmax (one thread per row, or four
+// where there are few; warps without rows pass), warps 12-15 gather the next piece's Q rows and write the
 // last one's results.  Loops are kept short: the first pass through each line of
 // code costs an instruction fetch that waits behind the K/V stream (a softmax
 // unrolled over its 128 columns spent 25 us of a call on that).
 //
 // Measured at D = 128: 24 requests of 9216 keys at most, 56 heads over 8, no
-// prefix: 90 us, 5.0 TB/s; 64 requests behind 15488 shared keys, 40 heads over 8:
-// 94 us, 3.5 TB/s (an SM streams 46 GB/s: its ring over the loaded latency, and
-// the SMs that work on the prefix stream nothing); 16 requests of 5 tokens: 41 us.
+// prefix: 86 us, 5.3 TB/s; 64 requests behind 15488 shared keys, 40 heads over 8:
+// 96 us, 3.5 TB/s (a tile of the prefix takes 4600 cycles for its 256 rows, one of
+// a suffix 2300: every SM is busy, fewer than half of the time with a stream);
+// 16 requests of 5 tokens: 38 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -105,7 +106,7 @@ __device__ __forceinline__ int suffix_len(const PrefixParams& p, int b) {
 __device__ __forceinline__ int key_tiles(int keys) { return (keys + 127) >> 7; }
 
 // The line of key tiles (see the header comment), measured in units: a tile of a
-// block of more than 128 rows costs both slots a pass (3700 cycles against 1950
+// block of more than 128 rows costs both slots a pass (4600 cycles against 2300
 // measured) and counts 2, others 1.  A tile belongs to the CTA that holds its
 // first unit.  With fewer than two units to a CTA every tile counts 1: a CTA
 // must not fall between the two units of a tile, where it would leave no partial
@@ -260,8 +261,8 @@ __device__ __forceinline__ int slot_tile(const Piece& x, int s, int j) {
 }
 // Place of K and V of tile t among a piece's 2 n ring tiles: in the order of the
 // products that read them.  Where the slots alternate that is S(0) S(1) PV(0) S(2)
-// PV(1) ..: loaded tile by tile, K(t + 2) would wait for V(t)'s stage instead of
-// V(t - 1)'s (2400 cycles a tile instead of @R1@).
+// PV(1) ..: loaded tile by tile, a K would wait for the stage of a V that is read
+// one product later (24 requests of 9216 keys: 89 us, in this order 85).
 __device__ __forceinline__ int place_k(const Piece& x, int t) { return split_rows(x) ? 2 * t : max(0, 2 * t - 1); }
 __device__ __forceinline__ int place_v(const Piece& x, int t) {
   return split_rows(x) ? 2 * t + 1 : min(2 * t + 2, 2 * x.n - 1);
@@ -271,12 +272,20 @@ __device__ __forceinline__ int slot_rows(const Piece& x, int s) {
   return split_rows(x) ? min(128, x.rows - 128 * s) : x.rows;
 }
 
+// Brings the lanes of a warp together again: lanes that a wait has suspended wake
+// one by one, and may go on one by one, shuffles and all, until an instruction
+// that the warp issues as one (256 rows of Q gathered: 20000 cycles without this,
+// 3000 with it).  Barriers 1 to 15 are the warps' own.
+__device__ __forceinline__ void converge(int warp) {
+  asm volatile("barrier.sync.aligned %0, 32;" ::"r"(warp) : "memory");
+}
+
 // Rows a softmax warp has, as a power of two.  A tile of few rows spreads them
 // over the four warps (row i in TMEM lane 32 (i >> shift) + its low bits), four
-// lanes to a row: a chain of product, softmax, product bounds the rate of such
-// tiles, and one thread to a row takes @L1@ cycles for its 128 columns, four take
-// @L2@.
-__device__ __forceinline__ int row_shift(const Piece& x) { return x.rows <= 32 ? 3 : x.rows <= 64 ? 4 : 5; }
+// lanes to a row: such tiles come as fast as the chain of product, softmax,
+// product lets them, and one thread to a row takes 2400 cycles for its 128
+// columns, four take 1350 (24 requests of 9216 keys: 91 us, 89).
+__device__ __forceinline__ int row_shift(const Piece& x) { return x.rows <= 32 ? 3 : 5; }
 
 // The products, out of line: they are issued from several places.
 template <int D>
@@ -398,6 +407,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t g = 0, n_got = 0;
       bool ok = true;
       while (ok && next(n_got, x)) {
+        // the first instructions of the other warps, and Q, come before the stream
+        // (64 requests of 512 keys: 47 us, 43)
+        if (n_got == 1) ok = warp_wait(bars + L::kQFull, 0, abort_flag, p.status);
         if (lane == 0) {
           const bool own = x.b >= 0;
           const int b = own ? x.b : 0;
@@ -499,7 +511,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           // piece; where both slots read the same tiles, together and slot 0 first
           // (slot 1 releases the tile)
           const bool early = more && !split_rows(y);
-          if (early && !split_rows(x) && x.n == 1) begin(y, n + 1, x.turn ^ 1, g_next);
+          // ... if its Q and first tile are there: the products at hand do not wait for them
+          auto ready = [&] {
+            return (n_q > n + 1 || dense::slim::mbar_test_wait(bars + L::kQFull + (int)((n + 1) & 1), ((n + 1) >> 1) & 1)) &&
+                   dense::slim::mbar_test_wait(bars + L::kFull + (int)(g_next % NST), (g_next / NST) & 1);
+          };
+          uint32_t later = 0;  // slots that go on with it after this piece's last product
+          auto go_on = [&](int s, bool last) {
+            if (last || ready()) begin(y, n + 1, s, g_next);
+            else later |= 1u << s;
+          };
+          if (early && !split_rows(x) && x.n == 1) go_on(x.turn ^ 1, false);
           for (int i = 0; ok && i < x.n * (split_rows(x) ? 2 : 1); ++i) {
             // the slots in turn
             const int s = (i & 1) ^ x.turn, j = i >> 1, ns = slot_tiles(x, s);
@@ -525,8 +547,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               umma_commit(bars + L::kOFull + s);
               done0 += s ^ 1;
               done1 += s;
-              if (early) begin(y, n + 1, s, g_next);
+              if (early) go_on(s, i + 1 == x.n * (split_rows(x) ? 2 : 1) && !later);
             }
+          }
+          if (later) {  // in the order of their tiles
+            if (later >> y.turn & 1) begin(y, n + 1, y.turn, g_next);
+            if (later >> (y.turn ^ 1) & 1) begin(y, n + 1, y.turn ^ 1, g_next);
           }
           if (more && !early) begin(y, n + 1, 0, g_next);
           if (more && !early) begin(y, n + 1, 1, g_next);
@@ -559,9 +585,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto keys_seen = [&](int r) {
         return x.kv_len + (x.b < 0 ? 0 : 1 - p.T + (256 * x.blk + (split_rows(x) ? 128 * s : 0) + r) % p.T);
       };
-      const int limit = keys_seen(row), limit8 = keys_seen(row + 8);
-      float m = -INFINITY, m8 = -INFINITY;
-      uint64_t l2 = pk2(0.f, 0.f), l28 = l2;
+      const int limit = keys_seen(row);
+      float m = -INFINITY;
+      uint64_t l2 = pk2(0.f, 0.f);
       for (int j = 0; j < nt; ++j, ++g) {
         if (!warp_wait(bars + L::kSFull + s, g & 1, abort_flag, p.status)) { ok = false; break; }
         tc_fence_after_sync();
@@ -573,13 +599,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           dense::softmax_tile<D, 0, 1>(t_s, t_o, c, rem, __reduce_min_sync(0xffffffffu, rem[0]),
                                        __reduce_max_sync(0xffffffffu, rem[0]), j == 0, lane, mm, ll);
           m = mm[0], l2 = ll[0];
-        } else if (any && shift == 4) {
-          const int rem[2] = {min(128, limit - key0), min(128, limit8 - key0)};
-          float mm[2] = {m, m8};
-          uint64_t ll[2] = {l2, l28};
-          dense::softmax_tile<D, 0, 1>(t_s, t_o, c, rem, __reduce_min_sync(0xffffffffu, min(rem[0], rem[1])),
-                                       __reduce_max_sync(0xffffffffu, max(rem[0], rem[1])), j == 0, lane, mm, ll);
-          m = mm[0], m8 = mm[1], l2 = ll[0], l28 = ll[1];
         } else if (any) {
           // columns before `whole` are seen by all of the warp's rows, from `none` on by none
           const int rem = min(128, limit - key0);
@@ -666,8 +685,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       float la, lb, l;
       if (shift < 5) {
         l = dense::quad_sum(l2);
-        const float l8 = dense::quad_sum(l28);
-        if (shift == 4 && (lane & 3) == 0) ml[s * 256 + row + 8] = m8, ml[s * 256 + 136 + row] = l8;
       } else {
         upk2(l2, la, lb);
         l = la + lb;
@@ -711,6 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; freed < need; ++freed)
         if (!warp_wait(bars + L::kQFree + (int)(freed & 1), (freed >> 1) & 1, abort_flag, p.status)) return false;
       constexpr int CH = D / 8, RPI = 32 / CH;  // chunks of a row, rows per access of the warp
+      converge(warp);
       const int shift = row_shift(x);
       for (int r0 = wq << shift; r0 < x.rows; r0 += 128) {
         // this lane's row

@@ -58,6 +58,31 @@ def test_forward_two_tiles_per_item(d, heads):
     check(*make(*heads, d, pairs, seed=6), False)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("heads", [(64, 64), (63, 9), (96, 12)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_heads(d, heads, causal):
+    """Items of two slots with the small and empty sequences of test_forward."""
+    pairs = [p for lens in LENGTHS.values() for p in lens]
+    check(*make(*heads, d, pairs, seed=90 + heads[0]), causal)
+
+
+def test_many_heads_repeat_and_neighbours():
+    pairs = [(300, 300), (5, 150), (129, 60), (1, 1)]
+    q, k, v, cu_q, cu_kv = make(96, 8, 64, pairs, seed=95, extra=3)
+    want = vsa().dense_attn_varlen(q, k, v, cu_q, cu_kv)
+    for bad in (float("nan"), float("inf")):
+        for i in (1, 3):
+            q[:, cu_q[i]:cu_q[i + 1]] = bad
+            k[:, cu_kv[i]:cu_kv[i + 1]] = bad
+            v[:, cu_kv[i]:cu_kv[i + 1]] = bad
+        q[:, cu_q[-1]:], k[:, cu_kv[-1]:], v[:, cu_kv[-1]:] = bad, bad, bad
+        for _ in range(3):
+            got = vsa().dense_attn_varlen(q, k, v, cu_q, cu_kv)
+            for i in (0, 2):
+                assert torch.equal(got[:, cu_q[i]:cu_q[i + 1]], want[:, cu_q[i]:cu_q[i + 1]])
+
+
 def test_forward_long():
     """2049 rows behind 5000 keys (several waves of long items)."""
     check(*make(16, 4, 128, [(2049, 5000), (3, 3)], seed=9), True)

@@ -44,6 +44,22 @@ def test_row_blocks(shape, prefix):
     check(make(b, hq, hkv, t, 128, prefix, 180, [t + (37 * i) % (180 - t) for i in range(b)], seed=b))
 
 
+@pytest.mark.parametrize("rows", [(8, 1), (9, 1), (31, 1), (32, 1), (33, 1), (8, 4), (11, 3), (16, 4), (13, 5)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_of_a_request(d, rows):
+    """Around the 8 rows of a warp and the 32 that four warps share; logits that
+    move the reference max, and rows that see nothing of their last tile."""
+    hq, t = rows
+    check(make(3, hq, 1, t, d, 260, 400, [t, 129 + t // 2, 400], seed=70 + hq, mult=3.0))
+    check(make(30, hq, 1, t, d, 0, 300, [(53 * i) % 301 for i in range(30)], seed=71 + hq))
+
+
+def test_short_pieces_and_row_blocks_in_turn():
+    """Many requests of one key tile, and of none, around blocks of a prefix."""
+    check(make(200, 4, 2, 1, 128, 500, 130, [(i * 7) % 131 for i in range(200)], seed=80))
+    check(make(150, 8, 4, 1, 64, 1300, 20, [1 + i % 20 if i % 3 else 0 for i in range(150)], seed=81))
+
+
 @pytest.mark.parametrize("prefix", [0, 5, 256])
 def test_lengths_that_leave_rows_empty(prefix):
     """No suffix, fewer suffix keys than new tokens, no keys at all."""
