@@ -56,6 +56,7 @@ def test_rows_of_a_request(d, rows):
 
 def test_short_pieces_and_row_blocks_in_turn():
     """Many requests of one key tile, and of none, around blocks of a prefix."""
+    check(make(33, 8, 1, 1, 128, 640, 180, [(37 * i) % 181 for i in range(33)], seed=79))  # 256 + 8 rows
     check(make(200, 4, 2, 1, 128, 500, 130, [(i * 7) % 131 for i in range(200)], seed=80))
     check(make(150, 8, 4, 1, 64, 1300, 20, [1 + i % 20 if i % 3 else 0 for i in range(150)], seed=81))
 
