@@ -873,10 +873,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
       const float* part = (kind ? p.part_s : p.part_p) + lane * E;
       for (int i0 = 0; i0 < count; i0 += 32) {
         const float mine = i0 + lane < count ? lse[first + (long long)(i0 + lane) * rows] : -INFINITY;
+        // nothing seen in any of them (a NaN is not that, though the maximum passes over it)
+        if (__all_sync(0xffffffffu, mine == -INFINITY)) continue;
         float top = mine;
 #pragma unroll
         for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-        if (top == -INFINITY) continue;
         const float nm = fmaxf(m, top), a = fast_exp2(m - nm);
         m = nm;
         l *= a;
