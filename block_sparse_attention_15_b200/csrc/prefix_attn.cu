@@ -892,9 +892,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
           float v[E];
           if (E == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
           else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
-          l += w;
+          // a part of which the row saw nothing weighs nothing, whatever its v left there (0 * NaN)
+          const bool none = x == -INFINITY;
+          l += none ? 0.f : w;
 #pragma unroll
-          for (int e = 0; e < E; ++e) o[e] = fmaf(w, v[e], o[e]);
+          for (int e = 0; e < E; ++e) o[e] = none ? o[e] : fmaf(w, v[e], o[e]);
         }
       }
     }

@@ -105,3 +105,19 @@ def test_logits_of_minus_infinity(shape, d):
     got, lse = call((args[0], kp, args[2], ks, *args[4:]))
     assert (got[:, :hq // hkv] == 0).all() and (lse[:, :hq // hkv] == -math.inf).all()
     assert torch.isfinite(got).all() and torch.isfinite(lse[:, hq // hkv:]).all()
+
+
+def test_pieces_that_a_token_does_not_see():
+    """A NaN in v of a key tile that an earlier drafted token sees nothing of:
+    that token's partial result there weighs nothing, not 0 * NaN."""
+    args = make(60, 4, 2, 3, 64, 300, 300, [258] * 60, seed=9)
+    clean = call(args)
+    vs = args[4].clone()
+    vs[:, :, 256:258] = math.nan  # the keys of the two last tokens begin a tile of their own
+    out, lse = call((*args[:4], vs, args[5]))
+    assert torch.isnan(out[:, :, 1:]).all()
+    # where the tile is a share of its own token 0 is whole; it may be NaN elsewhere (0 * NaN in one product)
+    whole = torch.isfinite(out[:, :, 0]).all(-1)
+    assert whole.any()
+    assert torch.equal(out[:, :, 0][whole], clean[0][:, :, 0][whole])
+    assert torch.equal(lse, clean[1])
