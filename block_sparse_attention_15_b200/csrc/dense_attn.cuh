@@ -366,7 +366,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, float c
         float a, b;
         upk2(ffma2(pk2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), cc, nm2[w]), a, b);
         if (!kMask && (k & 7) < POLY) {
-          upk2(exp2_fma2_t<true>(a, b), a, b);
+          upk2(exp2_fma2_any(a, b), a, b);
         } else {
           a = fast_exp2(a);
           b = fast_exp2(b);

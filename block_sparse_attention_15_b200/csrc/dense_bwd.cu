@@ -79,12 +79,6 @@ __device__ __forceinline__ uint32_t sw128(uint32_t row, uint32_t chunk) {
   return row * 128u + ((chunk ^ (row & 7u)) << 4);
 }
 
-__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
 // D = A B^T over N rows of B from its row `from` on: A [128][D] bf16 in TMEM, B a
 // tile [D / 64][128 rows][128 B].
 template <int D, int N>
