@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float a, b;
           upk2(e, a, b);
           if (!kMask && (q & 7) < DENSE_BWD_POLY8) {
-            upk2(exp2_fma2_t<true>(a, b), a, b);
+            upk2(exp2_fma2_any(a, b), a, b);
           } else {
             a = fast_exp2(a);
             b = fast_exp2(b);
@@ -1028,7 +1028,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (at + 1 < under) b = -INFINITY;
               }
               if (!kMask && (k & 7) < DENSE_BWD_POLY8) {
-                upk2(exp2_fma2_t<true>(a, b), a, b);
+                upk2(exp2_fma2_any(a, b), a, b);
               } else {
                 a = fast_exp2(a);
                 b = fast_exp2(b);
