@@ -860,7 +860,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 4; ++e) {
             const int r = 32 * e + lane;
             const bool real = r < left;
-            nl[e] = real ? -kLog2 * p.lse[at + r] : -INFINITY;  // no row: p = 0
+            // no row, or one whose logits are all -inf: p = 0
+            const float lse = real ? p.lse[at + r] : -INFINITY;
+            nl[e] = lse == -INFINITY ? -INFINITY : -kLog2 * lse;
             de[e] = real ? p.delta[at + r] : 0.f;
           }
           if (g >= (uint32_t)NROW &&

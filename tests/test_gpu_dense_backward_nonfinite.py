@@ -7,7 +7,8 @@ import pytest
 import torch
 
 from . import dense_ref as R
-from .test_gpu_dense_nonfinite import HEADS, inputs, seeing_rows, vsa
+from .test_gpu_dense import make, vsa
+from .test_gpu_dense_nonfinite import HEADS, inputs, seeing_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +68,29 @@ def test_nan_in_query_rows(d, heads, causal):
             bad[h, cu_q[1] + start + h] = True
         qb[bad, d - 1] = math.nan
         check_nan(gradients(qb, k, v, cu_q, cu_kv, causal, dout)[2], clean, bad, cu_q, cu_kv, causal, heads[1])
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("heads", [(4, 4), (4, 2), (8, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_whose_logits_are_all_minus_infinity(d, heads, causal):
+    """Finite inputs whose logits leave fp32's range: such a row's output is 0, its
+    log-sum-exp -inf, and its share of every gradient 0."""
+    lens = [(65, 65), (300, 420), (1500, 1500)] if heads == (8, 1) else [(65, 65), (300, 420), (40, 33)]
+    q, k, v, cu_q, cu_kv = make(*heads, d, lens, seed=d + heads[0] + 7)
+    dout = R.normal(q.shape, d)
+    q[..., 0] = 0
+    k[..., 0] = -2.0 ** 100
+    dead = torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda")
+    dead[:, cu_q[1]:cu_q[2]:7], dead[1, cu_q[2] - 1], dead[0, 10] = True, True, True
+    q[dead] = 0
+    q[dead, 0] = 2.0 ** 100  # logits of -2^200
+    out, lse, got = gradients(q, k, v, cu_q, cu_kv, causal, dout)
+    # (in 64 bits, where these logits are numbers, only rows without keys have lse = -inf)
+    without_keys = torch.isinf(R.forward(q, k, v, cu_q, cu_kv, causal)[1]).cuda()
+    assert (out[dead] == 0).all() and torch.equal(lse == -math.inf, dead | without_keys)
+    # in 64 bits the rows take no part where their dout is 0
+    dout[dead] = 0
+    want, tol = R.backward(q, k, v, dout, cu_q, cu_kv, causal)
+    for name, x, y, z in zip(("dq", "dk", "dv"), got, want, tol):
+        R.assert_within(x, y, z, name)
