@@ -686,11 +686,13 @@ def _cumulative(xs, name):
         try:
             return array.array("i", xs)
         except TypeError:
-            pass  # tensors' or arrays' elements
-    a = np.asarray(xs, dtype=np.int32)
+            pass  # arrays' or tensors' elements, or what is refused below
+    a = np.asarray(xs)
     if a.ndim != 1:
         raise ValueError(f"{name} must be a 1-D sequence")
-    return array.array("i", a.tolist())
+    if a.dtype.kind not in "iu":
+        raise TypeError(f"{name} must hold integers, got {a.dtype}")
+    return array.array("i", a.astype(np.int32).tolist())
 
 
 def _dense_common(q, k, v, cu_seqlens_q, cu_seqlens_kv):

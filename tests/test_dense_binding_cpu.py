@@ -1,0 +1,21 @@
+"""Host checks of the dense entries' binding (no GPU)."""
+import numpy as np
+import pytest
+import torch
+
+from block_sparse_attention_15_b200 import binding as B
+
+
+@pytest.mark.parametrize("xs", [[0, 5, 12], (0, 5, 12), np.array([0, 5, 12]), np.array([0, 5, 12], dtype=np.uint8),
+                                torch.tensor([0, 5, 12]), torch.tensor([0, 5, 12], dtype=torch.int32),
+                                [np.int64(0), torch.tensor(5), 12], range(0, 3)])
+def test_cumulative_lengths(xs):
+    got = B._cumulative(xs, "cu")
+    assert got.typecode == "i" and list(got) == ([0, 1, 2] if isinstance(xs, range) else [0, 5, 12])
+
+
+@pytest.mark.parametrize("xs", [[0, 10.7], (0, 5.0), np.array([0.0, 10.7]), torch.tensor([0.0, 10.7]),
+                                [torch.tensor(0), torch.tensor(10.7)], np.array([False, True])])
+def test_cumulative_lengths_that_are_no_integers(xs):
+    with pytest.raises(TypeError):
+        B._cumulative(xs, "cu")
