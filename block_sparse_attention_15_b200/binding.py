@@ -685,14 +685,16 @@ def _cumulative(xs, name):
     if isinstance(xs, (list, tuple)):
         try:
             return array.array("i", xs)
-        except TypeError:
+        except (TypeError, OverflowError):
             pass  # arrays' or tensors' elements, or what is refused below
     a = np.asarray(xs)
     if a.ndim != 1:
         raise ValueError(f"{name} must be a 1-D sequence")
     if a.dtype.kind not in "iu":
         raise TypeError(f"{name} must hold integers, got {a.dtype}")
-    return array.array("i", a.astype(np.int32).tolist())
+    if a.size and (a.min() < -2 ** 31 or a.max() >= 2 ** 31):
+        raise ValueError(f"{name} holds a value outside the 32-bit range")
+    return array.array("i", a.tolist())
 
 
 def _dense_common(q, k, v, cu_seqlens_q, cu_seqlens_kv):

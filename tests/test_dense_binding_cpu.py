@@ -19,3 +19,12 @@ def test_cumulative_lengths(xs):
 def test_cumulative_lengths_that_are_no_integers(xs):
     with pytest.raises(TypeError):
         B._cumulative(xs, "cu")
+
+
+@pytest.mark.parametrize("xs", [[0, 2 ** 32 + 10], np.array([0, 2 ** 32 + 10]), torch.tensor([0, 2 ** 32 + 10]),
+                                np.array([0, 2 ** 31]), np.array([0, 2 ** 64 - 1], dtype=np.uint64), [[0, 5]],
+                                np.zeros((1, 2), dtype=np.int32)])
+def test_cumulative_lengths_out_of_range(xs):
+    """64-bit values must not wrap into valid ones."""
+    with pytest.raises(ValueError):
+        B._cumulative(xs, "cu")
