@@ -673,6 +673,9 @@ def _on(index, stream, call):
     current and memory allocated on that stream."""
     if stream is None and torch.cuda.current_device() == index:
         return call(_raw_stream(index))
+    if stream is not None and stream.device.index != index:
+        # (kernels there would reach for this device's memory)
+        raise ValueError(f"stream is on {stream.device}, q on cuda:{index}")
     with torch.cuda.device(index):
         if stream is None:
             return call(_raw_stream(index))

@@ -28,3 +28,15 @@ def test_cumulative_lengths_out_of_range(xs):
     """64-bit values must not wrap into valid ones."""
     with pytest.raises(ValueError):
         B._cumulative(xs, "cu")
+
+
+def test_stream_of_another_device():
+    """Refused before anything is allocated or launched."""
+    class Stream:
+        device = torch.device("cuda", 1)
+        cuda_stream = 0
+
+    calls = []
+    with pytest.raises(ValueError):
+        B._on(0, Stream(), calls.append)
+    assert not calls
