@@ -730,6 +730,9 @@ def _workspace(t, need, like):
     """(tensor, address, bytes)."""
     if t is None:
         t = torch.empty(max(need, 256), dtype=_U8, device=like.device)
+    elif not t.is_contiguous():
+        # an expanded view has fewer bytes behind it than elements
+        raise ValueError("workspace must be contiguous")
     return t, t.data_ptr(), t.numel() * t.element_size()
 
 

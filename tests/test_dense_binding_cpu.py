@@ -40,3 +40,13 @@ def test_stream_of_another_device():
     with pytest.raises(ValueError):
         B._on(0, Stream(), calls.append)
     assert not calls
+
+
+def test_workspace_must_be_contiguous():
+    """The bytes of an expanded or strided view are not all there."""
+    like = torch.empty(1)
+    for bad in (torch.empty(1, dtype=torch.uint8).expand(1 << 20), torch.empty(64, 64)[:, ::2]):
+        with pytest.raises(ValueError):
+            B._workspace(bad, 0, like)
+    ws = torch.empty(100, dtype=torch.float32)
+    assert B._workspace(ws, 0, like) == (ws, ws.data_ptr(), 400)
