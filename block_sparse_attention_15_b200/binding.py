@@ -817,7 +817,7 @@ def shared_prefix_attn(q, k_prefix, v_prefix, k_suffix, v_suffix, suffix_lens, *
     step, or the check of a few drafted tokens.
 
     q: [B, Hq, T, D]; k_prefix, v_prefix: [Hkv, P, D], kept once for all
-    requests (P may be 0); k_suffix, v_suffix: [B, Hkv, capacity, D], the last T
+    requests (P may be 0; both None: no prefix); k_suffix, v_suffix: [B, Hkv, capacity, D], the last T
     of a request's ``suffix_lens[b]`` keys being its new tokens'; all may be
     strided views (token-major caches transposed).  suffix_lens: CUDA int32
     [B], read on the device.  Token t sees the prefix and its first
@@ -826,7 +826,10 @@ def shared_prefix_attn(q, k_prefix, v_prefix, k_suffix, v_suffix, suffix_lens, *
     (B, Hq, T, D), qs, qp = _heads(q, "q")
     ks_shape, kss, ksp = _heads(k_suffix, "k_suffix")
     vs_shape, vss, vsp = _heads(v_suffix, "v_suffix")
-    kp, vp = _rows(k_prefix, "k_prefix"), _rows(v_prefix, "v_prefix")
+    if k_prefix is None and v_prefix is None:
+        kp = vp = (ks_shape[1], 0, D, 0, 0, None)
+    else:
+        kp, vp = _rows(k_prefix, "k_prefix"), _rows(v_prefix, "v_prefix")
     _require(suffix_lens, torch.int32, "suffix_lens")
     Hkv, P, cap = kp[0], kp[1], ks_shape[2]
     if vp[:3] != kp[:3] or kp[2] != D:
