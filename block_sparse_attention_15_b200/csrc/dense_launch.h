@@ -119,6 +119,7 @@ struct PrefixParams {
   int pfx_rows, sfx_rows;           // rows of a partial result
   // workspace
   float *part_p, *part_s, *part_lse_p, *part_lse_s;
+  int* tiles_before;                // [B + 1] suffix key tiles of the requests before one, or null
   TmaAxes kp_ax, vp_ax, ks_ax, vs_ax;
 };
 struct PrefixTensors {

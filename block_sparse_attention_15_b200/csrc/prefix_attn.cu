@@ -120,6 +120,7 @@ struct Line {
 
 // Sum of the key tiles of requests [0, b_end).
 __device__ __forceinline__ int suffix_tiles_before(const PrefixParams& p, int b_end, int lane) {
+  if (p.tiles_before) return p.tiles_before[b_end];
   int sum = 0;
   for (int b = lane; b < b_end; b += 32) sum += key_tiles(suffix_len(p, b));
 #pragma unroll
@@ -182,25 +183,38 @@ struct Walk {
     int tiles = key_tiles(p.prefix_len), rows = p.B * p.rows_per_req, blocks = p.pfx_blocks;
     if (r >= line.pfx * tiles) {
       r -= line.pfx * tiles;
-      // the request whose suffix holds unit r: 32 requests at a time
-      for (int b0 = 0;; b0 += 32) {
-        const int mine_u = b0 + lane < p.B ? key_tiles(suffix_len(p, b0 + lane)) * line.sfx : 0;
-        int sum = mine_u;
+      // the request whose suffix holds unit r
+      if (p.tiles_before) {
+        // the last request with no more than r units before it
+        int lo = 0, hi = p.B - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (p.tiles_before[mid] * line.sfx <= r) lo = mid;
+          else hi = mid - 1;
+        }
+        b = lo;
+        r -= p.tiles_before[b] * line.sfx;
+      } else {
+        // 32 requests at a time
+        for (int b0 = 0;; b0 += 32) {
+          const int mine_u = b0 + lane < p.B ? key_tiles(suffix_len(p, b0 + lane)) * line.sfx : 0;
+          int sum = mine_u;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, sum, o);
-          if (lane >= o) sum += v;
+          for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += v;
+          }
+          const int all = __shfl_sync(0xffffffffu, sum, 31);
+          if (r >= all && b0 + 32 < p.B) {
+            r -= all;
+            continue;
+          }
+          const unsigned past = __ballot_sync(0xffffffffu, sum > r);
+          const int i = past ? __ffs(past) - 1 : 31;
+          r -= __shfl_sync(0xffffffffu, sum - mine_u, i);
+          b = b0 + i;
+          break;
         }
-        const int all = __shfl_sync(0xffffffffu, sum, 31);
-        if (r >= all && b0 + 32 < p.B) {
-          r -= all;
-          continue;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, sum > r);
-        const int i = past ? __ffs(past) - 1 : 31;
-        r -= __shfl_sync(0xffffffffu, sum - mine_u, i);
-        b = b0 + i;
-        break;
       }
       tiles = max(1, key_tiles(suffix_len(p, b)));
       rows = p.rows_per_req;
@@ -840,6 +854,40 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Suffix key tiles of the requests before each one, for batches whose lengths
+// are too many for every warp of the other two kernels to add up: without it a
+// call's time grew with the square of the batch.  One block, a thread per
+// request, 1024 of them at a time.
+constexpr int kTableThreads = 1024;
+__global__ void __launch_bounds__(kTableThreads) prefix_table_kernel(const __grid_constant__ PrefixParams p) {
+  __shared__ int warp_sum[kTableThreads / 32];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  int before = 0;  // of the requests before these 1024
+  for (int b0 = 0; b0 < p.B; b0 += kTableThreads) {
+    const int b = b0 + (int)threadIdx.x;
+    const int mine = b < p.B ? key_tiles(suffix_len(p, b)) : 0;
+    int sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (lane == 31) warp_sum[warp] = sum;
+    __syncthreads();
+    int all = warp_sum[lane];  // as many warps as lanes
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, all, o);
+      if (lane >= o) all += v;
+    }
+    const int ahead = __shfl_sync(0xffffffffu, all, (warp + 31) & 31);  // warps before this one
+    if (b < p.B) p.tiles_before[b] = before + (warp ? ahead : 0) + sum - mine;
+    before += __shfl_sync(0xffffffffu, all, 31);
+    __syncthreads();  // warp_sum is read
+  }
+  if (threadIdx.x == 0) p.tiles_before[p.B] = before;
+}
+
 // Joins the rows' partials: weights 2^(lse_i - max), fp32, in the order of the
 // line.  A block has kJoinRows rows of one request and key head, one per warp.
 constexpr int kJoinWarps = 4, kJoinRows = 4;
@@ -936,6 +984,14 @@ static size_t parts_of(long long segments, int rows) {
 }
 static size_t a256(size_t x) { return (x + 255) & ~size_t(255); }
 
+// Requests from which on their key tiles are added up once, by a kernel of its
+// own (64 query heads over 8, 1000 shared and up to 200 own keys, us by the warps
+// and by the kernel: 64 requests 37, 41; 200: 94, 97; 256: 121, 121; 512: 211, 205;
+// 4096: 2055, 1548; 65536 with 8 heads over 1: 19550, 2118).
+#ifndef PREFIX_TABLE_REQUESTS
+#define PREFIX_TABLE_REQUESTS 512
+#endif
+
 size_t prefix_workspace(PrefixParams* p, int D, void* base) {
   prefix_shape(p);
   const bool pfx = p->prefix_len > 0, sfx = p->suffix_cap > 0;
@@ -952,6 +1008,8 @@ size_t prefix_workspace(PrefixParams* p, int D, void* base) {
   p->part_s = take(ns * D);
   p->part_lse_p = take(np);
   p->part_lse_s = take(ns);
+  p->tiles_before = nullptr;
+  if (sfx && p->B >= PREFIX_TABLE_REQUESTS) p->tiles_before = reinterpret_cast<int*>(take((size_t)p->B + 1));
   return off;
 }
 
@@ -968,6 +1026,7 @@ static int launch_prefix_t(PrefixParams p, const CUtensorMap* m, cudaStream_t st
   const int grid = cap < kPrefixGrid ? (int)(cap > 0 ? cap : 1) : kPrefixGrid;
   // 20 us per tile of a CTA's share, ten times what one takes: a wait may last a piece
   p.item_us = (int)std::min(20 * (cap / grid + 1), 1000000000LL);
+  if (p.tiles_before) prefix::prefix_table_kernel<<<1, prefix::kTableThreads, 0, stream>>>(p);
   kern<<<grid, prefix::kThreads, L::kAlloc, stream>>>(m[0], m[1], m[2], m[3], p);
   if (cudaGetLastError() != cudaSuccess) return VSA_ERR_CUDA;
   // set up while the attention kernel runs; waits for it before it reads partial results

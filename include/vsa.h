@@ -653,7 +653,7 @@ size_t shared_prefix_attn_workspace_size(int B, int Hq, int Hkv, int T, int D, i
  *              no two calls in flight may share it
  * scale        <= 0 selects 1/sqrt(D)
  * D 64 or 128; Hq a multiple of Hkv (VSA_ERR_SHAPE).  16-byte aligned views.
- * Two launches on `stream`.
+ * Two launches on `stream`, three from 512 requests on.
  */
 int shared_prefix_attn(const void* q, const void* k_prefix, const void* v_prefix, const void* k_suffix,
                        const void* v_suffix, const int32_t* suffix_lens, const vsa_prefix_layout* layout,
