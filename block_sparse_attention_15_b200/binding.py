@@ -749,7 +749,12 @@ def dense_attn_varlen(q, k, v, cu_seqlens_q, cu_seqlens_kv, *, causal: bool = Tr
     ``out`` past the last sequence are left as they were (0 when it is
     allocated here).  With ``return_lse`` also returns the fp32 [Hq, q_rows]
     natural-log log-sum-exp (-inf where a row sees no key), which
-    :func:`dense_attn_varlen_backward` takes."""
+    :func:`dense_attn_varlen_backward` takes.  ``scale``: None, or a value <= 0,
+    is 1/sqrt(D).  Probabilities are rounded to bf16 for the product with v.
+
+    The result carries no autograd history, even where q, k or v require
+    gradients: those come from :func:`dense_attn_varlen_backward`, called by a
+    training step itself or in the backward of a ``torch.autograd.Function``."""
     qi, ki, vi, cq, ck = _dense_common(q, k, v, cu_seqlens_q, cu_seqlens_kv)
     index = q.get_device()
     _same_device(index, k, v, out)
@@ -779,7 +784,8 @@ def dense_attn_varlen_backward(q, k, v, out, dout, lse, cu_seqlens_q, cu_seqlens
     ``out`` and ``lse`` come from that call, the other arguments are its own.
     ``dout`` and the gradients may be strided views like q and k.  dk and dv sum
     over the query heads of a key head.  Rows of given gradients past the last
-    sequence are left as they were (0 where they are allocated here)."""
+    sequence are left as they were (0 where they are allocated here).
+    Probabilities and ds are rounded to bf16 for the products that sum them."""
     qi, ki, vi, cq, ck = _dense_common(q, k, v, cu_seqlens_q, cu_seqlens_kv)
     oi, gi = _rows(out, "out"), _rows(dout, "dout")
     if oi[:3] != qi[:3] or gi[:3] != qi[:3]:
@@ -822,7 +828,10 @@ def shared_prefix_attn(q, k_prefix, v_prefix, k_suffix, v_suffix, suffix_lens, *
     strided views (token-major caches transposed).  suffix_lens: CUDA int32
     [B], read on the device.  Token t sees the prefix and its first
     ``suffix_lens[b] - T + 1 + t`` suffix keys.  Returns [B, Hq, T, D], with
-    ``return_lse`` also the fp32 [B, Hq, T] natural-log log-sum-exp."""
+    ``return_lse`` also the fp32 [B, Hq, T] natural-log log-sum-exp.  ``scale``:
+    None, or a value <= 0, is 1/sqrt(D).  Probabilities are rounded to bf16 for
+    the product with v.  A NaN or infinity in a new token's v may reach the
+    request's earlier new tokens, although they do not see it."""
     (B, Hq, T, D), qs, qp = _heads(q, "q")
     ks_shape, kss, ksp = _heads(k_suffix, "k_suffix")
     vs_shape, vss, vsp = _heads(v_suffix, "v_suffix")

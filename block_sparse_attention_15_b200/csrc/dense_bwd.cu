@@ -13,10 +13,12 @@
 // How (sm_100a): two kernels, each with one kind of accumulator in TMEM, so
 // that every sum has one owner and a fixed order (no atomics).  The price is
 // that S and dout V^T are formed twice (7 products of 128 x 128 x D instead of
-// 5).  One kernel for all five would send its dq tiles to memory as fp32 sums,
-// 64 KB per pair of tiles each way through shared memory, and keep dS there too:
-// some 3800 cycles of shared-memory traffic (128 bytes a cycle) per pair of
-// tiles, against the 4700 cycles that these seven products take.
+// 5).  One kernel for all five was estimated, not built: it would send its dq
+// tiles to memory as fp32 sums, 64 KB per pair of tiles each way through shared
+// memory, and keep dS there too, some 3800 cycles of shared-memory traffic (128
+// bytes a cycle) per pair of tiles, against the 4700 cycles that these seven
+// products take; the key tiles that add to a query tile would have to take turns
+// for the sums to keep their order.
 //
 //  dq:     a work item is one 128-row query tile of one head.  Per key tile
 //            S = Q K^T, dP = dO V^T, dQ += dS K
@@ -43,9 +45,10 @@
 // its A operand in TMEM, 861 with it in shared memory (A's 4 KB per instruction
 // do not load under the multiplication), so dq has 3 x 596 = 1788 cycles a tile
 // and dk/dv 2 x 596 + 2 x 861 = 2914 (TMEM holds no K and V beside two sums of
-// 128 columns).  Measured on 8192 rows, 40 heads over 8: 2390 and 3110 cycles;
-// without any softmax work 2230 and 3060.  1.94 ms together, 886 TFLOP/s of the
-// five products, at 1.58 GHz (the power limit's clock).
+// 128 columns).  Measured on 8192 rows, 40 heads over 8: 2455 and 3290 cycles of
+// the launch for each of an SM's pairs of tiles (start, end and the half-empty
+// tiles on the diagonal included), 1.91 ms together, 900 TFLOP/s of the five
+// products, at 1.7 GHz; called back to back, under the power limit, 2.19 ms.
 // P and dS are rounded to bf16 for the tensor core; everything else is fp32.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -71,6 +74,8 @@ constexpr int kThreads = 768;
 constexpr int kSoftmaxWarps = 16;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2 = 1.4426950408889634f;
+// 0 / 1 / 2 / 3: 1943, 1909, 1907, 1930 us on 8192 rows, 40 heads over 8; 764, 756,
+// 756, 764 on seven documents of 8192 rows together, 56 over 8
 #ifndef DENSE_BWD_POLY8
 #define DENSE_BWD_POLY8 2  // column pairs in eight whose exponential runs on the FMA pipe
 #endif

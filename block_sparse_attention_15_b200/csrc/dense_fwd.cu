@@ -18,10 +18,11 @@
 // The tensor pipe alternates between the slots, so one slot's softmax runs
 // under the other slot's products.  With at most two query tiles
 // per SM an item is one of them: both slots have it, take its key tiles in turn,
-// and their results are joined on the way out.  At D = 128 a product takes 596 cycles with
-// its A operand in TMEM and 861 with it in shared memory (measured: A's loads do
-// not overlap the products), so 1457 per tile bound the rate; TMEM is full (S and
-// O of two slots), which keeps Q out of it.
+// and their results are joined on the way out.  At D = 128 a product takes 596
+// cycles with its A operand in TMEM and 861 with it in shared memory (measured:
+// A's loads do not overlap the products), so 1457 per tile bound the rate; the
+// TMEM of one SM is full (S and O of two slots), which keeps Q out of it in this
+// form.
 //
 // One CTA per SM, 768 threads, item after item:
 //   warp 0      K and V tiles (one ring of NST stages, K(j) then V(j))
@@ -32,13 +33,15 @@
 //   warp 3      finds the work items, loads their Q tiles
 //   warps 4-11, 12-19   softmax of slot 0, slot 1, 16 rows a warp (softmax_tile)
 //   warps 20-23 epilogue: O / l, bf16 rows
-// Measured on 15488 rows, 40 heads over 8, causal: 2.10 ms, 1170 TFLOP/s (0.72 of
-// the measured bf16 peak), about 1650 cycles a tile; four softmax warps a slot,
-// one row per thread: 2.51 ms.  Part of the exponentials run on the FMA pipe
-// (DENSE_POLY8 0 / 1 / 2 / 3 of 8: 828, 820, 814, 826 us on three full clips of
-// 3000 to 9216 rows; the special-function unit alone does 16 a cycle).
-// P is rounded to bf16 for the tensor core (half a step is 2^-9 of a value,
-// and its error averages over the keys); sums, maxima and O stay fp32.
+// Measured on 15488 rows, 40 heads over 8, causal: 2.06-2.16 ms, 1140-1190 TFLOP/s
+// (0.70-0.73 of the measured bf16 peak), about 1650 cycles a tile; called back to
+// back, under the power limit, 2.39 ms.  (An earlier form with four softmax warps
+// a slot, one row per thread: 2.51 ms single, where this one had 2.14.)  Part of
+// the exponentials run on the FMA pipe (DENSE_POLY8 0 / 1 / 2 / 3 of 8: 745, 753,
+// 725, 739 us on three full clips of 3000 to 9216 rows; the special-function unit
+// alone does 16 a cycle).
+// P is rounded to bf16 for the tensor core (half a step is at most 2^-8 of a
+// value, and its error averages over the keys); sums, maxima and O stay fp32.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -20,7 +20,8 @@
 // pieces, one per CTA, whatever the lengths are (they are read on the device).
 // A CTA's part of a segment leaves a partial result (normalised rows, log2
 // sums) in the workspace; segment + CTA numbers it, as both only grow along the
-// line.  A second kernel joins each row's partials.
+// line.  A second kernel joins each row's partials.  Where requests are many, a
+// kernel before them adds up their key tiles.
 // Within a CTA the two slots share the key tiles: with more than 128 rows each
 // slot takes half of the rows, otherwise both have the same rows and take
 // alternate key tiles, two chains of product, softmax, product in flight, and
@@ -35,10 +36,10 @@
 // unrolled over its 128 columns spent 25 us of a call on that).
 //
 // Measured at D = 128: 24 requests of 9216 keys at most, 56 heads over 8, no
-// prefix: 86 us, 5.3 TB/s; 64 requests behind 15488 shared keys, 40 heads over 8:
-// 96 us, 3.5 TB/s (a tile of the prefix takes 4600 cycles for its 256 rows, one of
+// prefix: 84-87 us, 5.2-5.4 TB/s; 64 requests behind 15488 shared keys, 40 heads
+// over 8: 93-97 us, 3.5 TB/s (a tile of the prefix takes 4600 cycles for its 256 rows, one of
 // a suffix 2300: every SM is busy, fewer than half of the time with a stream);
-// 16 requests of 5 tokens: 38 us.
+// 16 requests of 5 tokens: 38-40 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -552,10 +552,15 @@ typedef struct vsa_dense_layout {
  * 0, Lk) (the last row sees every key):
  *   lse(r) = log sum_{j < n(r)} exp(scale q_r . k_j)
  *   out(r) = sum_{j < n(r)} exp(scale q_r . k_j - lse(r)) v_j
- * A row that sees no key gives out = 0 and lse = -inf.  Lengths may be 0.
- * What k and v hold past a sequence's rows never matters (NaN included); a
- * NaN or infinity in a sequence's own v reaches the rows that see it and may
- * reach other rows of that sequence.
+ * A row that sees no key, or none whose logit is above -inf, gives out = 0 and
+ * lse = -inf.  Lengths may be 0.
+ * What k and v hold past a sequence's rows never matters (NaN included).  A
+ * row with a NaN or +inf among its logits gives NaN, and no other row does for
+ * it; a NaN or infinity in a sequence's own v reaches the rows that see it and
+ * may reach other rows of that sequence (0 * inf in a product).
+ * Logits, maxima, sums, out's accumulator and lse are fp32; probabilities are
+ * rounded to bf16 for the product with v, some of them after an exponential of
+ * 7.5e-5 relative error (2^-13.7), and out is rounded once.
  *
  * q        device bf16 [Hq, q_rows, D] view
  * k, v     device bf16 [Hkv, kv_rows, D] views
@@ -587,10 +592,14 @@ size_t dense_attn_varlen_backward_workspace_size(const int32_t* cu_seqlens_q, co
  *   p = exp(scale q_r . k_j - lse(r)) where r sees j, delta = sum_d dout out,
  *   ds = p (dout_r . v_j - delta(r)),  dq = scale ds k,
  *   dk = scale sum over the group's heads of ds^T q,  dv likewise of p^T dout.
- * Rows that see no key get dq = 0, keys that no row sees dk = dv = 0.  Sums
- * are fp32 in a fixed order: the same call gives the same bits.  What the
- * tensors hold past a sequence's rows never matters; a NaN or infinity in a
- * sequence's own rows may reach any gradient of that sequence.
+ * Rows that see no key, or none whose logit is above -inf, get dq = 0 and add
+ * nothing to dk and dv; keys that no row sees get dk = dv = 0.  Sums are fp32 in
+ * a fixed order: the same call gives the same bits.  p and ds are rounded to
+ * bf16 for the products that sum them (the exponentials as in the forward
+ * call), the gradients once.  What the tensors hold past a sequence's rows never
+ * matters; a row whose lse is NaN makes its dq and the dk and dv of the keys it
+ * sees NaN, and a NaN or infinity in a sequence's own rows may reach any
+ * gradient of that sequence.
  *
  * q, k, v, cu_seqlens_*, n_seqs, heads, D, rows, causal, scale: as in the
  *          forward call
@@ -637,8 +646,13 @@ size_t shared_prefix_attn_workspace_size(int B, int Hq, int Hkv, int T, int D, i
  * the whole prefix and its first suffix_lens[b] - T + 1 + t suffix keys; query
  * head h reads key head h / (Hq / Hkv):
  *   out = softmax(scale q . k) v    over the keys the row sees
- * A row that sees no key gives out = 0 and lse = -inf.  What the caches hold
- * past the lengths never matters (NaN included).
+ * A row that sees no key, or none whose logit is above -inf, gives out = 0 and
+ * lse = -inf.  What the caches hold past the lengths never matters (NaN
+ * included).  A row with a NaN or +inf among its logits gives NaN; a NaN or
+ * infinity in v_prefix, or in a request's own v, reaches the rows that see it,
+ * and one in a later new token's v may reach the request's earlier tokens, too
+ * (0 * inf in a product).  Probabilities are rounded to bf16 for the product
+ * with v, out once; all else, partial results included, is fp32.
  *
  * q            device bf16 [B, Hq, T, D] view
  * k_prefix, v_prefix  device bf16 [Hkv, prefix_len, D] views (NULL if empty)
