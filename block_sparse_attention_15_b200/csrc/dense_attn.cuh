@@ -259,6 +259,36 @@ __device__ __forceinline__ void tmem_st_16x128_32(uint32_t taddr, const uint32_t
       : "memory");
 }
 
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// 2^x for a pair of floats on the FMA pipe, as exp2_fma2 has it (the same cubic),
+// for any x < 128: NaN gives NaN, and what is below -126.5, -infinity too, gives
+// 0.  The clamp keeps NaN; 2^j is made a number of its own, whose exponent field is
+// 0 at j = -127, and multiplied by, which keeps NaN as well.  (The sparse kernels'
+// form adds j to the exponent field, one instruction less, and turns NaN and
+// -infinity into 2^-120.)
+__device__ __forceinline__ uint64_t exp2_fma2_any(float x0, float x1) {
+  constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
+  float c0, c1;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(c0) : "f"(x0), "f"(-127.f));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(c1) : "f"(x1), "f"(-127.f));
+  const uint64_t xx = pk2(c0, c1);
+  const uint64_t t = fadd2(xx, pk2(kRound, kRound));
+  const uint64_t j = fadd2(t, pk2(-kRound, -kRound));
+  const uint64_t f = ffma2(j, pk2(-1.f, -1.f), xx);
+  uint64_t q = ffma2(f, pk2(0x1.c3f760p-5f, 0x1.c3f760p-5f), pk2(0x1.f0de1ap-3f, 0x1.f0de1ap-3f));
+  q = ffma2(q, f, pk2(0x1.62f31ap-1f, 0x1.62f31ap-1f));
+  q = ffma2(q, f, pk2(0x1.fff692p-1f, 0x1.fff692p-1f));
+  float t0, t1;
+  upk2(t, t0, t1);  // their low bits hold j
+  return fmul2(q, pk2(__int_as_float((__float_as_int(t0) << 23) + 0x3f800000),
+                      __int_as_float((__float_as_int(t1) << 23) + 0x3f800000)));
+}
+
 // Largest excess (log2 units) of a logit over its row's reference max that is
 // exponentiated without moving the reference: probabilities stay below 2^8.
 constexpr float kRefresh = 8.f;

@@ -33,8 +33,8 @@
 //   warp 3      finds the work items, loads their Q tiles
 //   warps 4-11, 12-19   softmax of slot 0, slot 1, 16 rows a warp (softmax_tile)
 //   warps 20-23 epilogue: O / l, bf16 rows
-// Measured on 15488 rows, 40 heads over 8, causal: 2.06-2.16 ms, 1140-1190 TFLOP/s
-// (0.70-0.73 of the measured bf16 peak), about 1650 cycles a tile; called back to
+// Measured on 15488 rows, 40 heads over 8, causal: 2.06-2.18 ms, 1130-1190 TFLOP/s
+// (0.69-0.73 of the measured bf16 peak), about 1650 cycles a tile; called back to
 // back, under the power limit, 2.39 ms.  (An earlier form with four softmax warps
 // a slot, one row per thread: 2.51 ms single, where this one had 2.14.)  Part of
 // the exponentials run on the FMA pipe (DENSE_POLY8 0 / 1 / 2 / 3 of 8: 745, 753,

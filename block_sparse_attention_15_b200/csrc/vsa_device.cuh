@@ -418,11 +418,6 @@ __device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -436,46 +431,26 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 // error on that interval (Remez exchange; block_sparse_attention_15_b200/
 // exp2_fit.py computes these float32 coefficients and models these steps:
 // max relative error 7.49e-5 over [-120, 32], far below the bf16 rounding of
-// the probabilities).
-// The cubic of x - j; the low bits of t's halves hold j.
-__device__ __forceinline__ uint64_t exp2_fma2_cubic(uint64_t xx, uint64_t& t) {
+// the probabilities).  With CLAMP, x is clamped to >= -120, where the result
+// (2^-120) is negligible next to the row maximum's 1; without it the caller
+// guarantees x >= -120 (below that the exponent field would wrap).
+template <bool CLAMP>
+__device__ __forceinline__ uint64_t exp2_fma2_t(float x0, float x1) {
   constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
-  t = fadd2(xx, pk2(kRound, kRound));
+  const uint64_t xx = CLAMP ? pk2(fmaxf(x0, -120.f), fmaxf(x1, -120.f)) : pk2(x0, x1);
+  const uint64_t t = fadd2(xx, pk2(kRound, kRound));
   const uint64_t j = fadd2(t, pk2(-kRound, -kRound));
   const uint64_t f = ffma2(j, pk2(-1.f, -1.f), xx);
   uint64_t q = ffma2(f, pk2(0x1.c3f760p-5f, 0x1.c3f760p-5f), pk2(0x1.f0de1ap-3f, 0x1.f0de1ap-3f));
   q = ffma2(q, f, pk2(0x1.62f31ap-1f, 0x1.62f31ap-1f));
-  return ffma2(q, f, pk2(0x1.fff692p-1f, 0x1.fff692p-1f));
-}
-// With CLAMP, x is clamped to >= -120, where the result (2^-120) is negligible
-// next to the row maximum's 1; without it the caller guarantees x >= -120 (below
-// that the exponent field would wrap).  A NaN comes out as a number.
-template <bool CLAMP>
-__device__ __forceinline__ uint64_t exp2_fma2_t(float x0, float x1) {
-  uint64_t t;
-  const uint64_t q = exp2_fma2_cubic(CLAMP ? pk2(fmaxf(x0, -120.f), fmaxf(x1, -120.f)) : pk2(x0, x1), t);
+  q = ffma2(q, f, pk2(0x1.fff692p-1f, 0x1.fff692p-1f));
   float q0, q1, t0, t1;
   upk2(q, q0, q1);
   upk2(t, t0, t1);
-  // shifted into the exponent field, j scales q by 2^j
+  // the low bits of t hold j; shifted into the exponent field they scale q by 2^j
   const float r0 = __int_as_float(__float_as_int(q0) + (__float_as_int(t0) << 23));
   const float r1 = __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
   return pk2(r0, r1);
-}
-// The same for any x < 128: NaN gives NaN, and what is below -126.5, -infinity
-// too, gives 0.  The clamp keeps NaN; 2^j is made a number of its own, whose
-// exponent field is 0 at j = -127, and multiplied by, which keeps NaN as well.
-__device__ __forceinline__ uint64_t exp2_fma2_any(float x0, float x1) {
-  float c0, c1;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(c0) : "f"(x0), "f"(-127.f));
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(c1) : "f"(x1), "f"(-127.f));
-  uint64_t t;
-  const uint64_t q = exp2_fma2_cubic(pk2(c0, c1), t);
-  float t0, t1;
-  upk2(t, t0, t1);
-  const uint64_t scale = pk2(__int_as_float((__float_as_int(t0) << 23) + 0x3f800000),
-                             __int_as_float((__float_as_int(t1) << 23) + 0x3f800000));
-  return fmul2(q, scale);
 }
 __device__ __forceinline__ uint64_t exp2_fma2(float x0, float x1) {
   return exp2_fma2_t<true>(x0, x1);

@@ -1,6 +1,9 @@
-"""The dense kernels' FMA-pipe exponential (exp2_fma2_any in vsa_device.cuh),
+"""The dense kernels' FMA-pipe exponential (exp2_fma2_any in dense_attn.cuh),
 modelled in float32 with its integer steps: the sparse kernels' values where
 those are normal numbers, 0 below, NaN kept."""
+import os
+import re
+
 import numpy as np
 
 from block_sparse_attention_15_b200 import exp2_fit as E
@@ -31,3 +34,11 @@ def test_small_values_and_values_that_are_none():
     assert (model([-126.6, -127.0, -150.0, -1e30, -np.inf]) == 0).all()
     with np.errstate(invalid="ignore"):
         assert np.isnan(model([np.nan, -np.nan, np.inf])).all()
+
+
+def test_source_holds_the_fitted_coefficients():
+    path = os.path.join(os.path.dirname(E.__file__), "csrc", "dense_attn.cuh")
+    body = open(path).read()
+    body = body[body.index("exp2_fma2_any(float"):]
+    lits = re.findall(r"pk2\((-?0x1\.[0-9a-f]+p-?\d+)f,", body[:body.index("\n}\n")])
+    assert [np.float32(float.fromhex(x)) for x in reversed(lits)] == list(E.coefficients_f32())
