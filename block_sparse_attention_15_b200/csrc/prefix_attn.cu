@@ -484,11 +484,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // consumed.  (Scalars: an array indexed by the slot would live in memory.)
         uint32_t done0 = 0, done1 = 0, gs0 = 0, gs1 = 0;
         uint32_t g = 0, n_got = 0, n_q = 0;
+        int n_s = 0;  // S products of the latest piece so far
         bool ok = true;
         auto wait = [&](int bar, uint32_t ph) {
           if (!mbar_wait(bars + bar, ph & 1, abort_flag, p.status)) ok = false;
         };
-        // S(j) of slot s of the piece numbered n, whose ring tiles start at gx
+        // S(j) of slot s of the piece numbered n, whose ring tiles start at gx.  (All S of
+        // a piece are issued before the first of the next one.)
         auto do_s = [&](const Piece& x, uint32_t n, int s, int j, uint32_t gx) {
           const int tile = slot_tile(x, s, j);
           const bool split = split_rows(x);
@@ -496,6 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (n_q == n) {  // the piece's first product
             wait(L::kQFull + (int)(n & 1), n >> 1);
             ++n_q;
+            n_s = 0;
           }
           wait(L::kFull + (int)(gk % NST), gk / NST);
           if (!ok) return;
@@ -504,7 +507,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                      sbase + L::kRingOff + (gk % NST) * L::kTile);
           umma_commit(bars + L::kSFull + s);
           if (s == 1 || !split) umma_commit(bars + L::kEmpty + (int)(gk % NST));
-          if (tile == x.n - 1 && (s == 1 || !split)) umma_commit(bars + L::kQFree + (int)(n & 1));  // the piece's last S
+          // The piece's last S: counted, for the slots' first S may be issued in either
+          // order (slot 0 goes on first after a piece of more than 128 rows, and a slot that
+          // found the piece not ready comes after the other), so that of two key tiles the
+          // second may come first.  With its Q free too early the next 256 rows came over it.
+          if (++n_s == (split ? 2 * x.n : x.n)) umma_commit(bars + L::kQFree + (int)(n & 1));
         };
         Piece x, y;
         auto next_one = [&](Piece& z) {
