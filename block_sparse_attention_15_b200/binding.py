@@ -823,9 +823,9 @@ def shared_prefix_attn(q, k_prefix, v_prefix, k_suffix, v_suffix, suffix_lens, *
     step, or the check of a few drafted tokens.
 
     q: [B, Hq, T, D]; k_prefix, v_prefix: [Hkv, P, D], kept once for all
-    requests (P may be 0; both None: no prefix); k_suffix, v_suffix: [B, Hkv, capacity, D], the last T
-    of a request's ``suffix_lens[b]`` keys being its new tokens'; all may be
-    strided views (token-major caches transposed).  suffix_lens: CUDA int32
+    requests (P may be 0; both None: no prefix); k_suffix, v_suffix: [B, Hkv,
+    capacity, D], the last T of a request's ``suffix_lens[b]`` keys being its new
+    tokens'; all may be strided views (token-major caches transposed).  suffix_lens: CUDA int32
     [B], read on the device.  Token t sees the prefix and its first
     ``suffix_lens[b] - T + 1 + t`` suffix keys.  Returns [B, Hq, T, D], with
     ``return_lse`` also the fp32 [B, Hq, T] natural-log log-sum-exp.  ``scale``:

@@ -37,9 +37,9 @@
 //
 // Measured at D = 128: 24 requests of 9216 keys at most, 56 heads over 8, no
 // prefix: 84-87 us, 5.2-5.4 TB/s; 64 requests behind 15488 shared keys, 40 heads
-// over 8: 93-97 us, 3.5 TB/s (a tile of the prefix takes 4600 cycles for its 256 rows, one of
-// a suffix 2300: every SM is busy, fewer than half of the time with a stream);
-// 16 requests of 5 tokens: 38-40 us.
+// over 8: 93-99 us, 3.5 TB/s (a tile of the prefix takes 4600 cycles for its 256
+// rows, one of a suffix 2300: every SM is busy, fewer than half of the time with a
+// stream); 16 requests of 5 tokens: 38-40 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
